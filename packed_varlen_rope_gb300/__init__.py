@@ -43,6 +43,23 @@ from ._binding import (  # noqa: F401
     rope_strerror,
     rope_validate_cu_seqlens,
 )
+from ._attention import (  # noqa: F401
+    ATTN_EXPORTS,
+    AttnPagedDesc,
+    AttnVarlenDesc,
+    AttnVarlenGrads,
+    PagedKVCache,
+    RopeKVAppendDesc,
+    RopePagedKV,
+    apply_attn,
+    attn_fault,
+    attn_paged,
+    attn_paged_workspace_bytes,
+    attn_varlen_bwd,
+    attn_varlen_fwd,
+    new_paged_kv_cache,
+    rope_kv_append,
+)
 from .shards import cp_shards, shard_rows, shard_segments, ulysses_heads  # noqa: F401
 
 

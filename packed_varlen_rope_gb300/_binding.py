@@ -19,7 +19,7 @@ EXPORTS = (
     "rope_cos_sin_cache_bytes", "rope_qk_positions",
     "rope_validate_cu_seqlens", "rope_qk_inv_freq", "rope_strerror", "rope_qk_abi_version",
     "glu_fwd", "glu_bwd", "rope_qk_host", "rope_qk_host_static", "rope_qk_launch_info",
-    "rope_cos_sin_eval",
+    "rope_cos_sin_eval", "rope_kv_append",
 )
 
 GLU_KINDS = {"swiglu": 0, "geglu": 1, "geglu_tanh": 2}
@@ -168,6 +168,9 @@ def load_library(path: Optional[str] = None):
     lib.glu_fwd.restype = ctypes.c_int
     lib.glu_bwd.argtypes = [i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     lib.glu_bwd.restype = ctypes.c_int
+    from ._attention import _declare
+
+    _declare(lib)
     lib.rope_qk_abi_version.argtypes = []
     lib.rope_qk_abi_version.restype = ctypes.c_int
     if path is None:

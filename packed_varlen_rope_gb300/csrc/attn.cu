@@ -1,0 +1,196 @@
+// Entry points of the attention operators: argument checks on the host, then the launch.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn.h"
+#include "attn_internal.h"
+#include "host_checks.h"
+#include "paged_checks.h"
+
+namespace {
+
+using namespace pvr;
+
+constexpr int kMaxAttnDim = 128;
+constexpr int kMaxGroup = 128;
+
+int check_heads(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, float scale)
+{
+    if (T < 0 || n_seqs < 0 || hq < 1 || hkv < 1 || hq > (1 << 20) || hq % hkv != 0) return ROPE_ERR_SHAPE;
+    if (d < 16 || d > kMaxAttnDim || d % 16 != 0) return ROPE_ERR_HEAD_DIM;
+    if (hq / hkv > kMaxGroup || T > kMaxTokens) return ROPE_ERR_UNSUPPORTED;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return ROPE_ERR_THETA;
+    return ROPE_OK;
+}
+
+Rows rows_of(const View &v)
+{
+    return Rows{static_cast<__nv_bfloat16 *>(const_cast<void *>(v.base)), v.ts, v.hs};
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? ROPE_OK : ROPE_ERR_LAUNCH; }
+
+// Checks shared by the forward and the backward; fills the problem.
+int varlen_problem(const attn_varlen_desc &p, AttnProblem &a, View (&in)[3], View &out)
+{
+    int rc = check_heads(p.total_tokens, p.n_seqs, p.n_q_heads, p.n_kv_heads, p.head_dim, p.scale);
+    if (rc != ROPE_OK || p.total_tokens == 0) return rc;
+    if (p.cu_seqlens == nullptr) return ROPE_ERR_NULL;
+    const int64_t T = p.total_tokens, d = p.head_dim;
+    in[0] = View{p.q, T, p.n_q_heads, p.q_stride_token, p.q_stride_head, d};
+    in[1] = View{p.k, T, p.n_kv_heads, p.k_stride_token, p.k_stride_head, d};
+    in[2] = View{p.v, T, p.n_kv_heads, p.v_stride_token, p.v_stride_head, d};
+    out = View{p.out, T, p.n_q_heads, p.out_stride_token, p.out_stride_head, d};
+    for (const View *v : {&in[0], &in[1], &in[2], &out})
+        if ((rc = check_view(*v)) != ROPE_OK) return rc;
+    for (const View &v : in)
+        if (!views_disjoint(v, out)) return ROPE_ERR_OVERLAP;
+    a = AttnProblem{};
+    a.q = rows_of(in[0]);
+    a.k = rows_of(in[1]);
+    a.v = rows_of(in[2]);
+    a.out = rows_of(out);
+    a.lse = p.lse;
+    a.cu = p.cu_seqlens;
+    a.used = p.seq_used;
+    a.n_tokens = static_cast<int32_t>(T);
+    a.n_seqs = p.n_seqs;
+    a.hq = p.n_q_heads;
+    a.hkv = p.n_kv_heads;
+    a.group = p.n_q_heads / p.n_kv_heads;
+    a.d = p.head_dim;
+    a.causal = p.causal != 0;
+    a.scale = p.scale;
+    return ROPE_OK;
+}
+
+// Sizes of a paged call.
+int check_paged_sizes(const attn_paged_desc &p)
+{
+    int rc = check_heads(p.total_tokens, p.n_seqs, p.n_q_heads, p.cache.n_kv_heads, p.cache.head_dim, p.scale);
+    if (rc != ROPE_OK) return rc;
+    if (p.reserved != 0) return ROPE_ERR_UNSUPPORTED;
+    if (p.max_pages < 0 || p.max_kv_len < 0) return ROPE_ERR_SHAPE;
+    if (p.cache.page_size < 8 || p.cache.page_size > 65536 || p.cache.page_size % 8 != 0) return ROPE_ERR_SHAPE;
+    if (static_cast<int64_t>(p.max_pages) * p.cache.page_size > INT32_MAX / 2) return ROPE_ERR_UNSUPPORTED;
+    return ROPE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_varlen_fwd(const attn_varlen_desc *desc, void *stream)
+{
+    if (desc == nullptr) return ROPE_ERR_NULL;
+    AttnProblem a;
+    View in[3], out;
+    const int rc = varlen_problem(*desc, a, in, out);
+    if (rc != ROPE_OK || desc->total_tokens == 0) return rc;
+    if (!aligned(a.lse, 4)) return ROPE_ERR_ALIGN;
+    return status_of(launch_attn_simple_fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t attn_varlen_bwd_workspace_bytes(int64_t total_tokens, int32_t n_q_heads)
+{
+    if (total_tokens < 0 || total_tokens > kMaxTokens || n_q_heads < 1 || n_q_heads > (1 << 20)) return -1;
+    return total_tokens * n_q_heads * static_cast<int64_t>(sizeof(float));
+}
+
+int attn_varlen_bwd(const attn_varlen_desc *desc, const attn_varlen_grads *grads, void *workspace,
+                    int64_t workspace_bytes, void *stream)
+{
+    if (desc == nullptr || grads == nullptr) return ROPE_ERR_NULL;
+    AttnProblem a;
+    View in[5], out;
+    View qkv[3];
+    int rc = varlen_problem(*desc, a, qkv, out);
+    if (rc != ROPE_OK || desc->total_tokens == 0) return rc;
+    const int64_t T = desc->total_tokens, d = desc->head_dim;
+    const attn_varlen_grads &g = *grads;
+    for (int i = 0; i < 3; ++i) in[i] = qkv[i];
+    in[3] = out;
+    in[4] = View{g.dout, T, a.hq, g.dout_stride_token, g.dout_stride_head, d};
+    const View res[3] = {{g.dq, T, a.hq, g.dq_stride_token, g.dq_stride_head, d},
+                         {g.dk, T, a.hkv, g.dk_stride_token, g.dk_stride_head, d},
+                         {g.dv, T, a.hkv, g.dv_stride_token, g.dv_stride_head, d}};
+    if ((rc = check_view(in[4])) != ROPE_OK) return rc;
+    for (const View &v : res)
+        if ((rc = check_view(v)) != ROPE_OK) return rc;
+    for (int i = 0; i < 3; ++i) {
+        for (const View &v : in)
+            if (!views_disjoint(v, res[i])) return ROPE_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (!views_disjoint(res[j], res[i])) return ROPE_ERR_OVERLAP;
+    }
+    if (a.lse == nullptr || workspace == nullptr) return ROPE_ERR_NULL;
+    if (!aligned(a.lse, 4) || !aligned(workspace, 16)) return ROPE_ERR_ALIGN;
+    if (workspace_bytes < attn_varlen_bwd_workspace_bytes(T, a.hq)) return ROPE_ERR_WORKSPACE;
+    a.delta = static_cast<float *>(workspace);
+    a.dout = rows_of(in[4]);
+    a.dq = rows_of(res[0]);
+    a.dk = rows_of(res[1]);
+    a.dv = rows_of(res[2]);
+    return status_of(launch_attn_simple_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc)
+{
+    if (desc == nullptr) return ROPE_ERR_NULL;
+    const int rc = check_paged_sizes(*desc);
+    return rc != ROPE_OK ? rc : 0;
+}
+
+int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (desc == nullptr) return ROPE_ERR_NULL;
+    const attn_paged_desc &p = *desc;
+    const rope_paged_kv &c = p.cache;
+    int rc;
+    if ((rc = check_paged_sizes(p)) != ROPE_OK || (rc = check_paged(c)) != ROPE_OK) return rc;
+    const int64_t T = p.total_tokens, d = c.head_dim;
+    if (T == 0) return ROPE_OK;
+    if ((rc = check_page_table(p.cu_seqlens, p.kv_lens, p.page_table, p.page_table_stride, p.max_pages,
+                               p.n_seqs)) != ROPE_OK)
+        return rc;
+    const View q{p.q, T, p.n_q_heads, p.q_stride_token, p.q_stride_head, d};
+    const View out{p.out, T, p.n_q_heads, p.out_stride_token, p.out_stride_head, d};
+    for (const View *v : {&q, &out})
+        if ((rc = check_view(*v)) != ROPE_OK) return rc;
+    if (!views_disjoint(q, out)) return ROPE_ERR_OVERLAP;
+    if (c.n_pages > 0 && (overlap(c.k, 2 * k_span(c), p.out, out.bytes()) ||
+                          overlap(c.v, 2 * v_span(c), p.out, out.bytes())))
+        return ROPE_ERR_OVERLAP;
+    const int64_t need = attn_paged_workspace_bytes(desc);
+    if (need > 0 && workspace == nullptr) return ROPE_ERR_NULL;
+    if (need > 0 && !aligned(workspace, 16)) return ROPE_ERR_ALIGN;
+    if (workspace_bytes < need) return ROPE_ERR_WORKSPACE;
+
+    AttnProblem a{};
+    a.q = rows_of(q);
+    a.out = rows_of(out);
+    a.paged = 1;
+    a.pages = Pages{static_cast<const __nv_bfloat16 *>(c.k), static_cast<const __nv_bfloat16 *>(c.v),
+                    c.k_stride_page, c.k_stride_token, c.k_stride_head,
+                    c.v_stride_page, c.v_stride_token, c.v_stride_head,
+                    p.page_table, p.page_table_stride,
+                    c.n_pages > 0 ? p.max_pages : 0, c.page_size, static_cast<int32_t>(c.n_pages)};
+    a.cu = p.cu_seqlens;
+    a.used = p.kv_lens;
+    a.n_tokens = static_cast<int32_t>(T);
+    a.n_seqs = p.n_seqs;
+    a.hq = p.n_q_heads;
+    a.hkv = c.n_kv_heads;
+    a.group = a.hq / a.hkv;
+    a.d = c.head_dim;
+    a.causal = p.causal != 0;
+    a.scale = p.scale;
+    return status_of(launch_attn_simple_fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_fault(void) { return 0; }
+
+}  // extern "C"
