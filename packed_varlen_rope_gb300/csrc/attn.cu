@@ -19,9 +19,10 @@ constexpr int kMaxGroup = 128;
 
 int check_heads(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, float scale)
 {
-    if (T < 0 || n_seqs < 0 || hq < 1 || hkv < 1 || hq > (1 << 20) || hq % hkv != 0) return ROPE_ERR_SHAPE;
+    if (T < 0 || n_seqs < 0 || hq < 1 || hkv < 1 || hq > (1 << 20) || hq % hkv != 0 || n_seqs > kMaxTokens) return ROPE_ERR_SHAPE;
     if (d < 16 || d > kMaxAttnDim || d % 16 != 0) return ROPE_ERR_HEAD_DIM;
-    if (hq / hkv > kMaxGroup || T > kMaxTokens) return ROPE_ERR_UNSUPPORTED;
+    // (token, head) rows are counted in 32 bits
+    if (hq / hkv > kMaxGroup || T > kMaxTokens || T * hq > INT32_MAX) return ROPE_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return ROPE_ERR_THETA;
     return ROPE_OK;
 }
@@ -79,6 +80,21 @@ int check_paged_sizes(const attn_paged_desc &p)
     return ROPE_OK;
 }
 
+// How many CTAs share the keys of a row: from the sizes on the host alone.
+int splits_of(const attn_paged_desc &p)
+{
+    if (p.total_tokens == 0) return 1;
+    AttnProblem a{};
+    a.n_tokens = static_cast<int32_t>(p.total_tokens);
+    a.n_seqs = p.n_seqs;
+    a.hq = p.n_q_heads;
+    a.hkv = p.cache.n_kv_heads;
+    a.group = a.hq / a.hkv;
+    int64_t keys = static_cast<int64_t>(p.max_pages) * p.cache.page_size;
+    if (p.max_kv_len > 0 && p.max_kv_len < keys) keys = p.max_kv_len;
+    return attn_fwd_splits(a, keys);
+}
+
 }  // namespace
 
 extern "C" {
@@ -91,7 +107,7 @@ int attn_varlen_fwd(const attn_varlen_desc *desc, void *stream)
     const int rc = varlen_problem(*desc, a, in, out);
     if (rc != ROPE_OK || desc->total_tokens == 0) return rc;
     if (!aligned(a.lse, 4)) return ROPE_ERR_ALIGN;
-    return status_of(launch_attn_simple_fwd(a, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_attn_fwd(a, 1, nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 int64_t attn_varlen_bwd_workspace_bytes(int64_t total_tokens, int32_t n_q_heads)
@@ -141,7 +157,8 @@ int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc)
 {
     if (desc == nullptr) return ROPE_ERR_NULL;
     const int rc = check_paged_sizes(*desc);
-    return rc != ROPE_OK ? rc : 0;
+    if (rc != ROPE_OK) return rc;
+    return 4 * attn_split_floats(desc->total_tokens, desc->n_q_heads, desc->cache.head_dim, splits_of(*desc));
 }
 
 int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream)
@@ -188,9 +205,9 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
     a.d = c.head_dim;
     a.causal = p.causal != 0;
     a.scale = p.scale;
-    return status_of(launch_attn_simple_fwd(a, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_attn_fwd(a, splits_of(p), static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
-int attn_fault(void) { return 0; }
+int attn_fault(void) { return pvr::attn_fault_word(); }
 
 }  // extern "C"

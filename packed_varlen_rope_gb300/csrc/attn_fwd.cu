@@ -1,0 +1,610 @@
+// Attention forward on the tensor cores (GB300, sm_103a): packed samples or a paged cache.
+//
+// Mathematics.  For each row the running maximum m and sum l of a softmax over key tiles:
+//   s = scale q.k;  m' = max(m, max s);  p = exp(s - m');  l' = l exp(m - m') + sum p;
+//   o' = o exp(m - m') + p V.  Exponentials are base 2 with scale*log2(e) folded in.
+// The rescaling of o and l is put off until the maximum has grown by more than 2^8, so p
+// stays below 256 and most tiles need none; the result is the same.
+//
+// Layout.  A CTA owns 256 rows of one key head: two tiles of 128 rows, a row being one
+// (token, query head) pair with the G heads that share the key head side by side, so every
+// key tile is loaded once for all of them and a decoding step fills rows with heads.  Key
+// and value tiles are 128 tokens, brought in by TMA through a ring of shared-memory
+// stages.  Warps 0-3 and 4-7 run the softmax of one tile of rows each (a row a thread,
+// scores straight from tensor memory), warp 8 issues the products, warp 9 the loads.
+// While one group computes its softmax the tensor core works for the other.
+//   S_x = Q_x K^T      128x128 in tensor memory, both operands from shared memory
+//   O_x += P_x V       P as bf16 over S's columns in tensor memory, V from shared memory
+//
+// The bound is the tensor core: per key tile and row tile two 128x128x128 products (1024
+// cycles at its rate) against about 700 issue cycles of softmax a warp scheduler.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_internal.h"
+#include "rope_qk.h"
+#include "tensor_core.cuh"
+#include "tensor_map.h"
+
+namespace pvr {
+
+__device__ int g_attn_fault;            // a bounded wait ran out
+
+namespace {
+
+constexpr int kThreads = 384;              // two softmax warpgroups, one for products and loads
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;   // 2 * 224 + 56 = 3 * 168, the launch's
+constexpr int kRows = 128;              // rows of a row tile
+constexpr int kKeys = 128;              // keys of a key tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.0f;           // log2 growth of the maximum that triggers a rescale
+constexpr float kFoldLimit = 4096.0f;   // |m| (log2) up to which m is folded into the FMA
+
+struct FwdArgs {
+    CUtensorMap q, k, v;
+    __nv_bfloat16 *out;
+    int64_t out_ts, out_hs;
+    float *lse;                         // [hq, T] or NULL
+    float *part_o, *part_lse;           // [split][T * hq][d], [split][T * hq], or NULL
+    const int32_t *cu, *used;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t max_pages, page_size, n_pages, box_rows;
+    int32_t n_tokens, n_seqs, hq, hkv, group, tile_tokens, d, causal;   // tile_tokens: of one row tile
+    int32_t n_slots, splits;
+    float scale;
+};
+
+template <int DP>
+struct Shared {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr int kTileBytes = kKeys * DP * 2;
+    static constexpr int kStages = DP == 128 ? 4 : 6;
+    static constexpr int kOffKV = 2 * kTileBytes;                     // after the two Q tiles
+    static constexpr int kOffBars = kOffKV + kStages * kTileBytes;
+    static constexpr int kBytes = kOffBars + 256 + 1024;              // + alignment slack
+};
+
+template <int DP, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdArgs a)
+{
+    using Sh = Shared<DP>;
+    constexpr int kStages = Sh::kStages;
+    constexpr uint32_t kBoxBytes = kKeys * 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = smem_addr(smem);
+    const uint32_t bars = base + Sh::kOffBars;
+    const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_done = bars + 48, kv_full = bars + 64,
+                   kv_empty = kv_full + 8 * kStages, drain = kv_empty + 8 * kStages;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ TileSlot s_slot;
+    __shared__ int s_used;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_done + 8 * i, 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(kv_full + 8 * i, 1);
+            mbar_init(kv_empty + 8 * i, 1);
+        }
+        mbar_init(drain, 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (warp == 8) tmem_alloc(smem_addr(&s_tmem), 512);
+    if (warp == 9 && lane == 0) {
+        tma_prefetch_map(&a.q);
+        tma_prefetch_map(&a.k);
+        tma_prefetch_map(&a.v);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int kvh = blockIdx.x % a.hkv;
+    const int split = blockIdx.y;
+    // causal rows near a sample's end have the most keys: late slots go first
+    const int slot = a.n_slots - 1 - static_cast<int>(blockIdx.x) / a.hkv;
+    const int cta_tokens = 2 * a.tile_tokens;
+    if (warp == 0) {
+        const TileSlot f = find_slot(a.cu, a.n_seqs, a.n_tokens, cta_tokens, slot);
+        int used = 0;
+        if (f.sample >= 0 && f.sample < a.n_seqs) used = a.used != nullptr ? __ldg(a.used + f.sample) : f.end - f.start;
+        if (lane == 0) {
+            s_slot = f;
+            s_used = used;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const TileSlot where = s_slot;
+    const int first = where.tile * cta_tokens;                         // token of the sample the CTA starts at
+    const int len = where.end - where.start;
+    const bool live = where.tile >= 0 && first < len;
+    // rows in use, keys, and how far past a row's index its keys go
+    int rows_used, keys, offset;
+    if (PAGED) {
+        const bool inside = where.sample >= 0 && where.sample < a.n_seqs;
+        const int kv = max(s_used, -1);
+        rows_used = inside ? len : 0;
+        keys = inside ? static_cast<int>(min(static_cast<int64_t>(max(kv, 0)),
+                                             static_cast<int64_t>(a.max_pages) * a.page_size)) : 0;
+        offset = kv - len;
+    } else {
+        rows_used = min(len, max(s_used, 0));
+        keys = rows_used;
+        offset = 0;
+    }
+    // keys that row `i` of the sample sees (a prefix)
+    auto limit = [&](int i) {
+        if (i >= rows_used || i + offset < 0) return 0;
+        return a.causal ? min(keys, i + offset + 1) : keys;
+    };
+    int count[2], lo_tile = 0, n_tiles = 0;
+    {
+        int n[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int last = min(first + (x + 1) * a.tile_tokens, rows_used) - 1;
+            n[x] = live && last >= first + x * a.tile_tokens ? (limit(last) + kKeys - 1) / kKeys : 0;
+        }
+        const int all = max(n[0], n[1]);
+        const int chunk = (all + a.splits - 1) / a.splits;
+        lo_tile = split * chunk;
+        const int hi = min(all, lo_tile + chunk);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) count[x] = max(0, min(n[x], hi) - lo_tile);
+        n_tiles = max(count[0], count[1]);
+    }
+    constexpr uint32_t kColS = 0, kColO = 256;
+
+    if (warp >= 8) {
+    regs_shrink<kRegsOther>();
+    if (warp == 9) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x) {
+                if (count[x] == 0) continue;
+                mbar_expect_tx(q_full + 8 * x, static_cast<uint32_t>(a.group * a.tile_tokens) * 128 * Sh::kBoxes);
+                for (int b = 0; b < Sh::kBoxes; ++b)
+                    tma_load_3d(base + x * Sh::kTileBytes + b * kBoxBytes, &a.q, 64 * b, kvh * a.group,
+                                where.start + first + x * a.tile_tokens, q_full + 8 * x);
+            }
+        }
+        const int per_tile = kKeys / a.box_rows;                       // boxes down a tile
+        const int box = lane % (PAGED ? per_tile : 1), col = lane / (PAGED ? per_tile : 1);
+        int issued = 0;
+        for (int i = 0; i < n_tiles; ++i) {
+            const int key0 = (lo_tile + i) * kKeys;
+            int c_slot = where.start + key0, c_page = 0;
+            if (PAGED) {
+                // keys past the sequence's end read as zero: a page coordinate past the pool's
+                const int key = key0 + box * a.box_rows;
+                c_page = a.n_pages;
+                c_slot = 0;
+                if (key < keys) {
+                    const int index = key / a.page_size;
+                    c_page = __ldg(a.table + where.sample * a.table_stride + index);
+                    c_slot = key - index * a.page_size;
+                    if (c_page < 0 || c_page >= a.n_pages) c_page = a.n_pages;
+                }
+            }
+            bool ok = true;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int t = 2 * i + kv, stage = t % kStages;
+                if (t >= kStages) ok = mbar_wait(kv_empty + 8 * stage, (t / kStages - 1) & 1, &s_abort, &g_attn_fault);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = kv_full + 8 * stage;
+                const uint32_t dst = base + Sh::kOffKV + stage * Sh::kTileBytes + col * kBoxBytes +
+                                     static_cast<uint32_t>(box * a.box_rows) * 128;
+                if (lane == 0) mbar_expect_tx(bar, Sh::kTileBytes);
+                __syncwarp();
+                if (col < Sh::kBoxes) tma_load_4d(dst, kv == 0 ? &a.k : &a.v, 64 * col, c_slot, kvh, c_page, bar);
+                ++issued;
+            }
+            if (!ok) break;
+        }
+        if (s_abort != 0) {             // copies in flight land before the memory is given back
+            for (int t = max(0, issued - kStages); t < issued; ++t)
+                for (int w = 0; w < kWaitLimit && !mbar_try(kv_full + 8 * (t % kStages), (t / kStages) & 1); ++w) {}
+            for (int x = 0; x < 2; ++x)
+                if (count[x] > 0)
+                    for (int w = 0; w < kWaitLimit && !mbar_try(q_full + 8 * x, 0); ++w) {}
+        }
+    } else if (warp == 8) {
+        // --------------------------------------------------------- products
+        constexpr uint32_t kDescS = mma_desc(kRows, kKeys, false);
+        constexpr uint32_t kDescO = mma_desc(kRows, DP, true);
+        auto scores = [&](int x, int stage) {
+            const uint32_t q = base + x * Sh::kTileBytes, k = base + Sh::kOffKV + stage * Sh::kTileBytes;
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s) {
+                const uint32_t at = (s / 4) * kBoxBytes + (s % 4) * 32;
+                mma_ss(tmem + kColS + x * kKeys, smem_desc(q + at, 0, 1024), smem_desc(k + at, 0, 1024), kDescS, s > 0);
+            }
+            tc_commit(s_full + 8 * x);
+        };
+        bool ok = true;
+        auto wait = [&](uint32_t bar, int phase) {
+            if (ok && !mbar_wait(bar, phase & 1, &s_abort, &g_attn_fault)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        };
+        if (n_tiles > 0) {
+            wait(kv_full, 0);
+            for (int x = 0; x < 2; ++x) {
+                if (count[x] == 0) continue;
+                wait(q_full + 8 * x, 0);
+                if (ok && lane == 0) scores(x, 0);
+            }
+            if (ok && lane == 0) tc_commit(kv_empty);
+        }
+        for (int i = 0; ok && i < n_tiles; ++i) {
+            const int tv = 2 * i + 1, sv = tv % kStages, tk = 2 * i + 2, sk = tk % kStages;
+            const uint32_t v = base + Sh::kOffKV + sv * Sh::kTileBytes;
+            wait(kv_full + 8 * sv, tv / kStages);
+            // value rows past the last key (another sample's, or stale) are cleared: their
+            // weights are zero, but zero times NaN is not
+            const int valid = keys - (lo_tile + i) * kKeys;
+            if (ok && valid < kKeys) {
+                for (int r = valid + (lane >> 3); r < kKeys; r += 4)
+                    for (int b = 0; b < Sh::kBoxes; ++b)
+                        *reinterpret_cast<uint4 *>(smem + (v - base) + b * kBoxBytes + r * 128 + (lane & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            bool have_k = false;
+            for (int x = 0; x < 2; ++x) {
+                if (i >= count[x]) continue;
+                wait(p_full + 8 * x, i);
+                if (ok && lane == 0) {
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s)
+                        mma_ts(tmem + kColO + x * DP, tmem + kColS + x * kKeys + s * 8,
+                               smem_desc(v + s * 2048, kBoxBytes, 1024), kDescO, i > 0 || s > 0);
+                    if (i + 1 == count[x]) tc_commit(o_done + 8 * x);
+                }
+                if (i + 1 < count[x]) {
+                    if (!have_k) wait(kv_full + 8 * sk, tk / kStages);
+                    have_k = true;
+                    if (ok && lane == 0) scores(x, sk);
+                }
+            }
+            if (ok && lane == 0) {
+                tc_commit(kv_empty + 8 * sv);
+                if (i + 1 < n_tiles) tc_commit(kv_empty + 8 * sk);
+            }
+        }
+        if (!ok) {                      // products in flight finish before tensor memory is freed
+            if (lane == 0) tc_commit(drain);
+            for (int w = 0; w < kWaitLimit && !mbar_try(drain, 0); ++w) {}
+        }
+        __syncwarp();
+    }
+    } else {
+        // ---------------------------------------------------------- softmax
+        regs_grow<kRegsSoftmax>();
+        const int x = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + kColS + x * kKeys, t_o = tmem + lanes + kColO + x * DP;
+        const int tok0 = first + x * a.tile_tokens;                    // of the sample
+        const int i_tok = tok0 + row / a.group;
+        const bool mine = live && row < a.group * a.tile_tokens && i_tok < len;
+        const int lim = mine ? limit(i_tok) : 0;
+        const int lim_all = limit(tok0);                               // the fewest keys a row of the tile sees
+        const float c = a.scale * kLog2e;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < count[x]; ++i) {
+            ok = mbar_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, reinterpret_cast<uint32_t(&)[32]>(s[32 * j]));
+            tc_wait_ld(reinterpret_cast<uint32_t(&)[32]>(s[0]));
+#pragma unroll
+            for (int j = 1; j < 4; ++j) tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32 * j]));
+            const int key0 = (lo_tile + i) * kKeys;
+            if (key0 + kKeys > lim_all) {
+                const int left = lim - key0;
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j >= left) s[j] = 0xff800000u;
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[j]));
+            const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if (i == 0) {
+                m = high;
+            } else if (__any_sync(0xffffffffu, (high - m) * c > kGrow)) {
+                // S of this tile is complete, and with it every earlier product into O
+                const float grown = fmaxf(m, high);
+                const float shrink = m == grown ? 1.0f : ex2((m - grown) * c);
+                m = grown;
+                l *= shrink;
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + 16 * j, o);
+                    tc_wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                    tmem_st16(t_o + 16 * j, o);
+                }
+            }
+            // p = 2^(s c - m c): the product s c is exact inside the FMA, and the rounding of
+            // m c is common to the row, so it cancels against l -- unless it is large
+            float mc = m == -INFINITY ? 0.0f : m * c;
+            if (__any_sync(0xffffffffu, fabsf(mc) > kFoldLimit)) {
+                const float shift = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int j = 0; j < 128; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
+                mc = 0.0f;
+            }
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                float2 p = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, mc2);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                sum[j & 1] = add2(sum[j & 1], p);
+                s[j] = pack_bf16(p.x, p.y);
+            }
+            tmem_st32(t_s, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+            tmem_st32(t_s + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 8 * x);
+        }
+        if (ok && count[x] > 0) {
+            ok = mbar_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        }
+        // epilogue: rows outside the pack, and rows that see no key, are zero (tiles that all
+        // rows in use see whole are not masked, so such rows may have summed anything)
+        if (lim == 0) l = 0.0f;
+        const int tok = where.start + i_tok;
+        const int head = kvh * a.group + row % a.group;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const bool joined = PAGED && a.splits > 1;
+        const int64_t at = static_cast<int64_t>(tok) * a.hq + head;
+        if (ok && mine) {
+            if (joined) {
+                a.part_lse[static_cast<int64_t>(split) * a.n_tokens * a.hq + at] =
+                    l > 0.0f ? m * c + log2f(l) : -INFINITY;
+            } else if (a.lse != nullptr) {
+                a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l > 0.0f ? m * a.scale + kLn2 * log2f(l) : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+            uint32_t o[32];
+            __syncwarp();
+            if (ok && count[x] > 0) {
+                tmem_ld32(t_o + 32 * j, o);
+                tc_wait_ld(o);
+            }
+            if (!ok || !mine) continue;
+            if (l == 0.0f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+            if (joined) {
+                float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(split) * a.n_tokens * a.hq + at) *
+                                                                        a.d + 32 * j);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (32 * j + 4 * e < a.d && l > 0.0f)
+                        dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                             __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + tok * a.out_ts + head * a.out_hs + 32 * j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (32 * j + 8 * e >= a.d) continue;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        w[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+                    dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// Joins the partial results of the splits: o = sum_i w_i o_i, w_i = 2^(lse_i - lse).  One
+// warp a row, 4 elements a lane.
+__global__ void __launch_bounds__(128) attn_join_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
+                                                        __nv_bfloat16 *__restrict__ out, int64_t out_ts, int64_t out_hs,
+                                                        int n_rows, int hq, int d, int splits)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= n_rows) return;
+    float m = -INFINITY;
+    for (int i = lane; i < splits; i += 32) m = fmaxf(m, part_lse[static_cast<int64_t>(i) * n_rows + row]);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.0f;
+    if (m > -INFINITY) {
+        for (int i0 = 0; i0 < splits; i0 += 32) {
+            const float mine = i0 + lane < splits ? part_lse[static_cast<int64_t>(i0 + lane) * n_rows + row] : -INFINITY;
+            const int n = min(32, splits - i0);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float lse = __shfl_sync(0xffffffffu, mine, i);
+                if (lse == -INFINITY) continue;            // nothing was written there
+                const float w = exp2f(lse - m);
+                l += w;
+                if (4 * lane < d) {
+                    const float4 o = *reinterpret_cast<const float4 *>(
+                        part_o + (static_cast<int64_t>(i0 + i) * n_rows + row) * d + 4 * lane);
+                    acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w;
+                }
+            }
+        }
+    }
+    if (4 * lane >= d) return;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int tok = row / hq, head = row % hq;
+    *reinterpret_cast<uint2 *>(out + tok * out_ts + head * out_hs + 4 * lane) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+template <int DP, bool PAGED>
+cudaError_t launch_fwd(const FwdArgs &a, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> sized{0};
+    const cudaError_t err = allow_smem(attn_fwd_kernel<DP, PAGED>, Shared<DP>::kBytes, sized);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.hkv), static_cast<unsigned>(a.splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shared<DP>::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<DP, PAGED>, a);
+}
+
+}  // namespace
+
+// Splits of the keys: enough CTAs to fill the GPU, at least two key tiles a split.
+int attn_fwd_splits(const AttnProblem &p, int64_t max_kv)
+{
+    const int tile = kRows / p.group;
+    const int64_t ctas = static_cast<int64_t>(slot_count(p.n_tokens, p.n_seqs, 2 * tile)) * p.hkv;
+    const int64_t tiles = (max_kv + kKeys - 1) / kKeys;
+    int64_t want = kSMs / ctas;
+    if (want > tiles / 2) want = tiles / 2;
+    return static_cast<int>(want < 1 ? 1 : want > 128 ? 128 : want);
+}
+
+cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, cudaStream_t stream)
+{
+    FwdArgs a;
+    const int dp = p.d <= 64 ? 64 : 128;
+    const int tile = kRows / p.group;
+    a.tile_tokens = tile;
+    {
+        const int64_t ext[3] = {p.d, p.hq, p.n_tokens}, st[3] = {1, p.q.hs, p.q.ts};
+        const int box[3] = {64, p.group, tile};
+        if (!make_map(&a.q, p.q.p, 3, ext, st, box)) return cudaErrorInvalidValue;
+    }
+    a.box_rows = kKeys;
+    if (p.paged) {
+        a.box_rows = p.pages.page_size & -p.pages.page_size;
+        if (a.box_rows > kKeys) a.box_rows = kKeys;
+        // an empty pool: a map over one page that no coordinate reaches
+        const bool none = p.pages.n_pages == 0;
+        const int64_t ext[4] = {p.d, p.pages.page_size, p.hkv, none ? 1 : p.pages.n_pages};
+        const int64_t ks[4] = {1, p.pages.k_ts, p.pages.k_hs, p.pages.k_ps};
+        const int64_t vs[4] = {1, p.pages.v_ts, p.pages.v_hs, p.pages.v_ps};
+        const int box[4] = {64, a.box_rows, 1, 1};
+        if (!make_map(&a.k, none ? p.q.p : p.pages.k, 4, ext, ks, box) ||
+            !make_map(&a.v, none ? p.q.p : p.pages.v, 4, ext, vs, box))
+            return cudaErrorInvalidValue;
+    } else {
+        const int64_t ext[4] = {p.d, p.n_tokens, p.hkv, 1};
+        const int64_t ks[4] = {1, p.k.ts, p.k.hs, 0}, vs[4] = {1, p.v.ts, p.v.hs, 0};
+        const int box[4] = {64, kKeys, 1, 1};
+        if (!make_map(&a.k, p.k.p, 4, ext, ks, box) || !make_map(&a.v, p.v.p, 4, ext, vs, box))
+            return cudaErrorInvalidValue;
+    }
+    a.out = p.out.p;
+    a.out_ts = p.out.ts;
+    a.out_hs = p.out.hs;
+    a.lse = p.lse;
+    a.cu = p.cu;
+    a.used = p.used;
+    a.table = p.pages.table;
+    a.table_stride = p.pages.table_stride;
+    a.max_pages = p.pages.max_pages;
+    a.page_size = p.pages.page_size;
+    a.n_pages = p.pages.n_pages;
+    a.n_tokens = p.n_tokens;
+    a.n_seqs = p.n_seqs;
+    a.hq = p.hq;
+    a.hkv = p.hkv;
+    a.group = p.group;
+    a.d = p.d;
+    a.causal = p.causal;
+    a.n_slots = slot_count(p.n_tokens, p.n_seqs, 2 * tile);
+    a.splits = splits;
+    a.scale = p.scale;
+    const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;
+    a.part_o = workspace;
+    a.part_lse = splits > 1 ? workspace + splits * rows * p.d : nullptr;
+    cudaError_t err;
+    if (p.paged) err = dp == 64 ? launch_fwd<64, true>(a, stream) : launch_fwd<128, true>(a, stream);
+    else err = dp == 64 ? launch_fwd<64, false>(a, stream) : launch_fwd<128, false>(a, stream);
+    if (err != cudaSuccess || splits <= 1) return err;
+    return launch_attn_join(a.part_o, a.part_lse, p, splits, stream);
+}
+
+cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
+                             cudaStream_t stream)
+{
+    const int rows = p.n_tokens * p.hq;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel, part_o, part_lse, p.out.p, p.out.ts, p.out.hs, rows, p.hq, p.d,
+                              splits);
+}
+
+int attn_fault_word()
+{
+    int word = 0;
+    if (cudaMemcpyFromSymbol(&word, g_attn_fault, sizeof word) != cudaSuccess) return ROPE_ERR_LAUNCH;
+    return word;
+}
+
+}  // namespace pvr

@@ -35,7 +35,19 @@ struct AttnProblem {
     float scale;
 };
 
-cudaError_t launch_attn_simple_fwd(const AttnProblem &p, cudaStream_t stream);
+constexpr int kSMs = 152;
+
+// Forward on the tensor cores; with splits > 1 the keys of every row are split over that
+// many CTAs, and workspace holds attn_split_floats() floats.
+cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, cudaStream_t stream);
+int attn_fwd_splits(const AttnProblem &p, int64_t max_kv);
+inline int64_t attn_split_floats(int64_t n_tokens, int hq, int d, int splits)
+{
+    return splits > 1 ? n_tokens * hq * (static_cast<int64_t>(d) + 1) * splits : 0;
+}
+cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
+                             cudaStream_t stream);
+int attn_fault_word();
 cudaError_t launch_attn_simple_bwd(const AttnProblem &p, cudaStream_t stream);
 
 }  // namespace pvr

@@ -96,46 +96,6 @@ __device__ void key_value(const AttnProblem &p, const Sample &s, int seq_row, in
     v = load4(g.v + page * g.v_ps + slot * g.v_ts + kvh * g.v_hs + e);
 }
 
-__device__ int row_of(const AttnProblem &p, int t)
-{
-    int lo = 0, hi = p.n_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__global__ void simple_fwd(const AttnProblem p)
-{
-    const int64_t w = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32;
-    const int t = static_cast<int>(w / p.hq), head = static_cast<int>(w % p.hq), e = (threadIdx.x & 31) * 4;
-    if (t >= p.n_tokens) return;
-    Sample s;
-    float m = -INFINITY, l = 0.f;
-    float4 o = zero4();
-    if (sample_of(p, t, s)) {
-        const int seq = row_of(p, t);
-        const float4 q = e < p.d ? load4(p.q.p + t * p.q.ts + head * p.q.hs + e) : zero4();
-        const int last = p.causal ? min(s.keys, t - s.start + s.offset + 1) : s.keys;
-        for (int j = 0; j < last; ++j) {
-            float4 k, v;
-            key_value(p, s, seq, j, head / p.group, e, k, v);
-            const float x = dot(q, k) * p.scale;
-            const float m2 = fmaxf(m, x);
-            const float c = expf(m - m2), pj = expf(x - m2);
-            l = l * c + pj;
-            o.x *= c; o.y *= c; o.z *= c; o.w *= c;
-            axpy(o, pj, v);
-            m = m2;
-        }
-    }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    if (e < p.d) store4(p.out.p + t * p.out.ts + head * p.out.hs + e, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
-    if (p.lse != nullptr && e == 0) p.lse[static_cast<int64_t>(head) * p.n_tokens + t] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
 __global__ void simple_bwd_dq(const AttnProblem p)
 {
     const int64_t w = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32;
@@ -193,12 +153,6 @@ __global__ void simple_bwd_dkv(const AttnProblem p)
 unsigned grid_of(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-cudaError_t launch_attn_simple_fwd(const AttnProblem &p, cudaStream_t stream)
-{
-    simple_fwd<<<grid_of(int64_t(p.n_tokens) * p.hq), 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attn_simple_bwd(const AttnProblem &p, cudaStream_t stream)
 {

@@ -1,0 +1,297 @@
+// Blackwell tensor-core building blocks (sm_103a, PTX): mbarriers with bounded waits, TMA
+// tile loads, tensor memory and tcgen05.mma, as the attention kernels use them.
+//
+// Shared-memory tiles are boxes of 64 bf16 columns (128 bytes a row) in the 128-byte
+// swizzle, the layout TMA writes and the matrix descriptors name: 8 rows x 128 bytes are a
+// swizzle atom of 1024 bytes, and every box starts on a 1024-byte boundary.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace pvr {
+
+// Waits are bounded: after kWaitLimit tries of about a microsecond the waiter raises the
+// CTA's abort flag and the device's fault word, every other wait of the CTA then ends too,
+// and the kernel drains its copies, frees its tensor memory and returns.
+constexpr int kWaitLimit = 1 << 20;
+constexpr uint32_t kWaitHintNs = 1000;
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+                 " selp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity), "r"(kWaitHintNs)
+                 : "memory");
+    return done != 0;
+}
+
+// Waits for the phase of the given parity; false when the CTA gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
+{
+    if (mbar_try(bar, parity)) return true;
+    for (int i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if (*abort_flag != 0) return false;
+    }
+    *abort_flag = 1;
+    atomicExch(fault, 1);
+    return false;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Shared-memory writes of this thread become visible to the tensor core and TMA.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+
+// Arrives on the barrier when every tcgen05.mma this thread has issued is complete.
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Matrix descriptor of a 128-byte-swizzled bf16 tile at a shared-memory address: strides in
+// bytes.  K-major operands (the product's sum runs along the row): `stride` 1024 from one
+// group of 8 rows to the next, `lead` unused.  MN-major operands (the sum runs down the
+// rows): `stride` 1024 from 8 rows to the next 8, `lead` from one box of 64 columns to the
+// next.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+{
+    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: bf16 x bf16 -> binary32, M x N, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] B[smem], one k step of 16.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem].
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+}
+
+#define PVR_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
+                     "=r"(a[i + 6]), "=r"(a[i + 7])
+#define PVR_W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), \
+                     "r"(a[i + 6]), "r"(a[i + 7])
+
+// 32 consecutive columns of this warp's 32 lanes (one row a lane).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : PVR_R8(r, 0), PVR_R8(r, 8), PVR_R8(r, 16), PVR_R8(r, 24)
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : PVR_R8(r, 0), PVR_R8(r, 8)
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                 "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+                 ::"r"(addr), PVR_W8(r, 0), PVR_W8(r, 8), PVR_W8(r, 16), PVR_W8(r, 24)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                 "%13, %14, %15, %16};"
+                 ::"r"(addr), PVR_W8(r, 0), PVR_W8(r, 8)
+                 : "memory");
+}
+
+#define PVR_RW8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), \
+                      "+r"(a[i + 6]), "+r"(a[i + 7])
+
+// The loads before it are complete.  Naming the registers orders every use of them after
+// the wait; tmem_loaded does that for further registers of the same wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PVR_RW8(r, 0), PVR_RW8(r, 8), PVR_RW8(r, 16), PVR_RW8(r, 24)::"memory");
+}
+
+__device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PVR_RW8(r, 0), PVR_RW8(r, 8)::"memory");
+}
+
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32])
+{
+    asm volatile("" : PVR_RW8(r, 0), PVR_RW8(r, 8), PVR_RW8(r, 16), PVR_RW8(r, 24)::"memory");
+}
+
+// This warpgroup's registers a thread from here on (its share of the block's at launch).
+template <int N>
+__device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 2^x from the special-function unit (subnormal results flush to zero).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Both halves of a pair through one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+        " mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n"
+        " mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The sample a tile slot belongs to.  The token axis [0, T) is cut at cu[0..n] into n + 2
+// stretches (what lies before the pack, the samples, what lies after it), and stretch s
+// owns the slots from floor(start_s / tile) + s on: room for every one of its tiles,
+// with no prefix sum over the samples and no size read on the host.  T / tile + n + 2 slots
+// cover any pack; those past a stretch's last tile are empty.
+struct TileSlot {
+    int sample;        // -1 or n: outside the pack
+    int start, end;    // the stretch's tokens [start, end), inside [0, T]
+    int tile;          // index of the tile in the stretch
+};
+
+// Called by a whole warp.  Whatever cu holds, start and end stay in [0, T].
+__device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, int n, int T, int tile_tokens, int slot)
+{
+    const int lane = threadIdx.x & 31;
+    auto bound = [&](int s) {                      // first token of stretch s, s in [0, n + 2]
+        if (s <= 0) return 0;
+        if (s >= n + 2) return T;
+        return min(max(__ldg(cu + (s - 1)), 0), T);
+    };
+    int lo = 0, len = n + 2;
+    while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int s = lo + lane * step;
+        const bool below = s < lo + len && bound(s) / tile_tokens + s <= slot;
+        const uint32_t vote = __ballot_sync(0xffffffffu, below);
+        const int hit = vote == 0xffffffffu ? 31 : __ffs(~vote) - 2;       // last of the leading run
+        const int at = lo + max(hit, 0) * step;
+        len = min(step, lo + len - at);
+        lo = at;
+    }
+    TileSlot r;
+    r.sample = lo - 1;
+    r.start = bound(lo);
+    r.end = max(bound(lo + 1), r.start);
+    r.tile = slot - (r.start / tile_tokens + lo);
+    return r;
+}
+
+__host__ __device__ inline int slot_count(int T, int n, int tile_tokens) { return T / tile_tokens + n + 2; }
+
+}  // namespace pvr
