@@ -313,7 +313,7 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
     """Gradients (dq, dk, dv) of ``attn_varlen_fwd`` for the output gradient ``dout`` (C entry
     point ``attn_varlen_bwd``), with the ``out`` and ``lse`` that it returned and its other
     arguments.  dq, dk and dv are written whole (new tensors unless given; rows of no sample
-    get 0).  ``workspace``: a CUDA tensor of at least 4 * T * Hq bytes; allocated through
+    get 0).  ``workspace``: a CUDA tensor of at least 8 * T * Hq bytes; allocated through
     torch unless given."""
     import torch
 

@@ -113,7 +113,7 @@ int attn_varlen_fwd(const attn_varlen_desc *desc, void *stream)
 int64_t attn_varlen_bwd_workspace_bytes(int64_t total_tokens, int32_t n_q_heads)
 {
     if (total_tokens < 0 || total_tokens > kMaxTokens || n_q_heads < 1 || n_q_heads > (1 << 20)) return -1;
-    return total_tokens * n_q_heads * static_cast<int64_t>(sizeof(float));
+    return total_tokens * n_q_heads * 2 * static_cast<int64_t>(sizeof(float));
 }
 
 int attn_varlen_bwd(const attn_varlen_desc *desc, const attn_varlen_grads *grads, void *workspace,
@@ -145,12 +145,12 @@ int attn_varlen_bwd(const attn_varlen_desc *desc, const attn_varlen_grads *grads
     if (a.lse == nullptr || workspace == nullptr) return ROPE_ERR_NULL;
     if (!aligned(a.lse, 4) || !aligned(workspace, 16)) return ROPE_ERR_ALIGN;
     if (workspace_bytes < attn_varlen_bwd_workspace_bytes(T, a.hq)) return ROPE_ERR_WORKSPACE;
-    a.delta = static_cast<float *>(workspace);
+    a.stats = static_cast<float *>(workspace);
     a.dout = rows_of(in[4]);
     a.dq = rows_of(res[0]);
     a.dk = rows_of(res[1]);
     a.dv = rows_of(res[2]);
-    return status_of(launch_attn_simple_bwd(a, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_attn_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc)
@@ -208,6 +208,11 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
     return status_of(launch_attn_fwd(a, splits_of(p), static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
-int attn_fault(void) { return pvr::attn_fault_word(); }
+int attn_fault(void)
+{
+    int fwd = 0, bwd = 0;
+    if (attn_fault_word(&fwd) != 0 || attn_bwd_fault_word(&bwd) != 0) return ROPE_ERR_LAUNCH;
+    return fwd != 0 || bwd != 0 ? 1 : 0;
+}
 
 }  // extern "C"

@@ -27,15 +27,13 @@
 #include <cstdint>
 
 #include "attn_internal.h"
-#include "rope_qk.h"
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
 namespace pvr {
+namespace {
 
 __device__ int g_attn_fault;            // a bounded wait ran out
-
-namespace {
 
 constexpr int kThreads = 384;              // two softmax warpgroups, one for products and loads
 constexpr int kRegsSoftmax = 224, kRegsOther = 56;   // 2 * 224 + 56 = 3 * 168, the launch's
@@ -600,11 +598,9 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
                               splits);
 }
 
-int attn_fault_word()
+int attn_fault_word(int *word)
 {
-    int word = 0;
-    if (cudaMemcpyFromSymbol(&word, g_attn_fault, sizeof word) != cudaSuccess) return ROPE_ERR_LAUNCH;
-    return word;
+    return cudaMemcpyFromSymbol(word, g_attn_fault, sizeof *word) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace pvr

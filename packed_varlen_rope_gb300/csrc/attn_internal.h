@@ -26,7 +26,7 @@ struct AttnProblem {
     Rows q, k, v, out;
     Rows dout, dq, dk, dv;          // backward
     float *lse;                     // [hq, tokens] or NULL
-    float *delta;                   // backward workspace, [hq, tokens]
+    float *stats;                   // backward workspace, two floats per [hq, tokens]
     Pages pages;                    // read when paged is set, else k and v
     int32_t paged;
     const int32_t *cu;
@@ -47,7 +47,9 @@ inline int64_t attn_split_floats(int64_t n_tokens, int hq, int d, int splits)
 }
 cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
                              cudaStream_t stream);
-int attn_fault_word();
-cudaError_t launch_attn_simple_bwd(const AttnProblem &p, cudaStream_t stream);
+int attn_fault_word(int *word);       // 0, and the device's fault word
+int attn_bwd_fault_word(int *word);
+// Backward: the rows' statistics, then dk and dv, then dq.
+cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream);
 
 }  // namespace pvr
