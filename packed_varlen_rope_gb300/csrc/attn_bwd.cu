@@ -197,6 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 __syncwarp();
                 tc_fence_after();
             };
+            const uint32_t ubase = uniform(base), utmem = uniform(tmem);
+            const uint32_t d_x = desc_lo(ubase, 0), d_y = desc_lo(ubase + Sh::kOffY, 0),
+                           d_ymn = desc_lo(ubase + Sh::kOffY, kYBox);
             // S and dP of tile t
             auto scores = [&](int t) {
                 const int stage = t % kStages, b = t & 1;
@@ -213,21 +216,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                     fence_async_smem();
                     __syncwarp();
                 }
-                if (ok && lane == 0) {
+                if (ok && elect_one()) {
+                    const uint32_t yd = d_y + stage * (Sh::kStageBytes >> 4);
 #pragma unroll
                     for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t ax = (s / 4) * kXBox + (s % 4) * 32, ay = (s / 4) * kYBox + (s % 4) * 32;
-                        mma_ss(tmem + kColS + b * kY, smem_desc(base + ax, 0, 1024), smem_desc(base + y + ay, 0, 1024),
-                               kDescS, s > 0);
+                        const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
+                        mma_ss(utmem + kColS + b * kY, d_x + ax, yd + ay, kDescS, s > 0);
                     }
 #pragma unroll
                     for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t ax = (s / 4) * kXBox + (s % 4) * 32, ay = (s / 4) * kYBox + (s % 4) * 32;
-                        mma_ss(tmem + kColP + b * kY, smem_desc(base + Sh::kXBytes + ax, 0, 1024),
-                               smem_desc(base + y + Sh::kYBytes + ay, 0, 1024), kDescS, s > 0);
+                        const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
+                        mma_ss(utmem + kColP + b * kY, d_x + (Sh::kXBytes >> 4) + ax, yd + (Sh::kYBytes >> 4) + ay, kDescS,
+                               s > 0);
                     }
                     tc_commit(s_full + 8 * b);
                 }
+                __syncwarp();
             };
             if (n_tiles > 0) {
                 wait(x_full, 0);
@@ -236,22 +240,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             for (int t = 0; ok && t < n_tiles; ++t) {
                 if (t + 1 < n_tiles) scores(t + 1);
                 const int stage = t % kStages, b = t & 1;
-                const uint32_t y = base + Sh::kOffY + stage * Sh::kStageBytes;
+                const uint32_t y = d_ymn + stage * (Sh::kStageBytes >> 4);
                 wait(p_full + 8 * b, t >> 1);
-                if (ok && lane == 0) {
+                if (ok && elect_one()) {
                     if (KEYS) {
 #pragma unroll
                         for (int s = 0; s < kY / 16; ++s)
-                            mma_ts(tmem + kCol2, tmem + kColS + b * kY + s * 8,
-                                   smem_desc(y + Sh::kYBytes + s * 2048, kYBox, 1024), kDescA, t > 0 || s > 0);
+                            mma_ts(utmem + kCol2, utmem + kColS + b * kY + s * 8,
+                                   y + (Sh::kYBytes >> 4) + s * (2048 >> 4), kDescA, t > 0 || s > 0);
                     }
 #pragma unroll
                     for (int s = 0; s < kY / 16; ++s)
-                        mma_ts(tmem + kCol1, tmem + kColP + b * kY + s * 8, smem_desc(y + s * 2048, kYBox, 1024), kDescA,
-                               t > 0 || s > 0);
+                        mma_ts(utmem + kCol1, utmem + kColP + b * kY + s * 8, y + s * (2048 >> 4), kDescA, t > 0 || s > 0);
                     tc_commit(y_empty + 8 * stage);
                     if (t + 1 == n_tiles) tc_commit(done);
                 }
+                __syncwarp();
             }
             if (!ok) {                  // products in flight finish before tensor memory is freed
                 if (lane == 0) tc_commit(drain);

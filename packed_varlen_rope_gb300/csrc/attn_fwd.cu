@@ -35,8 +35,9 @@ namespace {
 
 __device__ int g_attn_fault;            // a bounded wait ran out
 
-constexpr int kThreads = 384;              // two softmax warpgroups, one for products and loads
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;   // 2 * 224 + 56 = 3 * 168, the launch's
+constexpr int kThreads = 640;           // four softmax warpgroups, one for products and loads
+constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 4 * 104 + 64 = 5 * 96, the launch's
 constexpr int kRows = 128;              // rows of a row tile
 constexpr int kKeys = 128;              // keys of a key tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -85,13 +86,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
     __shared__ int s_used;
+    __shared__ float s_swap[2][2][2][kRows];                           // [parity][row tile][half][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 8);
             mbar_init(o_done + 8 * i, 1);
         }
         for (int i = 0; i < kStages; ++i) {
@@ -103,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
-    if (warp == 8) tmem_alloc(smem_addr(&s_tmem), 512);
-    if (warp == 9 && lane == 0) {
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);
+    if (warp == kLoadWarp && lane == 0) {
         tma_prefetch_map(&a.q);
         tma_prefetch_map(&a.k);
         tma_prefetch_map(&a.v);
@@ -171,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
     constexpr uint32_t kColS = 0, kColO = 256;
 
-    if (warp >= 8) {
+    if (warp >= kMmaWarp) {
     regs_shrink<kRegsOther>();
-    if (warp == 9) {
+    if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) {
@@ -227,18 +229,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (count[x] > 0)
                     for (int w = 0; w < kWaitLimit && !mbar_try(q_full + 8 * x, 0); ++w) {}
         }
-    } else if (warp == 8) {
+    } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         constexpr uint32_t kDescS = mma_desc(kRows, kKeys, false);
         constexpr uint32_t kDescO = mma_desc(kRows, DP, true);
+        const uint32_t ubase = uniform(base), utmem = uniform(tmem);
+        const uint32_t d_q = desc_lo(ubase, 0), d_k = desc_lo(ubase + Sh::kOffKV, 0),
+                       d_v = desc_lo(ubase + Sh::kOffKV, kBoxBytes);
         auto scores = [&](int x, int stage) {
-            const uint32_t q = base + x * Sh::kTileBytes, k = base + Sh::kOffKV + stage * Sh::kTileBytes;
+            const uint32_t q = d_q + x * (Sh::kTileBytes >> 4), k = d_k + stage * (Sh::kTileBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < DP / 16; ++s) {
-                const uint32_t at = (s / 4) * kBoxBytes + (s % 4) * 32;
-                mma_ss(tmem + kColS + x * kKeys, smem_desc(q + at, 0, 1024), smem_desc(k + at, 0, 1024), kDescS, s > 0);
+                for (int s = 0; s < DP / 16; ++s) {
+                    const uint32_t at = ((s / 4) * kBoxBytes + (s % 4) * 32) >> 4;
+                    mma_ss(utmem + kColS + x * kKeys, q + at, k + at, kDescS, s > 0);
+                }
+                tc_commit(s_full + 8 * x);
             }
-            tc_commit(s_full + 8 * x);
+            __syncwarp();
         };
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
@@ -251,13 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             for (int x = 0; x < 2; ++x) {
                 if (count[x] == 0) continue;
                 wait(q_full + 8 * x, 0);
-                if (ok && lane == 0) scores(x, 0);
+                if (ok) scores(x, 0);
             }
-            if (ok && lane == 0) tc_commit(kv_empty);
+            if (ok && elect_one()) tc_commit(kv_empty);
+            __syncwarp();
         }
         for (int i = 0; ok && i < n_tiles; ++i) {
             const int tv = 2 * i + 1, sv = tv % kStages, tk = 2 * i + 2, sk = tk % kStages;
-            const uint32_t v = base + Sh::kOffKV + sv * Sh::kTileBytes;
             wait(kv_full + 8 * sv, tv / kStages);
             // value rows past the last key (another sample's, or stale) are cleared: their
             // weights are zero, but zero times NaN is not
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (ok && valid < kKeys) {
                 for (int r = valid + (lane >> 3); r < kKeys; r += 4)
                     for (int b = 0; b < Sh::kBoxes; ++b)
-                        *reinterpret_cast<uint4 *>(smem + (v - base) + b * kBoxBytes + r * 128 + (lane & 7) * 16) =
+                        *reinterpret_cast<uint4 *>(smem + Sh::kOffKV + sv * Sh::kTileBytes + b * kBoxBytes + r * 128 + (lane & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 __syncwarp();
@@ -274,23 +282,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             for (int x = 0; x < 2; ++x) {
                 if (i >= count[x]) continue;
                 wait(p_full + 8 * x, i);
-                if (ok && lane == 0) {
+                if (ok && elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kKeys / 16; ++s)
-                        mma_ts(tmem + kColO + x * DP, tmem + kColS + x * kKeys + s * 8,
-                               smem_desc(v + s * 2048, kBoxBytes, 1024), kDescO, i > 0 || s > 0);
+                        mma_ts(utmem + kColO + x * DP, utmem + kColS + x * kKeys + s * 8,
+                               d_v + sv * (Sh::kTileBytes >> 4) + s * (2048 >> 4), kDescO, i > 0 || s > 0);
                     if (i + 1 == count[x]) tc_commit(o_done + 8 * x);
                 }
+                __syncwarp();
                 if (i + 1 < count[x]) {
                     if (!have_k) wait(kv_full + 8 * sk, tk / kStages);
                     have_k = true;
-                    if (ok && lane == 0) scores(x, sk);
+                    if (ok) scores(x, sk);
                 }
             }
-            if (ok && lane == 0) {
+            if (ok && elect_one()) {
                 tc_commit(kv_empty + 8 * sv);
                 if (i + 1 < n_tiles) tc_commit(kv_empty + 8 * sk);
             }
+            __syncwarp();
         }
         if (!ok) {                      // products in flight finish before tensor memory is freed
             if (lane == 0) tc_commit(drain);
@@ -300,11 +310,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
     } else {
         // ---------------------------------------------------------- softmax
+        // a row is two threads', 64 of a tile's keys each
         regs_grow<kRegsSoftmax>();
-        const int x = warp >> 2;
-        const int row = threadIdx.x & 127;
+        const int x = warp >> 3, half = (warp >> 2) & 1;
+        const int row = (warp & 3) * 32 + lane;
+        const int pair = 1 + x * 4 + (warp & 3);                       // the two warps' barrier
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + kColS + x * kKeys, t_o = tmem + lanes + kColO + x * DP;
+        const uint32_t t_s = tmem + lanes + kColS + x * kKeys + half * 64;
+        const uint32_t t_p = tmem + lanes + kColS + x * kKeys + half * 32;
+        const uint32_t t_o = tmem + lanes + kColO + x * DP + half * (DP / 2);
         const int tok0 = first + x * a.tile_tokens;                    // of the sample
         const int i_tok = tok0 + row / a.group;
         const bool mine = live && row < a.group * a.tile_tokens && i_tok < len;
@@ -313,31 +327,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const float c = a.scale * kLog2e;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
+        // after a wait that ran out the loop goes on without waiting, so that the pair's
+        // barriers stay matched
         for (int i = 0; i < count[x]; ++i) {
-            ok = mbar_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            if (ok) ok = mbar_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
+            ok = __all_sync(0xffffffffu, ok);
             __syncwarp();
             tc_fence_after();
-            uint32_t s[128];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, reinterpret_cast<uint32_t(&)[32]>(s[32 * j]));
+            uint32_t s[64];
+            tmem_ld32(t_s, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+            tmem_ld32(t_s + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
             tc_wait_ld(reinterpret_cast<uint32_t(&)[32]>(s[0]));
-#pragma unroll
-            for (int j = 1; j < 4; ++j) tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32 * j]));
+            tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32]));
             const int key0 = (lo_tile + i) * kKeys;
             if (key0 + kKeys > lim_all) {
-                const int left = lim - key0;
+                const int left = lim - key0 - 64 * half;
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
+                for (int j = 0; j < 64; ++j)
                     if (j >= left) s[j] = 0xff800000u;
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[j]));
-            const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            for (int j = 0; j < 64; j += 2)
+                top[(j >> 1) & 3] = max3(top[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+            // past the barrier both warps have read their scores, and P may overwrite them
+            s_swap[i & 1][x][half][row] = high;
+            tc_fence_before();
+            named_barrier(pair, 64);
+            tc_fence_after();
+            high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
             if (i == 0) {
                 m = high;
             } else if (__any_sync(0xffffffffu, (high - m) * c > kGrow)) {
@@ -347,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 m = grown;
                 l *= shrink;
 #pragma unroll
-                for (int j = 0; j < DP / 16; ++j) {
+                for (int j = 0; j < DP / 32; ++j) {
                     uint32_t o[16];
                     tmem_ld16(t_o + 16 * j, o);
                     tc_wait_ld16(o);
@@ -362,31 +381,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (__any_sync(0xffffffffu, fabsf(mc) > kFoldLimit)) {
                 const float shift = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                for (int j = 0; j < 128; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
+                for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
                 mc = 0.0f;
             }
             const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
+            for (int j = 0; j < 32; ++j) {
                 float2 p = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, mc2);
                 p.x = ex2(p.x);
                 p.y = ex2(p.y);
                 sum[j & 1] = add2(sum[j & 1], p);
                 s[j] = pack_bf16(p.x, p.y);
             }
-            tmem_st32(t_s, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            tmem_st32(t_s + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+            tmem_st32(t_p, reinterpret_cast<uint32_t(&)[32]>(s[0]));
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * x);
         }
-        if (ok && count[x] > 0) {
-            ok = mbar_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
+        if (count[x] > 0) {
+            if (ok) ok = mbar_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
             ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();
             tc_fence_after();
+            s_swap[count[x] & 1][x][half][row] = l;
+            named_barrier(pair, 64);
+            l += s_swap[count[x] & 1][x][half ^ 1][row];
         }
         // epilogue: rows outside the pack, and rows that see no key, are zero (tiles that all
         // rows in use see whole are not masked, so such rows may have summed anything)
@@ -396,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const bool joined = PAGED && a.splits > 1;
         const int64_t at = static_cast<int64_t>(tok) * a.hq + head;
-        if (ok && mine) {
+        if (ok && mine && half == 0) {
             if (joined) {
                 a.part_lse[static_cast<int64_t>(split) * a.n_tokens * a.hq + at] =
                     l > 0.0f ? m * c + log2f(l) : -INFINITY;
@@ -405,10 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
         }
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j) {
+        for (int j = 0; j < DP / 64; ++j) {
+            const int col = half * (DP / 2) + 32 * j;
             uint32_t o[32];
             __syncwarp();
-            if (ok && count[x] > 0) {
+            if (count[x] > 0) {
                 tmem_ld32(t_o + 32 * j, o);
                 tc_wait_ld(o);
             }
@@ -419,17 +442,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             if (joined) {
                 float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(split) * a.n_tokens * a.hq + at) *
-                                                                        a.d + 32 * j);
+                                                                        a.d + col);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (32 * j + 4 * e < a.d && l > 0.0f)
+                    if (col + 4 * e < a.d && l > 0.0f)
                         dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
             } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(a.out + tok * a.out_ts + head * a.out_hs + 32 * j);
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + tok * a.out_ts + head * a.out_hs + col);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (32 * j + 8 * e >= a.d) continue;
+                    if (col + 8 * e >= a.d) continue;
                     uint32_t w[4];
 #pragma unroll
                     for (int f = 0; f < 4; ++f)
@@ -441,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }

@@ -14,11 +14,10 @@
 
 namespace pvr {
 
-// Waits are bounded: after kWaitLimit tries of about a microsecond the waiter raises the
+// Waits are bounded: after kWaitLimit tries (each of them suspends for a while) the waiter raises the
 // CTA's abort flag and the device's fault word, every other wait of the CTA then ends too,
 // and the kernel drains its copies, frees its tensor memory and returns.
-constexpr int kWaitLimit = 1 << 20;
-constexpr uint32_t kWaitHintNs = 1000;
+constexpr int kWaitLimit = 1 << 22;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
 {
@@ -44,10 +43,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
     asm volatile("{\n .reg .pred p;\n"
-                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
                  " selp.b32 %0, 1, 0, p;\n}"
                  : "=r"(done)
-                 : "r"(bar), "r"(parity), "r"(kWaitHintNs)
+                 : "r"(bar), "r"(parity)
                  : "memory");
     return done != 0;
 }
@@ -110,16 +109,29 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
+
+// The value of lane 0, which the compiler then knows to be the same in every lane: what the
+// tensor core's instructions take must live in uniform registers, and a value that is not
+// known to be uniform costs about 100 cycles an instruction to get there.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Matrix descriptor of a 128-byte-swizzled bf16 tile at a shared-memory address: strides in
 // bytes.  K-major operands (the product's sum runs along the row): `stride` 1024 from one
 // group of 8 rows to the next, `lead` unused.  MN-major operands (the sum runs down the
 // rows): `stride` 1024 from 8 rows to the next 8, `lead` from one box of 64 columns to the
-// next.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+// next.  The low word holds the address: a step of n bytes adds n >> 4.
+__device__ __forceinline__ constexpr uint32_t desc_lo(uint32_t addr, uint32_t lead)
 {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-           (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+    return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor: bf16 x bf16 -> binary32, M x N, B K-major or MN-major.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major)
@@ -128,20 +140,21 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major)
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] B[smem], one k step of 16.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// D[tmem] (+)= A[smem] B[smem], one k step of 16; operands by their descriptors' low words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %4, 0;\n"
+                 " mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(kDescHi) : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem].
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.u32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(kDescHi) : "memory");
 }
 
 #define PVR_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
@@ -214,6 +227,19 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Meets the other warps that name this barrier (ids 1..15), `threads` in all.
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
