@@ -192,10 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             constexpr uint32_t kDescA = mma_desc(kX, DP, true);
             bool ok = true;
             auto wait = [&](uint32_t bar, int phase) {
-                if (ok && !mbar_wait(bar, phase & 1, &s_abort, &g_attn_bwd_fault)) ok = false;
-                ok = __all_sync(0xffffffffu, ok);
-                __syncwarp();
-                tc_fence_after();
+                if (ok) ok = warp_wait(bar, phase & 1, &s_abort, &g_attn_bwd_fault);
             };
             const uint32_t ubase = uniform(base), utmem = uniform(tmem);
             const uint32_t d_x = desc_lo(ubase, 0), d_y = desc_lo(ubase + Sh::kOffY, 0),
@@ -242,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 const int stage = t % kStages, b = t & 1;
                 const uint32_t y = d_ymn + stage * (Sh::kStageBytes >> 4);
                 wait(p_full + 8 * b, t >> 1);
+                tc_fence_after();
                 if (ok && elect_one()) {
                     if (KEYS) {
 #pragma unroll
@@ -274,10 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                     const int r = y * kY + lane + 32 * i;
                     v[i] = r < rows ? __ldg(src + r) : make_float2(-INFINITY, 0.0f);
                 }
-                bool ok = true;
-                if (t >= kStages)
-                    ok = mbar_wait(y_empty + 8 * stage, (t / kStages - 1) & 1, &s_abort, &g_attn_bwd_fault);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (t >= kStages && !warp_wait(y_empty + 8 * stage, (t / kStages - 1) & 1, &s_abort, &g_attn_bwd_fault))
+                    break;
                 float *dst = reinterpret_cast<float *>(smem + Sh::kOffY + stage * Sh::kStageBytes + 2 * Sh::kYBytes);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -309,13 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         for (int t = w; t < n_tiles; t += 2) {
             const int y0 = (y_lo + t % per_pass) * kY;
             const int stage = t % kStages;
-            ok = mbar_wait(s_full + 8 * w, (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
-            if (KEYS && ok) ok = mbar_wait(y_full + 8 * stage, (t / kStages) & 1, &s_abort, &g_attn_bwd_fault);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            __syncwarp();
+            ok = warp_wait(s_full + 8 * w, (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
+            if (KEYS && ok) ok = warp_wait(y_full + 8 * stage, (t / kStages) & 1, &s_abort, &g_attn_bwd_fault);
+            if (!ok) break;
             tc_fence_after();
             const float *st = reinterpret_cast<const float *>(smem + Sh::kOffY + stage * Sh::kStageBytes + 2 * Sh::kYBytes);
             // columns [from, to) are visible: keys of a query row, or queries of a key row
@@ -371,9 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(p_full + 8 * w);
         }
         if (ok && n_tiles > 0) {
-            ok = mbar_wait(done, 0, &s_abort, &g_attn_bwd_fault);
-            ok = __all_sync(0xffffffffu, ok);
-            __syncwarp();
+            ok = warp_wait(done, 0, &s_abort, &g_attn_bwd_fault);
             tc_fence_after();
         }
         // epilogue: dk by one group and dv by the other, or half of dq's columns each

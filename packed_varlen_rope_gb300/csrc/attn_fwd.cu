@@ -3,8 +3,10 @@
 // Mathematics.  For each row the running maximum m and sum l of a softmax over key tiles:
 //   s = scale q.k;  m' = max(m, max s);  p = exp(s - m');  l' = l exp(m - m') + sum p;
 //   o' = o exp(m - m') + p V.  Exponentials are base 2 with scale*log2(e) folded in.
-// The rescaling of o and l is put off until the maximum has grown by more than 2^8, so p
-// stays below 256 and most tiles need none; the result is the same.
+// m is the maximum of the first tile and stays until a later one exceeds it by more than
+// 2^30: floating-point weights keep their precision whatever the scale, and sums of 2^24
+// weights below 2^30 stay far inside binary32.  So a tile's weights are computed without
+// waiting for its maximum, and o is hardly ever rescaled.
 //
 // Layout.  A CTA owns 256 rows of one key head: two tiles of 128 rows, a row being one
 // (token, query head) pair with the G heads that share the key head side by side, so every
@@ -25,6 +27,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "tensor_core.cuh"
@@ -37,13 +40,12 @@ __device__ int g_attn_fault;            // a bounded wait ran out
 
 constexpr int kThreads = 640;           // four softmax warpgroups, one for products and loads
 constexpr int kMmaWarp = 16, kLoadWarp = 17;
-constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 4 * 104 + 64 = 5 * 96, the launch's
 constexpr int kRows = 128;              // rows of a row tile
 constexpr int kKeys = 128;              // keys of a key tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrow = 8.0f;           // log2 growth of the maximum that triggers a rescale
-constexpr float kFoldLimit = 4096.0f;   // |m| (log2) up to which m is folded into the FMA
+constexpr float kGrow = 30.0f;          // log2 growth of the maximum that triggers a rescale
+constexpr float kFoldLimit = 4096.0f;   // |m| (log2) up to which it is folded into an FMA: its rounding is 2^-13 at most
 
 struct FwdArgs {
     CUtensorMap q, k, v;
@@ -174,7 +176,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     constexpr uint32_t kColS = 0, kColO = 256;
 
     if (warp >= kMmaWarp) {
-    regs_shrink<kRegsOther>();
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
@@ -207,11 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool ok = true;
             for (int kv = 0; kv < 2; ++kv) {
                 const int t = 2 * i + kv, stage = t % kStages;
-                if (t >= kStages) ok = mbar_wait(kv_empty + 8 * stage, (t / kStages - 1) & 1, &s_abort, &g_attn_fault);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                if (t >= kStages) ok = warp_wait(kv_empty + 8 * stage, (t / kStages - 1) & 1, &s_abort, &g_attn_fault);
+                if (!ok) break;
                 const uint32_t bar = kv_full + 8 * stage;
                 const uint32_t dst = base + Sh::kOffKV + stage * Sh::kTileBytes + col * kBoxBytes +
                                      static_cast<uint32_t>(box * a.box_rows) * 128;
@@ -250,9 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         };
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
-            if (ok && !mbar_wait(bar, phase & 1, &s_abort, &g_attn_fault)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
+            if (ok) ok = warp_wait(bar, phase & 1, &s_abort, &g_attn_fault);
         };
         if (n_tiles > 0) {
             wait(kv_full, 0);
@@ -278,10 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 fence_async_smem();
                 __syncwarp();
             }
-            bool have_k = false;
+            if (i + 1 < n_tiles) wait(kv_full + 8 * sk, tk / kStages);
             for (int x = 0; x < 2; ++x) {
                 if (i >= count[x]) continue;
                 wait(p_full + 8 * x, i);
+                tc_fence_after();
                 if (ok && elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kKeys / 16; ++s)
@@ -290,11 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     if (i + 1 == count[x]) tc_commit(o_done + 8 * x);
                 }
                 __syncwarp();
-                if (i + 1 < count[x]) {
-                    if (!have_k) wait(kv_full + 8 * sk, tk / kStages);
-                    have_k = true;
-                    if (ok) scores(x, sk);
-                }
+                if (ok && i + 1 < count[x]) scores(x, sk);
             }
             if (ok && elect_one()) {
                 tc_commit(kv_empty + 8 * sv);
@@ -311,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     } else {
         // ---------------------------------------------------------- softmax
         // a row is two threads', 64 of a tile's keys each
-        regs_grow<kRegsSoftmax>();
         const int x = warp >> 3, half = (warp >> 2) & 1;
         const int row = (warp & 3) * 32 + lane;
         const int pair = 1 + x * 4 + (warp & 3);                       // the two warps' barrier
@@ -323,88 +315,110 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int i_tok = tok0 + row / a.group;
         const bool mine = live && row < a.group * a.tile_tokens && i_tok < len;
         const int lim = mine ? limit(i_tok) : 0;
-        const int lim_all = limit(tok0);                               // the fewest keys a row of the tile sees
+        // from the CTA's first key on: keys that every row of the tile sees, and that this
+        // thread's columns of the row see
+        const int whole = limit(tok0) - lo_tile * kKeys, visible = lim - lo_tile * kKeys - 64 * half;
         const float c = a.scale * kLog2e;
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, mc = 0.0f;
         bool ok = true;
+        bool folded = false;                                           // m is known, and small
+        // 32 of this thread's scores of tile i, those it does not see at -infinity
+        auto load = [&](int i, int h, uint32_t(&s)[32]) {
+            tmem_ld32(t_s + 32 * h, s);
+            tc_wait_ld(s);
+            if ((i + 1) * kKeys > whole) {
+                const int left = visible - i * kKeys - 32 * h;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j >= left) s[j] = 0xff800000u;
+            }
+        };
+        auto highest = [&](const uint32_t(&s)[32]) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+                top[(j >> 1) & 3] = max3(top[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            return max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+        };
+        // p = 2^(s c - fixed), packed, and their sum
+        auto weights = [&](const uint32_t(&s)[32], uint32_t *p, float fixed) {
+            const float2 c2 = make_float2(c, c), fixed2 = make_float2(-fixed, -fixed);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float2 x = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, fixed2);
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[j & 1] = add2(sum[j & 1], x);
+                p[j] = pack_bf16(x.x, x.y);
+            }
+            return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        };
         // after a wait that ran out the loop goes on without waiting, so that the pair's
         // barriers stay matched
         for (int i = 0; i < count[x]; ++i) {
-            if (ok) ok = mbar_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
-            ok = __all_sync(0xffffffffu, ok);
-            __syncwarp();
+            if (ok) ok = warp_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
             tc_fence_after();
-            uint32_t s[64];
-            tmem_ld32(t_s, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            tmem_ld32(t_s + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-            tc_wait_ld(reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32]));
-            const int key0 = (lo_tile + i) * kKeys;
-            if (key0 + kKeys > lim_all) {
-                const int left = lim - key0 - 64 * half;
+            // with the maximum so far: s c is exact inside the FMA, and m c small enough for its
+            // rounding not to matter
+            uint32_t p[32];
+            float high = -INFINITY, sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (j >= left) s[j] = 0xff800000u;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t s[32];
+                load(i, h, s);
+                high = fmaxf(high, highest(s));
+                if (folded) sum += weights(s, p + 16 * h, mc);
             }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 64; j += 2)
-                top[(j >> 1) & 3] = max3(top[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
-            // past the barrier both warps have read their scores, and P may overwrite them
             s_swap[i & 1][x][half][row] = high;
+            // past the barrier both warps have read their scores, and P may overwrite them
             tc_fence_before();
             named_barrier(pair, 64);
             tc_fence_after();
             high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
-            if (i == 0) {
-                m = high;
-            } else if (__any_sync(0xffffffffu, (high - m) * c > kGrow)) {
+            if (__any_sync(0xffffffffu, !folded || (high - m) * c > kGrow)) {
+                // a new maximum; both warps of the pair come here, as they hold the same rows.
                 // S of this tile is complete, and with it every earlier product into O
                 const float grown = fmaxf(m, high);
-                const float shrink = m == grown ? 1.0f : ex2((m - grown) * c);
-                m = grown;
-                l *= shrink;
+                if (i > 0) {
+                    const float shrink = m == grown ? 1.0f : ex2((m - grown) * c);
+                    l *= shrink;
+#pragma unroll 1
+                    for (int j = 0; j < DP / 32; ++j) {
+                        uint32_t o[16];
+                        tmem_ld16(t_o + 16 * j, o);
+                        tc_wait_ld16(o);
 #pragma unroll
-                for (int j = 0; j < DP / 32; ++j) {
-                    uint32_t o[16];
-                    tmem_ld16(t_o + 16 * j, o);
-                    tc_wait_ld16(o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-                    tmem_st16(t_o + 16 * j, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                        tmem_st16(t_o + 16 * j, o);
+                    }
                 }
-            }
-            // p = 2^(s c - m c): the product s c is exact inside the FMA, and the rounding of
-            // m c is common to the row, so it cancels against l -- unless it is large
-            float mc = m == -INFINITY ? 0.0f : m * c;
-            if (__any_sync(0xffffffffu, fabsf(mc) > kFoldLimit)) {
+                m = grown;
                 const float shift = m == -INFINITY ? 0.0f : m;
+                mc = shift * c;
+                folded = __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
+                sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
-                mc = 0.0f;
-            }
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t s[32];
+                    load(i, h, s);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                float2 p = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, mc2);
-                p.x = ex2(p.x);
-                p.y = ex2(p.y);
-                sum[j & 1] = add2(sum[j & 1], p);
-                s[j] = pack_bf16(p.x, p.y);
+                    for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
+                    sum += weights(s, p + 16 * h, 0.0f);
+                }
+                tc_fence_before();
+                named_barrier(pair, 64);
+                tc_fence_after();
             }
-            tmem_st32(t_p, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st32(t_p, p);
+            l += sum;
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * x);
         }
         if (count[x] > 0) {
-            if (ok) ok = mbar_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
-            ok = __all_sync(0xffffffffu, ok);
-            __syncwarp();
+            if (ok) ok = warp_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
             tc_fence_after();
             s_swap[count[x] & 1][x][half][row] = l;
             named_barrier(pair, 64);

@@ -51,10 +51,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
-// Waits for the phase of the given parity; false when the CTA gave up.
+// One thread waits for the phase of the given parity; false when the CTA gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
 {
-    if (mbar_try(bar, parity)) return true;
     for (int i = 0; i < kWaitLimit; ++i) {
         if (mbar_try(bar, parity)) return true;
         if (*abort_flag != 0) return false;
@@ -62,6 +61,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     *abort_flag = 1;
     atomicExch(fault, 1);
     return false;
+}
+
+// A converged warp waits; the result is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
+{
+    const bool ok = mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, fault);
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
