@@ -3,11 +3,10 @@
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 from typing import Optional
 
-from ._binding import (RopeCosSinCacheDesc, _cache_arg, _check, _check_cu, _on, _ptr, _stream, _view_args,
-                       load_library)
+from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, load_library
 
 ATTN_EXPORTS = ("attn_varlen_fwd", "attn_varlen_bwd", "attn_varlen_bwd_workspace_bytes", "attn_paged",
                 "attn_paged_workspace_bytes", "attn_fault")
@@ -62,16 +61,68 @@ class AttnPagedDesc(ctypes.Structure):
                 ("causal", _i32), ("scale", ctypes.c_float), ("reserved", _i32)]
 
 
+# A decoding step is a few microseconds on the GPU, so the calls below pack a descriptor in one
+# go (the structures above, as ``struct`` formats) and read each tensor's fields once.
+_VIEW = "Pqq"
+_PAGED = "88s"
+_APPEND_PACK = struct.Struct("@" + 4 * _VIEW + _PAGED + "PPPqiiiiqddP").pack
+_VARLEN_PACK = struct.Struct("@" + 4 * _VIEW + "PPPqiiiiif").pack
+_GRADS_PACK = struct.Struct("@" + 4 * _VIEW).pack
+_PAGED_PACK = struct.Struct("@" + 2 * _VIEW + _PAGED + "PPPqqqiiiifi").pack
+
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
+def _view(t, name: str):
+    """(pointer, token stride, head stride) of a bf16 CUDA [tokens, heads, head_dim] view."""
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or t.dtype is not _torch.bfloat16 or not t.is_cuda:
+        raise ValueError("%s must be a CUDA bf16 [tokens, heads, head_dim] view with head_dim contiguous" % name)
+    return t.data_ptr(), st[0], st[1]
+
+
+def _int32(t, dev: int, n: int, what: str) -> int:
+    """Pointer of a contiguous int32 [n] tensor on CUDA device ``dev``."""
+    if t.dtype is not _torch.int32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d values on the device of q" % (what, n))
+    return t.data_ptr()
+
+
+def _launch(fn, name: str, dev: int, stream, *args) -> None:
+    """Call an entry point with device ``dev`` current, on ``stream`` (a torch stream or an int)
+    or torch's current one of that device."""
+    c = _torch._C
+    if stream is None:
+        stream = c._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if c._cuda_getDevice() == dev:
+        st = fn(*args, stream)
+    else:
+        with _torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        _check(name, st)
+
+
 def _declare(lib):
-    """Signatures of the entry points (called by ``load_library``)."""
-    p = ctypes.POINTER
-    lib.rope_kv_append.argtypes = [p(RopeKVAppendDesc), _vp]
-    lib.attn_varlen_fwd.argtypes = [p(AttnVarlenDesc), _vp]
-    lib.attn_varlen_bwd.argtypes = [p(AttnVarlenDesc), p(AttnVarlenGrads), _vp, _i64, _vp]
+    """Signatures of the entry points (called by ``load_library``).  Descriptors go as ``byref``
+    of the structures above, or packed as bytes."""
+    lib.rope_kv_append.argtypes = [_vp, _vp]
+    lib.attn_varlen_fwd.argtypes = [_vp, _vp]
+    lib.attn_varlen_bwd.argtypes = [_vp, _vp, _vp, _i64, _vp]
     lib.attn_varlen_bwd_workspace_bytes.argtypes = [_i64, _i32]
     lib.attn_varlen_bwd_workspace_bytes.restype = _i64
-    lib.attn_paged.argtypes = [p(AttnPagedDesc), _vp, _i64, _vp]
-    lib.attn_paged_workspace_bytes.argtypes = [p(AttnPagedDesc)]
+    lib.attn_paged.argtypes = [_vp, _vp, _i64, _vp]
+    lib.attn_paged_workspace_bytes.argtypes = [_vp]
     lib.attn_paged_workspace_bytes.restype = _i64
     lib.attn_fault.argtypes = []
     for name in ("rope_kv_append", "attn_varlen_fwd", "attn_varlen_bwd", "attn_paged", "attn_fault"):
@@ -84,19 +135,21 @@ class PagedKVCache:
     two may be the halves of one pool).  page_size is a multiple of 8."""
 
     def __init__(self, k_pages, v_pages):
-        import torch
-
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4 or (t.numel() and t.stride(3) != 1):
+        torch = _torch or _load_torch()
+        ks, vs = k_pages.stride(), v_pages.stride()
+        for name, t, st in (("k_pages", k_pages, ks), ("v_pages", v_pages, vs)):
+            if t.dtype is not torch.bfloat16 or not t.is_cuda or len(st) != 4 or (st[3] != 1 and t.numel()):
                 raise ValueError("%s must be a CUDA bf16 [pages, page_size, kv_heads, head_dim] view with head_dim "
                                  "contiguous" % name)
-        if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
+        shape = k_pages.shape
+        if shape != v_pages.shape or k_pages.device != v_pages.device:
             raise ValueError("k_pages and v_pages must share shape and device")
         self.k_pages, self.v_pages = k_pages, v_pages
-        n, page, heads, d = k_pages.shape
-        ks, vs = k_pages.stride(), v_pages.stride()
+        n, page, heads, d = shape
         self.desc = RopePagedKV(k_pages.data_ptr(), ks[0], ks[1], ks[2], v_pages.data_ptr(), vs[0], vs[1], vs[2],
                                 n, page, heads, d, 0)
+        self._packed = bytes(self.desc)
+        self._dev, self._heads, self._dim = k_pages.get_device(), heads, d
 
     @property
     def device(self):
@@ -128,26 +181,23 @@ def new_paged_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: 
                         torch.empty(shape, dtype=torch.bfloat16, device=device))
 
 
-def _tables(desc, cache, device, page_table, kv_lens, cu_seqlens):
-    import torch
-
-    if not isinstance(cache, PagedKVCache):
+def _tables(cache, dev: int, page_table, kv_lens, cu_seqlens):
+    """The pointers and sizes (cu_seqlens, kv_lens, page_table, row stride, max_pages, n_seqs)."""
+    if type(cache) is not PagedKVCache and not isinstance(cache, PagedKVCache):
         raise ValueError("cache must be a PagedKVCache")
-    if cache.device != device:
-        raise ValueError("the cache is on %s, q on %s" % (cache.device, device))
-    _check_cu(cu_seqlens, device)
+    if cache._dev != dev:
+        raise ValueError("the cache is on %s, q on cuda:%d" % (cache.device, dev))
     n = cu_seqlens.numel() - 1
     if n < 0:
         raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
-    if kv_lens.dtype != torch.int32 or kv_lens.device != device or not kv_lens.is_contiguous() or kv_lens.numel() != n:
-        raise ValueError("kv_lens must be a contiguous int32 tensor of one length per sequence on the device of q")
-    if page_table.dtype != torch.int32 or page_table.device != device or page_table.dim() != 2 or \
-            page_table.shape[0] != n or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    cu = _int32(cu_seqlens, dev, n + 1, "cu_seqlens")
+    kv = _int32(kv_lens, dev, n, "kv_lens")
+    st, shape = page_table.stride(), page_table.shape
+    if page_table.dtype is not _torch.int32 or page_table.get_device() != dev or len(st) != 2 or shape[0] != n or \
+            (st[1] != 1 and shape[1] > 1):
         raise ValueError("page_table must be an int32 [n_seqs, max_pages] tensor with contiguous rows on the "
                          "device of q")
-    desc.cache = cache.desc
-    desc.cu_seqlens, desc.kv_lens, desc.page_table = _ptr(cu_seqlens), _ptr(kv_lens), _ptr(page_table)
-    desc.page_table_stride, desc.max_pages, desc.n_seqs = page_table.stride(0), page_table.shape[1], n
+    return cu, kv, page_table.data_ptr(), st[0], shape[1], n
 
 
 def _keep_for(stream, *tensors):
@@ -163,10 +213,6 @@ def _keep_for(stream, *tensors):
             t.record_stream(s)
 
 
-def _scale(scale, d: int) -> float:
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
-
-
 def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, theta: float, q_out=None,
                    position_scale: float = 1.0, cos_sin_cache=None, stream=None):
     """Rotate the new tokens' q [T, Hq, d] (in place, or into ``q_out``) and k [T, Hkv, d] by
@@ -175,28 +221,27 @@ def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens
     sequence, ``kv_lens`` (int32 [n]) counts its tokens in the cache with the new ones,
     ``page_table`` (int32 [n, max_pages]) names its pages; all on the device.  k and v are
     only read.  Returns the rotated q."""
-    desc = RopeKVAppendDesc()
-    desc.q, desc.q_stride_token, desc.q_stride_head = _view_args(q, "q")
-    desc.k, desc.k_stride_token, desc.k_stride_head = _view_args(k, "k")
-    desc.v, desc.v_stride_token, desc.v_stride_head = _view_args(v, "v")
+    _torch or _load_torch()
+    qv, kv, vv = _view(q, "q"), _view(k, "k"), _view(v, "v")
+    dev = q.get_device()
     T, hq, d = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != d or k.device != q.device or v.device != q.device:
+    shape = k.shape
+    if shape != v.shape or shape[0] != T or shape[2] != d or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k and v must share tokens, head_dim and device, k and v their heads")
-    _tables(desc, cache, q.device, page_table, kv_lens, cu_seqlens)
-    if k.shape[1] != cache.n_kv_heads or d != cache.head_dim:
-        raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (cache.n_kv_heads, cache.head_dim,
-                                                                            k.shape[1], d))
+    cu, lens, table, stride, width, n = _tables(cache, dev, page_table, kv_lens, cu_seqlens)
+    if shape[1] != cache._heads or d != cache._dim:
+        raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (cache._heads, cache._dim, shape[1], d))
+    ov = (0, 0, 0)
     if q_out is not None:
-        if q_out.shape != q.shape or q_out.device != q.device:
+        if q_out.shape != q.shape or q_out.get_device() != dev:
             raise ValueError("q_out must have the shape and device of q")
-        desc.q_out, desc.q_out_stride_token, desc.q_out_stride_head = _view_args(q_out, "q_out")
-    desc.n_q_heads, desc.total_tokens = hq, T
-    desc.theta, desc.position_scale = float(theta), float(position_scale)
-    ref = _cache_arg(cos_sin_cache, d, q.device)
-    if ref is not None:
-        desc.cos_sin_cache = ref
-    st = _on(q.device, load_library().rope_kv_append, ctypes.byref(desc), _stream(stream, q.device))
-    _check("rope_kv_append", st)
+        ov = _view(q_out, "q_out")
+    ref = None
+    if cos_sin_cache is not None:
+        ref = _cache_arg(cos_sin_cache, d, q.device)
+    desc = _APPEND_PACK(*qv, *kv, *vv, *ov, cache._packed, cu, lens, table, stride, width, n, hq, 0, T, float(theta),
+                        float(position_scale), 0 if ref is None else ctypes.addressof(ref.contents))
+    _launch(load_library().rope_kv_append, "rope_kv_append", dev, stream, desc)
     return q if q_out is None else q_out
 
 
@@ -209,81 +254,75 @@ def attn_paged(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, causal: 
     caches; 0: what the page table's width allows).  ``workspace``: a CUDA tensor for
     partial results (``attn_paged_workspace_bytes``); allocated through torch unless given.
     Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
-    import torch
-
-    desc = _paged_desc(q, cache, page_table, kv_lens, cu_seqlens, causal, scale, max_kv_len)
+    torch = _torch or _load_torch()
     made = out is None
     if made:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    elif out.shape != q.shape or out.device != q.device:
+    elif out.shape != q.shape or out.get_device() != q.get_device():
         raise ValueError("out must have the shape and device of q")
-    desc.out, desc.out_stride_token, desc.out_stride_head = _view_args(out, "out")
+    desc, dev = _paged_desc(q, out, cache, page_table, kv_lens, cu_seqlens, causal, scale, max_kv_len)
     lib = load_library()
     own = None
     if workspace is None:
-        need = int(lib.attn_paged_workspace_bytes(ctypes.byref(desc)))
-        if need > 0:
-            workspace = own = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _on(q.device, lib.attn_paged, ctypes.byref(desc), _ptr(workspace), nbytes, _stream(stream, q.device))
-    _check("attn_paged", st)
-    _keep_for(stream, own, out if made else None)
+        nbytes = lib.attn_paged_workspace_bytes(desc)
+        if nbytes > 0:
+            own = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = None if own is None else own.data_ptr()
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(lib.attn_paged, "attn_paged", dev, stream, desc, ws, nbytes)
+    if stream is not None:
+        _keep_for(stream, own, out if made else None)
     return out
 
 
-def _paged_desc(q, cache, page_table, kv_lens, cu_seqlens, causal, scale, max_kv_len):
-    desc = AttnPagedDesc()
-    desc.q, desc.q_stride_token, desc.q_stride_head = _view_args(q, "q")
-    _tables(desc, cache, q.device, page_table, kv_lens, cu_seqlens)
-    if q.shape[2] != cache.head_dim:
-        raise ValueError("the cache holds heads of %d, q has %d" % (cache.head_dim, q.shape[2]))
-    desc.total_tokens, desc.n_q_heads = q.shape[0], q.shape[1]
-    desc.max_kv_len, desc.causal = int(max_kv_len), 1 if causal else 0
-    desc.scale = _scale(scale, q.shape[2])
-    return desc
+def _paged_desc(q, out, cache, page_table, kv_lens, cu_seqlens, causal, scale, max_kv_len):
+    qv = _view(q, "q")
+    ov = (0, 0, 0) if out is None else _view(out, "out")
+    dev = q.get_device()
+    T, hq, d = q.shape
+    cu, lens, table, stride, width, n = _tables(cache, dev, page_table, kv_lens, cu_seqlens)
+    if d != cache._dim:
+        raise ValueError("the cache holds heads of %d, q has %d" % (cache._dim, d))
+    return _PAGED_PACK(*qv, *ov, cache._packed, cu, lens, table, stride, T, int(max_kv_len), width, n, hq,
+                       1 if causal else 0, d ** -0.5 if scale is None else scale, 0), dev
 
 
 def attn_paged_workspace_bytes(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, max_kv_len: int = 0) -> int:
     """Bytes of workspace ``attn_paged`` needs for these arguments (0: none)."""
-    desc = _paged_desc(q, cache, page_table, kv_lens, cu_seqlens, True, None, max_kv_len)
-    need = int(load_library().attn_paged_workspace_bytes(ctypes.byref(desc)))
+    _torch or _load_torch()
+    desc, _ = _paged_desc(q, None, cache, page_table, kv_lens, cu_seqlens, True, None, max_kv_len)
+    need = int(load_library().attn_paged_workspace_bytes(desc))
     if need < 0:
         _check("attn_paged_workspace_bytes", need)
     return need
 
 
 def _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used):
-    import torch
-
-    desc = AttnVarlenDesc()
-    desc.q, desc.q_stride_token, desc.q_stride_head = _view_args(q, "q")
-    desc.k, desc.k_stride_token, desc.k_stride_head = _view_args(k, "k")
-    desc.v, desc.v_stride_token, desc.v_stride_head = _view_args(v, "v")
-    desc.out, desc.out_stride_token, desc.out_stride_head = _view_args(out, "out")
+    """The packed descriptor, and the device."""
+    qv, kv, vv, ov = _view(q, "q"), _view(k, "k"), _view(v, "v"), _view(out, "out")
     T, hq, d = q.shape
-    dev = q.device
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != d or k.device != dev or v.device != dev:
+    dev = q.get_device()
+    shape = k.shape
+    if shape != v.shape or shape[0] != T or shape[2] != d or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k and v must share tokens, head_dim and device, k and v their heads")
-    if out.shape != q.shape or out.device != dev:
+    if out.shape != q.shape or out.get_device() != dev:
         raise ValueError("out must have the shape and device of q")
+    lp = 0
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (hq, T) or not lse.is_contiguous():
+        if lse.dtype is not _torch.float32 or lse.get_device() != dev or tuple(lse.shape) != (hq, T) or \
+                not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [heads, tokens] tensor on the device of q")
-        desc.lse = _ptr(lse)
-    _check_cu(cu_seqlens, dev)
-    if cu_seqlens.numel() < 1:
+        lp = lse.data_ptr()
+    n = cu_seqlens.numel() - 1
+    if n < 0:
         raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
-    desc.cu_seqlens, desc.n_seqs = _ptr(cu_seqlens), cu_seqlens.numel() - 1
-    if seq_used is not None:
-        _check_cu(seq_used, dev)
-        if seq_used.numel() != desc.n_seqs:
-            raise ValueError("seq_used must hold one int32 per sample")
-        desc.seq_used = _ptr(seq_used)
-    desc.total_tokens, desc.n_q_heads, desc.n_kv_heads, desc.head_dim = T, hq, k.shape[1], d
-    desc.causal, desc.scale = 1 if causal else 0, _scale(scale, d)
-    return desc
+    cu = _int32(cu_seqlens, dev, n + 1, "cu_seqlens")
+    used = 0 if seq_used is None else _int32(seq_used, dev, n, "seq_used")
+    return _VARLEN_PACK(*qv, *kv, *vv, *ov, lp, cu, used, T, n, hq, shape[1], d, 1 if causal else 0,
+                        d ** -0.5 if scale is None else scale), dev
 
 
 def attn_varlen_fwd(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] = None, seq_used=None, out=None,
@@ -295,16 +334,15 @@ def attn_varlen_fwd(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[fl
     ``scale``: 1/sqrt(d) unless given.  Returns out [T, Hq, d] (a new tensor unless given;
     rows that see no key are 0), with ``return_lse`` (out, lse): lse float32 [Hq, T], the
     natural logarithm of each row's sum, which the backward takes."""
-    import torch
-
+    torch = _torch or _load_torch()
     made = out is None
     if made:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if return_lse else None
-    desc = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
-    st = _on(q.device, load_library().attn_varlen_fwd, ctypes.byref(desc), _stream(stream, q.device))
-    _check("attn_varlen_fwd", st)
-    _keep_for(stream, out if made else None, lse)
+    desc, dev = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
+    _launch(load_library().attn_varlen_fwd, "attn_varlen_fwd", dev, stream, desc)
+    if stream is not None:
+        _keep_for(stream, out if made else None, lse)
     return (out, lse) if return_lse else out
 
 
@@ -315,38 +353,32 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
     arguments.  dq, dk and dv are written whole (new tensors unless given; rows of no sample
     get 0).  ``workspace``: a CUDA tensor of at least 8 * T * Hq bytes; allocated through
     torch unless given."""
-    import torch
-
+    torch = _torch or _load_torch()
     if lse is None:
         raise ValueError("the backward needs the forward's lse (return_lse=True)")
-    desc = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
-    g = AttnVarlenGrads()
-    made = []
-    grads = []
+    if dout is None:
+        raise ValueError("dout is required")
+    desc, dev = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
+    made, grads, packed = [], [], []
     for name, t, like in (("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is None:
-            if name == "dout":
-                raise ValueError("dout is required")
             t = torch.empty(like.shape, dtype=torch.bfloat16, device=q.device)
             made.append(t)
-        elif t.shape != like.shape or t.device != q.device:
+        elif t.shape != like.shape or t.get_device() != dev:
             raise ValueError("%s must have shape %s on %s" % (name, tuple(like.shape), q.device))
-        p, ts, hs = _view_args(t, name)
-        setattr(g, name, p)
-        setattr(g, name + "_stride_token", ts)
-        setattr(g, name + "_stride_head", hs)
+        packed += _view(t, name)
         grads.append(t)
     lib = load_library()
     if workspace is None:
-        need = int(lib.attn_varlen_bwd_workspace_bytes(q.shape[0], q.shape[1]))
+        need = lib.attn_varlen_bwd_workspace_bytes(q.shape[0], q.shape[1])
         workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=q.device)
         made.append(workspace)
-    elif not workspace.is_cuda or workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
-    st = _on(q.device, lib.attn_varlen_bwd, ctypes.byref(desc), ctypes.byref(g), _ptr(workspace),
-             workspace.numel() * workspace.element_size(), _stream(stream, q.device))
-    _check("attn_varlen_bwd", st)
-    _keep_for(stream, *made)
+    _launch(lib.attn_varlen_bwd, "attn_varlen_bwd", dev, stream, desc, _GRADS_PACK(*packed), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    if stream is not None:
+        _keep_for(stream, *made)
     return tuple(grads[1:])
 
 

@@ -80,10 +80,16 @@ int check_paged_sizes(const attn_paged_desc &p)
     return ROPE_OK;
 }
 
-// How many CTAs share the keys of a row: from the sizes on the host alone.
-int splits_of(const attn_paged_desc &p)
+// Which kernel serves a call and how it splits the keys: from the sizes on the host alone.
+struct PagedPlan {
+    DecodePlan decode;
+    int splits = 1;
+};
+
+PagedPlan plan_of(const attn_paged_desc &p)
 {
-    if (p.total_tokens == 0) return 1;
+    PagedPlan plan;
+    if (p.total_tokens == 0) return plan;
     AttnProblem a{};
     a.n_tokens = static_cast<int32_t>(p.total_tokens);
     a.n_seqs = p.n_seqs;
@@ -92,7 +98,9 @@ int splits_of(const attn_paged_desc &p)
     a.group = a.hq / a.hkv;
     int64_t keys = static_cast<int64_t>(p.max_pages) * p.cache.page_size;
     if (p.max_kv_len > 0 && p.max_kv_len < keys) keys = p.max_kv_len;
-    return attn_fwd_splits(a, keys);
+    plan.decode = attn_decode_plan(a, keys);
+    plan.splits = plan.decode.use ? plan.decode.splits : attn_fwd_splits(a, keys);
+    return plan;
 }
 
 }  // namespace
@@ -158,7 +166,7 @@ int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc)
     if (desc == nullptr) return ROPE_ERR_NULL;
     const int rc = check_paged_sizes(*desc);
     if (rc != ROPE_OK) return rc;
-    return 4 * attn_split_floats(desc->total_tokens, desc->n_q_heads, desc->cache.head_dim, splits_of(*desc));
+    return 4 * attn_split_floats(desc->total_tokens, desc->n_q_heads, desc->cache.head_dim, plan_of(*desc).splits);
 }
 
 int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream)
@@ -181,7 +189,8 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
     if (c.n_pages > 0 && (overlap(c.k, 2 * k_span(c), p.out, out.bytes()) ||
                           overlap(c.v, 2 * v_span(c), p.out, out.bytes())))
         return ROPE_ERR_OVERLAP;
-    const int64_t need = attn_paged_workspace_bytes(desc);
+    const PagedPlan plan = plan_of(p);
+    const int64_t need = 4 * attn_split_floats(T, p.n_q_heads, c.head_dim, plan.splits);
     if (need > 0 && workspace == nullptr) return ROPE_ERR_NULL;
     if (need > 0 && !aligned(workspace, 16)) return ROPE_ERR_ALIGN;
     if (workspace_bytes < need) return ROPE_ERR_WORKSPACE;
@@ -205,7 +214,10 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
     a.d = c.head_dim;
     a.causal = p.causal != 0;
     a.scale = p.scale;
-    return status_of(launch_attn_fwd(a, splits_of(p), static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)));
+    float *ws = static_cast<float *>(workspace);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return status_of(plan.decode.use ? launch_attn_decode(a, plan.decode, ws, st)
+                                     : launch_attn_fwd(a, plan.splits, ws, st));
 }
 
 int attn_fault(void)

@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
-    __shared__ int s_used;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -115,13 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const int order = static_cast<int>(blockIdx.x) / heads;
     const int slot = KEYS ? order : a.n_slots - 1 - order;
     if (warp == 0) {
-        const TileSlot f = find_slot(a.cu, a.n_seqs, a.n_tokens, kX, slot);
-        int used = 0;
-        if (f.sample >= 0 && f.sample < a.n_seqs) used = a.used != nullptr ? __ldg(a.used + f.sample) : f.end - f.start;
-        if (lane == 0) {
-            s_slot = f;
-            s_used = used;
-        }
+        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, kX, slot);
+        if (lane == 0) s_slot = f;
     }
     tc_fence_before();
     __syncthreads();
@@ -131,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const int first = where.tile * kX;                       // of the sample
     const int len = where.end - where.start;
     const bool live = where.tile >= 0 && first < len;
-    const int rows = min(len, max(s_used, 0));               // rows (and keys) in use
+    const int rows = min(len, max(where.used, 0));               // rows (and keys) in use
     // streamed tiles [y_lo, y_hi) of each pass, `passes` of them (the heads of the group)
     int y_lo = 0, y_hi = 0;
     if (live && first < rows) {

@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
-    __shared__ int s_used;
     __shared__ float s_swap[2][2][2][kRows];                           // [parity][row tile][half][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -122,13 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int slot = a.n_slots - 1 - static_cast<int>(blockIdx.x) / a.hkv;
     const int cta_tokens = 2 * a.tile_tokens;
     if (warp == 0) {
-        const TileSlot f = find_slot(a.cu, a.n_seqs, a.n_tokens, cta_tokens, slot);
-        int used = 0;
-        if (f.sample >= 0 && f.sample < a.n_seqs) used = a.used != nullptr ? __ldg(a.used + f.sample) : f.end - f.start;
-        if (lane == 0) {
-            s_slot = f;
-            s_used = used;
-        }
+        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, cta_tokens, slot);
+        if (lane == 0) s_slot = f;
     }
     tc_fence_before();
     __syncthreads();
@@ -142,13 +136,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     int rows_used, keys, offset;
     if (PAGED) {
         const bool inside = where.sample >= 0 && where.sample < a.n_seqs;
-        const int kv = max(s_used, -1);
+        const int kv = max(where.used, -1);
         rows_used = inside ? len : 0;
         keys = inside ? static_cast<int>(min(static_cast<int64_t>(max(kv, 0)),
                                              static_cast<int64_t>(a.max_pages) * a.page_size)) : 0;
         offset = kv - len;
     } else {
-        rows_used = min(len, max(s_used, 0));
+        rows_used = min(len, max(where.used, 0));
         keys = rows_used;
         offset = 0;
     }

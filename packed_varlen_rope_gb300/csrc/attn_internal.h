@@ -45,6 +45,14 @@ inline int64_t attn_split_floats(int64_t n_tokens, int hq, int d, int splits)
 {
     return splits > 1 ? n_tokens * hq * (static_cast<int64_t>(d) + 1) * splits : 0;
 }
+// The kernel for few new tokens a sequence: whether it serves the problem (sizes alone
+// decide), and over how many CTAs of a cluster and further splits a sequence's keys go.
+struct DecodePlan {
+    bool use = false;
+    int slots = 0, cluster = 1, splits = 1;
+};
+DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv);
+cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream);
 cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
                              cudaStream_t stream);
 int attn_fault_word(int *word);       // 0, and the device's fault word

@@ -294,10 +294,13 @@ struct TileSlot {
     int sample;        // -1 or n: outside the pack
     int start, end;    // the stretch's tokens [start, end), inside [0, T]
     int tile;          // index of the tile in the stretch
+    int used;          // the sample's entry of `used` (its length without one); 0 outside the pack
 };
 
-// Called by a whole warp.  Whatever cu holds, start and end stay in [0, T].
-__device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, int n, int T, int tile_tokens, int slot)
+// Called by a whole warp.  Whatever cu holds, start and end stay in [0, T].  Short packs
+// take one round of loads, the entries of `used` with them.
+__device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, const int32_t *__restrict__ used, int n,
+                                              int T, int tile_tokens, int slot)
 {
     const int lane = threadIdx.x & 31;
     auto bound = [&](int s) {                      // first token of stretch s, s in [0, n + 2]
@@ -305,22 +308,55 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, in
         if (s >= n + 2) return T;
         return min(max(__ldg(cu + (s - 1)), 0), T);
     };
-    int lo = 0, len = n + 2;
-    while (len > 1) {
-        const int step = (len + 31) >> 5;
-        const int s = lo + lane * step;
-        const bool below = s < lo + len && bound(s) / tile_tokens + s <= slot;
-        const uint32_t vote = __ballot_sync(0xffffffffu, below);
-        const int hit = vote == 0xffffffffu ? 31 : __ffs(~vote) - 2;       // last of the leading run
-        const int at = lo + max(hit, 0) * step;
-        len = min(step, lo + len - at);
-        lo = at;
-    }
     TileSlot r;
+    int lo;
+    constexpr int kShort = 4;
+    if (n + 3 <= 32 * kShort) {
+        int b[kShort], u[kShort], count = 0;
+#pragma unroll
+        for (int j = 0; j < kShort; ++j) {
+            const int s = lane + 32 * j;
+            b[j] = s <= n + 2 ? bound(s) : T;
+            u[j] = used != nullptr && s >= 1 && s <= n ? __ldg(used + (s - 1)) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kShort; ++j) {
+            const int s = lane + 32 * j;
+            count += __popc(__ballot_sync(0xffffffffu, s <= n + 1 && b[j] / tile_tokens + s <= slot));
+        }
+        lo = max(count - 1, 0);
+        r.start = r.end = r.used = 0;
+#pragma unroll
+        for (int j = 0; j < kShort; ++j) {
+            const int start = __shfl_sync(0xffffffffu, b[j], lo & 31), end = __shfl_sync(0xffffffffu, b[j], (lo + 1) & 31);
+            const int entry = __shfl_sync(0xffffffffu, u[j], lo & 31);
+            if (lo >> 5 == j) {
+                r.start = start;
+                r.used = entry;
+            }
+            if ((lo + 1) >> 5 == j) r.end = end;
+        }
+    } else {
+        lo = 0;
+        int len = n + 2;
+        while (len > 1) {
+            const int step = (len + 31) >> 5;
+            const int s = lo + lane * step;
+            const bool below = s < lo + len && bound(s) / tile_tokens + s <= slot;
+            const uint32_t vote = __ballot_sync(0xffffffffu, below);
+            const int hit = vote == 0xffffffffu ? 31 : __ffs(~vote) - 2;   // last of the leading run
+            const int at = lo + max(hit, 0) * step;
+            len = min(step, lo + len - at);
+            lo = at;
+        }
+        r.start = bound(lo);
+        r.end = bound(lo + 1);
+        r.used = used != nullptr && lo >= 1 && lo <= n ? __ldg(used + (lo - 1)) : 0;
+    }
     r.sample = lo - 1;
-    r.start = bound(lo);
-    r.end = max(bound(lo + 1), r.start);
+    r.end = max(r.end, r.start);
     r.tile = slot - (r.start / tile_tokens + lo);
+    if (used == nullptr && lo >= 1 && lo <= n) r.used = r.end - r.start;
     return r;
 }
 
