@@ -222,9 +222,10 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
 
 int attn_fault(void)
 {
-    int fwd = 0, bwd = 0;
-    if (attn_fault_word(&fwd) != 0 || attn_bwd_fault_word(&bwd) != 0) return ROPE_ERR_LAUNCH;
-    return fwd != 0 || bwd != 0 ? 1 : 0;
+    int fwd = 0, bwd = 0, dec = 0;
+    if (attn_fault_word(&fwd) != 0 || attn_bwd_fault_word(&bwd) != 0 || attn_decode_fault_word(&dec) != 0)
+        return ROPE_ERR_LAUNCH;
+    return fwd != 0 || bwd != 0 || dec != 0 ? 1 : 0;
 }
 
 }  // extern "C"

@@ -50,6 +50,7 @@ struct BwdArgs {
     const float2 *stats;                   // [hq, T]: (-lse log2(e), -D); -infinity first for rows not in use
     const int32_t *cu, *used;
     int32_t n_tokens, n_seqs, hq, hkv, group, d, causal, n_slots;
+    FastDiv div_x;                         // by kX
     float scale;
 };
 
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const int order = static_cast<int>(blockIdx.x) / heads;
     const int slot = KEYS ? order : a.n_slots - 1 - order;
     if (warp == 0) {
-        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, kX, slot);
+        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, a.div_x, slot);
         if (lane == 0) s_slot = f;
     }
     tc_fence_before();
@@ -486,6 +487,7 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
     a.causal = p.causal;
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, kX);
     a.scale = p.scale;
+    a.div_x = make_fastdiv(kX);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
     plain_config(cfg, attr, static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(xh), kThreads, Shared<DP>::kBytes,

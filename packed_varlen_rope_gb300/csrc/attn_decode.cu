@@ -8,7 +8,7 @@
 // Layout.  Up to 16 rows, (token, query head) pairs of one key head, fill one m16 tile of
 // the warp-level tensor product, so all heads of a group read the cache once.  Every warp
 // walks its own chunks of 16 keys (chunk w, w + W, ... of the sequence, W warps in all)
-// through its own ring of asynchronous copies, and meets no other warp until the end.  The
+// through its own ring of TMA loads, and meets no other warp until the end.  The
 // warps of a CTA join through shared memory, the CTAs of a cluster (up to 8 share a
 // sequence's keys) through distributed shared memory; only where that leaves SMs idle do
 // further splits join through the workspace in a second launch.
@@ -32,46 +32,39 @@
 namespace pvr {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 16;               // keys of a chunk
 constexpr int kRows = 16;
-constexpr int kStages = 3;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 30.0f;          // log2 growth of the maximum that triggers a rescale
 
+__device__ int g_attn_decode_fault;     // a bounded wait ran out
+
 struct DecodeArgs {
-    const __nv_bfloat16 *q;
-    int64_t q_ts, q_hs;
+    CUtensorMap q, k, v;
     __nv_bfloat16 *out;
     int64_t out_ts, out_hs;
-    Pages pages;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t max_pages, page_size, n_pages, box_rows;
     const int32_t *cu, *kv_lens;
     float *part_o, *part_lse;           // of each outer split, or NULL
     int32_t n_tokens, n_seqs, hq, hkv, group, d, causal, tile_tokens, splits;
-    FastDiv div_page;
+    FastDiv div_page, div_tile, div_group;
     float scale;
 };
 
-template <int DP>
+template <int DP, int WARPS>
 struct Shared {
-    static constexpr int kRowBytes = DP * 2;
-    static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;          // keys, then values
+    static constexpr int kRowBytes = DP * 2, kHalves = DP / 64;
+    static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;          // keys, then values, 64 of d at a time
+    static constexpr int kStages = 3;
     static constexpr int kWarpBytes = kStages * kChunkBytes;
-    static constexpr int kBytes = kWarps * kWarpBytes;
+    static constexpr int kOffQ = WARPS * kWarpBytes;
+    static constexpr int kBytes = kOffQ + kRows * kRowBytes + 1024;    // + alignment slack
     // after the loop the same memory holds each warp's o (binary32)
     static_assert(kWarpBytes >= kRows * DP * 4, "o of a warp fits its ring");
 };
-
-// 16 bytes global to shared, or zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -103,52 +96,66 @@ __device__ __forceinline__ uint32_t cluster_size()
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync()
+__device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-// What CTA `rank` of the cluster holds at this CTA's shared address `addr`.
-__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ void cluster_wait()
 {
-    float v;
-    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %1, %2;\n ld.shared::cluster.f32 %0, [p];\n}"
-                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
-    return v;
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank)
+// Stores at this CTA's shared address `addr`, in CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t rank, float v)
 {
-    float4 v;
-    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %4, %5;\n"
-                 " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n}"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
-    return v;
+    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.f32 [p], %2;\n}"
+                 ::"r"(addr), "r"(rank), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_store4(uint32_t addr, uint32_t rank, float4 v)
+{
+    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n"
+                 " st.shared::cluster.v4.f32 [p], {%2, %3, %4, %5};\n}"
+                 ::"r"(addr), "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_constant__ DecodeArgs a)
+template <int DP, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_constant__ DecodeArgs a)
 {
-    using Sh = Shared<DP>;
-    constexpr int kCols = DP / 8;                            // 16-byte columns of a row
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    __shared__ float s_cm[kRows], s_cl[kRows];               // the CTA's
-    __shared__ __align__(16) float s_o[kRows][DP];
+    using Sh = Shared<DP, WARPS>;
+    constexpr int kThreads = 32 * WARPS, kStages = Sh::kStages;
+    constexpr int kItems = kRows * DP / 4;                   // groups of four elements of o
+    constexpr uint32_t kHalfBytes = kKeys * 128;             // 64 of d of a chunk's keys
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t s_full[WARPS][kStages], s_qfull;
+    __shared__ float s_m[WARPS][kRows], s_l[WARPS][kRows];
+    // what the cluster's CTAs send: m and l of every row, and of o this CTA's share
+    __shared__ float s_pm[kMaxCluster][kRows], s_pl[kMaxCluster][kRows];
+    __shared__ float4 s_po[kItems];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t full = smem_addr(&s_full[warp][0]), q_full = smem_addr(&s_qfull);
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1);
+        if (warp == 0) mbar_init(q_full, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int unit = blockIdx.x / ranks, split = unit % a.splits;
     const int kvh = unit / a.splits % a.hkv, slot = unit / a.splits / a.hkv;
-    const TileSlot f = find_slot(a.cu, a.kv_lens, a.n_seqs, a.n_tokens, a.tile_tokens, slot);
+    const TileSlot f = find_slot(a.cu, a.kv_lens, a.n_seqs, a.n_tokens, a.div_tile, slot);
     const int first = f.tile * a.tile_tokens, len = f.end - f.start;
     if (f.tile < 0 || first >= len) return;                  // the whole cluster
+    if (ranks > 1) cluster_arrive();                         // this CTA runs: its memory may be written
     const bool inside = f.sample >= 0 && f.sample < a.n_seqs;
     const int kv = inside ? max(f.used, -1) : 0;
-    const int keys = inside ? static_cast<int>(min(static_cast<int64_t>(max(kv, 0)),
-                                                   static_cast<int64_t>(a.pages.max_pages) * a.pages.page_size)) : 0;
+    const int keys = inside ? min(max(kv, 0), a.max_pages * a.page_size) : 0;
     const int offset = kv - len;
     auto limit = [&](int i) {                                // keys that row i of the sample sees
         if (!inside || i >= len || i + offset < 0) return 0;
@@ -159,81 +166,70 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
     const int n_keys = limit(first + n_tok - 1);             // the most any row sees
     const int n_chunks = (n_keys + kKeys - 1) / kKeys;
 
+    // loads: a chunk is up to 8 boxes (keys or values, 64 of d, 16 or 8 keys), a lane each
+    const uint32_t ring = smem_addr(smem) + warp * Sh::kWarpBytes;
+    const int step = static_cast<int>(ranks) * a.splits * WARPS;
+    int chunk = (split * static_cast<int>(ranks) + static_cast<int>(rank)) * WARPS + warp;
+    const int box = lane & 7;
+    const int box_half = Sh::kHalves == 2 ? (box >> 1) & 1 : 0, box_key = (box >> Sh::kHalves) * a.box_rows;
+    const bool box_in = box_key < kKeys;
+    const uint32_t box_to = ((box & 1) * Sh::kHalves + box_half) * kHalfBytes + box_key * 128;
+    const CUtensorMap *map = (box & 1) == 0 ? &a.k : &a.v;
+    int page = a.n_pages, in_page = 0;                       // of this lane's box in the next chunk
+    // past the keys, and for a page id outside the pool, a coordinate past the pool's end: zeros
+    auto find_page = [&](int c) {
+        const int key = c * kKeys + box_key;
+        page = a.n_pages;
+        in_page = 0;
+        if (box_in && key < n_keys) {
+            const int index = static_cast<int>(fast_div(static_cast<uint32_t>(key), a.div_page));
+            in_page = key - index * a.page_size;
+            page = __ldg(a.table + f.sample * a.table_stride + index);
+            if (page < 0 || page >= a.n_pages) page = a.n_pages;
+        }
+    };
+    auto fetch = [&](int stage) {
+        if (box == 0) mbar_expect_tx(full + 8 * stage, Sh::kChunkBytes);
+        if (box_in)
+            tma_load_4d(ring + stage * Sh::kChunkBytes + box_to, map, 64 * box_half, in_page, kvh, page, full + 8 * stage);
+    };
+    // the first round: the ring but one stage at once, eight lanes a chunk
+    if (warp == 0 && lane == 31) {
+        mbar_expect_tx(q_full, static_cast<uint32_t>(a.group * a.tile_tokens) * Sh::kRowBytes);
+        for (int h = 0; h < Sh::kHalves; ++h)
+            tma_load_3d(smem_addr(smem) + Sh::kOffQ + h * kRows * 128, &a.q, 64 * h, kvh * a.group, f.start + first, q_full);
+    }
+    {
+        const int s = lane >> 3;
+        find_page(chunk + s * step);
+        if (s < kStages - 1 && chunk + s * step < n_chunks) fetch(s);
+    }
+    find_page(chunk + (kStages - 1) * step);
+
     // this lane's rows of the m16 tile: lane / 4 and that + 8
     int lim[2];
-    const __nv_bfloat16 *q_row[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int row = (lane >> 2) + 8 * r;
-        const bool in = row < n_rows;
-        const int tok = in ? row / a.group : 0, head = kvh * a.group + (in ? row - tok * a.group : 0);
-        lim[r] = in ? limit(first + tok) : 0;
-        q_row[r] = a.q + (f.start + first + tok) * a.q_ts + head * a.q_hs;
+        lim[r] = row < n_rows ? limit(first + static_cast<int>(fast_div(row, a.div_group))) : 0;
     }
-
-    const uint32_t ring = smem_addr(smem) + warp * Sh::kWarpBytes;
-    const int step = static_cast<int>(ranks) * a.splits * kWarps;
-    int chunk = (split * static_cast<int>(ranks) + static_cast<int>(rank)) * kWarps + warp;
-    const int32_t *table = a.pages.table + f.sample * a.pages.table_stride;
-    // a chunk's copies: lane l takes 16-byte column l % kCols of rows l / kCols, + 32 / kCols, ...
-    const int col = lane % kCols, row0 = lane / kCols;
-    constexpr int kRowStep = 32 / kCols;
-    const __nv_bfloat16 *k_base = a.pages.k + kvh * a.pages.k_hs + 8 * col;
-    const __nv_bfloat16 *v_base = a.pages.v + kvh * a.pages.v_hs + 8 * col;
-    const bool col_in = 8 * col < a.d;
-    // page ids of the chunk's two groups of 8 keys (a page holds whole groups)
-    auto pages_of = [&](int c, int (&id)[2], int (&at)[2]) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int key = c * kKeys + 8 * g;
-            id[g] = -1;
-            at[g] = 0;
-            if (key < n_keys) {
-                const int index = static_cast<int>(fast_div(static_cast<uint32_t>(key), a.div_page));
-                at[g] = key - index * a.pages.page_size;
-                id[g] = __ldg(table + index);
-            }
-        }
+    // ldmatrix addresses: matrix lane / 8, row lane % 8
+    const int mi = lane >> 3, mr = lane & 7;
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int phase) {
+        for (int i = 0; i < kWaitLimit; ++i)
+            if (__all_sync(0xffffffffu, mbar_try(bar, phase & 1))) return true;
+        if (lane == 0) atomicExch(&g_attn_decode_fault, 1);
+        return false;
     };
-    auto fetch = [&](int c, int stage, const int (&id)[2], const int (&at)[2]) {
-        const uint32_t dst = ring + stage * Sh::kChunkBytes;
-#pragma unroll
-        for (int j = 0; j < kKeys / kRowStep; ++j) {
-            const int r = row0 + j * kRowStep;
-            const int g = r >> 3;
-            const int page = g == 0 ? id[0] : id[1];
-            const bool valid = col_in && page >= 0 && page < a.pages.n_pages && c * kKeys + r < n_keys;
-            const int64_t slot_in = (g == 0 ? at[0] : at[1]) + (r & 7);
-            const uint32_t to = dst + r * Sh::kRowBytes + ((col ^ (r & 7)) << 4);
-            copy16(to, valid ? k_base + (page * a.pages.k_ps + slot_in * a.pages.k_ts) : a.q, valid);
-            copy16(to + kKeys * Sh::kRowBytes, valid ? v_base + (page * a.pages.v_ps + slot_in * a.pages.v_ts) : a.q, valid);
-        }
-    };
-
-    // the page ids of all chunks of the first round, then their copies
-    int id[2], at[2];
-    {
-        int ids[kStages - 1][2], ats[kStages - 1][2];
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) pages_of(chunk + s * step, ids[s], ats[s]);
-        pages_of(chunk + (kStages - 1) * step, id, at);
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            if (chunk + s * step < n_chunks) fetch(chunk + s * step, s, ids[s], ats[s]);
-            copy_commit();
-        }
-    }
-
-    // queries as the A operand: 16 x 16 per k step
+    // queries as the A operand: 16 x 16 per k step (rows past the tile's hold anything: they
+    // see no key)
     uint32_t qf[DP / 16][4];
+    ok = wait(q_full, 0);
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = 16 * s + 2 * (lane & 3) + 8 * (e >> 1);
-            const bool in = c < a.d && (lane >> 2) + 8 * (e & 1) < n_rows;
-            qf[s][e] = in ? __ldg(reinterpret_cast<const unsigned int *>(q_row[e & 1] + c)) : 0u;
-        }
+        const int r = 8 * (mi & 1) + mr, col = 2 * s + (mi >> 1);
+        ldmatrix4(qf[s], smem_addr(smem) + Sh::kOffQ + (col >> 3) * kRows * 128 + r * 128 + (((col & 7) ^ mr) << 4));
     }
     float o[DP / 8][4];
 #pragma unroll
@@ -243,22 +239,28 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     const float c = a.scale * kLog2e;
 
-    // ldmatrix addresses: matrix lane / 8, row lane % 8
-    const int mi = lane >> 3, mr = lane & 7;
-    int stage = 0;
-    for (; chunk < n_chunks; chunk += step) {
-        copy_wait<kStages - 2>();
-        __syncwarp();
+    int stage = 0, turn = 0;
+    for (; ok && chunk < n_chunks; chunk += step) {
+        if (!(ok = wait(full + 8 * stage, turn))) break;
         {   // the stage read one turn ago is free: the next chunk goes there
             const int next = chunk + (kStages - 1) * step;
-            const int to = stage == 0 ? kStages - 1 : stage - 1;
             if (next < n_chunks) {
-                fetch(next, to, id, at);
-                if (next + step < n_chunks) pages_of(next + step, id, at);
+                if (lane < 8) fetch(stage == 0 ? kStages - 1 : stage - 1);
+                find_page(next + step);
             }
-            copy_commit();
         }
-        const uint32_t kt = ring + stage * Sh::kChunkBytes, vt = kt + kKeys * Sh::kRowBytes;
+        const uint32_t kt = ring + stage * Sh::kChunkBytes, vt = kt + Sh::kHalves * kHalfBytes;
+        // value rows past the last key may hold anything: their weights are zero, but zero
+        // times NaN is not
+        const int valid = n_keys - chunk * kKeys;
+        if (valid < kKeys) {
+            for (int r = valid + (lane >> 3); r < kKeys; r += 4)
+                for (int h = 0; h < Sh::kHalves; ++h)
+                    *reinterpret_cast<uint4 *>(smem + warp * Sh::kWarpBytes + stage * Sh::kChunkBytes +
+                                               (Sh::kHalves + h) * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
         // S = Q K^T: two n8 tiles of 8 keys
         float s[2][4] = {};
 #pragma unroll
@@ -266,7 +268,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 uint32_t b[4];                               // 32 of d for 8 keys
-                ldmatrix4(b, kt + (8 * n + mr) * Sh::kRowBytes + (((4 * k + mi) ^ mr) << 4));
+                const int col = 4 * k + mi;
+                ldmatrix4(b, kt + (col >> 3) * kHalfBytes + (8 * n + mr) * 128 + (((col & 7) ^ mr) << 4));
                 mma16816(s[n], qf[2 * k], b[0], b[1]);
                 mma16816(s[n], qf[2 * k + 1], b[2], b[3]);
             }
@@ -317,13 +320,21 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
             uint32_t b[4];
-            ldmatrix4_t(b, vt + (8 * (mi & 1) + mr) * Sh::kRowBytes + (((2 * n + (mi >> 1)) ^ mr) << 4));
+            const int col = 2 * n + (mi >> 1);
+            ldmatrix4_t(b, vt + (col >> 3) * kHalfBytes + (8 * (mi & 1) + mr) * 128 + (((col & 7) ^ mr) << 4));
             mma16816(o[2 * n], p, b[0], b[1]);
             mma16816(o[2 * n + 1], p, b[2], b[3]);
         }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (++stage == kStages) {
+            stage = 0;
+            ++turn;
+        }
     }
-    copy_wait<0>();
+    if (!ok) {                          // copies in flight land before the memory is used again
+        for (int s = 0; s < kStages; ++s)
+            for (int t = 0; t < 2; ++t)
+                for (int i = 0; i < kWaitLimit / 64 && !mbar_try(full + 8 * s, t); ++i) {}
+    }
     __syncwarp();
 
     // ---- join: the warps of the CTA
@@ -344,64 +355,51 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
             *reinterpret_cast<float2 *>(mine + ((lane >> 2) + 8 * r) * DP + 8 * n + 2 * (lane & 3)) =
                 make_float2(o[n][2 * r], o[n][2 * r + 1]);
     __syncthreads();
+
+    // ---- and the CTAs of the cluster: item i of o goes to CTA i % ranks
+    if (ranks > 1) cluster_wait();
+    const int share = kItems / static_cast<int>(ranks);
     for (int i = threadIdx.x; i < n_rows * (DP / 4); i += kThreads) {
         const int row = i / (DP / 4), e = 4 * (i - row * (DP / 4));
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][row]);
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_m[w][row]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const float f = s_m[w][row] == -INFINITY ? 0.0f : ex2((s_m[w][row] - top) * c);
             const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * Sh::kWarpBytes) +
                                                                row * DP + e);
             acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
             sum += f * s_l[w][row];
         }
-        *reinterpret_cast<float4 *>(&s_o[row][e]) = acc;
-        if (e == 0) {
-            s_cm[row] = top;
-            s_cl[row] = sum;
+        const uint32_t to = i % ranks;
+        cluster_store4(smem_addr(&s_po[rank * share + i / ranks]), to, acc);
+        if (e < 4 * static_cast<int>(ranks)) {               // the row's first `ranks` items, one to each CTA
+            cluster_store(smem_addr(&s_pm[rank][row]), e >> 2, top);
+            cluster_store(smem_addr(&s_pl[rank][row]), e >> 2, sum);
         }
     }
-    if (ranks > 1) cluster_sync();
-    else __syncthreads();
-
-    // ---- join: the CTAs of the cluster; CTA r takes every ranks-th group of four elements
-    const uint32_t a_o = smem_addr(s_o), a_m = smem_addr(s_cm), a_l = smem_addr(s_cl);
-    for (int i = threadIdx.x * ranks + rank; i < n_rows * (DP / 4); i += kThreads * ranks) {
-        const int row = i / (DP / 4), e = 4 * (i - row * (DP / 4));
+    if (ranks > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    for (int j = threadIdx.x; j * ranks + rank < n_rows * (DP / 4); j += kThreads) {
+        const int i = j * ranks + rank, row = i / (DP / 4), e = 4 * (i - row * (DP / 4));
         if (e >= a.d) continue;
         float top = -INFINITY, sum = 0.0f;
+        for (uint32_t r = 0; r < ranks; ++r) top = fmaxf(top, s_pm[r][row]);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ranks == 1) {
-            top = s_cm[row];
-            x = *reinterpret_cast<const float4 *>(&s_o[row][e]);
-            sum = s_cl[row];
-        } else {
-            // all loads are independent (a CTA that saw no key holds zeros); past the cluster's
-            // size they repeat its own
-            float ms[kMaxCluster], ls[kMaxCluster];
-            float4 os[kMaxCluster];
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                const uint32_t from = r < static_cast<int>(ranks) ? r : rank;
-                ms[r] = cluster_load(a_m + 4 * row, from);
-                ls[r] = cluster_load(a_l + 4 * row, from);
-                os[r] = cluster_load4(a_o + 4 * (row * DP + e), from);
-                if (r >= static_cast<int>(ranks)) ms[r] = -INFINITY;
-            }
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) top = fmaxf(top, ms[r]);
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                const float f = ms[r] == -INFINITY ? 0.0f : ex2((ms[r] - top) * c);
-                x.x += f * os[r].x; x.y += f * os[r].y; x.z += f * os[r].z; x.w += f * os[r].w;
-                sum += f * ls[r];
-            }
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const float f = s_pm[r][row] == -INFINITY ? 0.0f : ex2((s_pm[r][row] - top) * c);
+            const float4 y = s_po[r * share + j];
+            x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+            sum += f * s_pl[r][row];
         }
-        const int tok_in = row / a.group;
+        const int tok_in = static_cast<int>(fast_div(row, a.div_group));
         const int head = kvh * a.group + row - tok_in * a.group;
         const int tok = f.start + first + tok_in;
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -415,14 +413,13 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
             if (e == 0) a.part_lse[to] = sum > 0.0f ? top * c + log2f(sum) : -INFINITY;
         }
     }
-    if (ranks > 1) cluster_sync();      // no CTA leaves while its memory is read
 }
 
-template <int DP>
+template <int DP, int WARPS>
 cudaError_t launch(const DecodeArgs &a, int cluster, int slots, cudaStream_t stream)
 {
     static std::atomic<uint64_t> sized{0};
-    const cudaError_t err = allow_smem(attn_decode_kernel<DP>, Shared<DP>::kBytes, sized);
+    const cudaError_t err = allow_smem(attn_decode_kernel<DP, WARPS>, Shared<DP, WARPS>::kBytes, sized);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -434,12 +431,12 @@ cudaError_t launch(const DecodeArgs &a, int cluster, int slots, cudaStream_t str
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(a.splits) * static_cast<unsigned>(slots) *
                        static_cast<unsigned>(a.hkv));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shared<DP>::kBytes;
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = Shared<DP, WARPS>::kBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DP>, a);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DP, WARPS>, a);
 }
 
 }  // namespace
@@ -454,27 +451,35 @@ DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv)
     // live CTAs of one rank: a sequence with new tokens fills at least one slot
     const int64_t ctas = static_cast<int64_t>(p.n_seqs < p.n_tokens ? p.n_seqs : p.n_tokens) * p.hkv;
     const int64_t chunks = (max_kv + kKeys - 1) / kKeys;
+    // a cluster of up to 8 CTAs a sequence: until the GPU is full, or, where sequences are long
+    // and may be uneven, until there are several rounds of CTAs
     plan.cluster = 1;
-    while (plan.cluster < kMaxCluster && ctas * plan.cluster < 8 * kSMs && chunks > 2 * plan.cluster * 2 * kWarps)
+    while (plan.cluster < kMaxCluster && chunks > 16 * plan.cluster &&
+           (ctas * plan.cluster < 2 * kSMs || (chunks > 128 * plan.cluster && ctas * plan.cluster < 8 * kSMs)))
         plan.cluster *= 2;
     plan.splits = 1;
-    while (ctas * plan.cluster * plan.splits * 2 <= kSMs && chunks > 32 * plan.cluster * plan.splits * kWarps &&
-           plan.splits < 64)
+    while (ctas * plan.cluster * plan.splits * 2 <= kSMs && chunks > 128 * plan.cluster * plan.splits && plan.splits < 64)
         plan.splits *= 2;
+    // one CTA an SM at most: eight warps each keep more loads in flight
+    plan.warps = ctas * plan.cluster * plan.splits <= kSMs ? 8 : 4;
     plan.use = static_cast<int64_t>(plan.slots) * p.hkv * plan.cluster * plan.splits <= INT32_MAX;
     return plan;
 }
 
 cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream)
 {
-    DecodeArgs a{};
-    a.q = p.q.p;
-    a.q_ts = p.q.ts;
-    a.q_hs = p.q.hs;
+    DecodeArgs a;
+    const int tile = kRows / p.group;
+    a.box_rows = p.pages.page_size % kKeys == 0 ? kKeys : 8;
+    if (!make_q_map(&a.q, p, tile) || !make_page_maps(&a.k, &a.v, p, a.box_rows)) return cudaErrorInvalidValue;
     a.out = p.out.p;
     a.out_ts = p.out.ts;
     a.out_hs = p.out.hs;
-    a.pages = p.pages;
+    a.table = p.pages.table;
+    a.table_stride = p.pages.table_stride;
+    a.max_pages = p.pages.max_pages;
+    a.page_size = p.pages.page_size;
+    a.n_pages = p.pages.n_pages;
     a.cu = p.cu;
     a.kv_lens = p.used;
     a.n_tokens = p.n_tokens;
@@ -484,17 +489,27 @@ cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, flo
     a.group = p.group;
     a.d = p.d;
     a.causal = p.causal;
-    a.tile_tokens = kRows / p.group;
+    a.tile_tokens = tile;
     a.splits = plan.splits;
+    a.div_tile = make_fastdiv(static_cast<uint32_t>(a.tile_tokens));
+    a.div_group = make_fastdiv(static_cast<uint32_t>(p.group));
     a.div_page = make_fastdiv(static_cast<uint32_t>(p.pages.page_size));
     a.scale = p.scale;
     const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;
     a.part_o = workspace;
     a.part_lse = plan.splits > 1 ? workspace + plan.splits * rows * p.d : nullptr;
-    const cudaError_t err = p.d <= 64 ? launch<64>(a, plan.cluster, plan.slots, stream)
-                                      : launch<128>(a, plan.cluster, plan.slots, stream);
+    const cudaError_t err = plan.warps == 8
+                                ? (p.d <= 64 ? launch<64, 8>(a, plan.cluster, plan.slots, stream)
+                                             : launch<128, 8>(a, plan.cluster, plan.slots, stream))
+                                : (p.d <= 64 ? launch<64, 4>(a, plan.cluster, plan.slots, stream)
+                                             : launch<128, 4>(a, plan.cluster, plan.slots, stream));
     if (err != cudaSuccess || plan.splits == 1) return err;
     return launch_attn_join(a.part_o, a.part_lse, p, plan.splits, stream);
+}
+
+int attn_decode_fault_word(int *word)
+{
+    return cudaMemcpyFromSymbol(word, g_attn_decode_fault, sizeof *word) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace pvr

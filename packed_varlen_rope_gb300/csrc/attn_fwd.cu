@@ -59,6 +59,7 @@ struct FwdArgs {
     int32_t max_pages, page_size, n_pages, box_rows;
     int32_t n_tokens, n_seqs, hq, hkv, group, tile_tokens, d, causal;   // tile_tokens: of one row tile
     int32_t n_slots, splits;
+    FastDiv div_cta;                    // by the CTA's tokens
     float scale;
 };
 
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int slot = a.n_slots - 1 - static_cast<int>(blockIdx.x) / a.hkv;
     const int cta_tokens = 2 * a.tile_tokens;
     if (warp == 0) {
-        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, cta_tokens, slot);
+        const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, a.div_cta, slot);
         if (lane == 0) s_slot = f;
     }
     tc_fence_before();
@@ -556,24 +557,13 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, 
     const int dp = p.d <= 64 ? 64 : 128;
     const int tile = kRows / p.group;
     a.tile_tokens = tile;
-    {
-        const int64_t ext[3] = {p.d, p.hq, p.n_tokens}, st[3] = {1, p.q.hs, p.q.ts};
-        const int box[3] = {64, p.group, tile};
-        if (!make_map(&a.q, p.q.p, 3, ext, st, box)) return cudaErrorInvalidValue;
-    }
+    if (!make_q_map(&a.q, p, tile)) return cudaErrorInvalidValue;
     a.box_rows = kKeys;
     if (p.paged) {
+        // the largest power of two that divides a page: boxes never straddle pages
         a.box_rows = p.pages.page_size & -p.pages.page_size;
         if (a.box_rows > kKeys) a.box_rows = kKeys;
-        // an empty pool: a map over one page that no coordinate reaches
-        const bool none = p.pages.n_pages == 0;
-        const int64_t ext[4] = {p.d, p.pages.page_size, p.hkv, none ? 1 : p.pages.n_pages};
-        const int64_t ks[4] = {1, p.pages.k_ts, p.pages.k_hs, p.pages.k_ps};
-        const int64_t vs[4] = {1, p.pages.v_ts, p.pages.v_hs, p.pages.v_ps};
-        const int box[4] = {64, a.box_rows, 1, 1};
-        if (!make_map(&a.k, none ? p.q.p : p.pages.k, 4, ext, ks, box) ||
-            !make_map(&a.v, none ? p.q.p : p.pages.v, 4, ext, vs, box))
-            return cudaErrorInvalidValue;
+        if (!make_page_maps(&a.k, &a.v, p, a.box_rows)) return cudaErrorInvalidValue;
     } else {
         const int64_t ext[4] = {p.d, p.n_tokens, p.hkv, 1};
         const int64_t ks[4] = {1, p.k.ts, p.k.hs, 0}, vs[4] = {1, p.v.ts, p.v.hs, 0};
@@ -601,6 +591,7 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, 
     a.causal = p.causal;
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, 2 * tile);
     a.splits = splits;
+    a.div_cta = make_fastdiv(static_cast<uint32_t>(2 * tile));
     a.scale = p.scale;
     const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;
     a.part_o = workspace;

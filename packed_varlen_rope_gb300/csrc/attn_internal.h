@@ -49,7 +49,7 @@ inline int64_t attn_split_floats(int64_t n_tokens, int hq, int d, int splits)
 // decide), and over how many CTAs of a cluster and further splits a sequence's keys go.
 struct DecodePlan {
     bool use = false;
-    int slots = 0, cluster = 1, splits = 1;
+    int slots = 0, cluster = 1, splits = 1, warps = 4;
 };
 DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv);
 cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream);
@@ -57,6 +57,7 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
                              cudaStream_t stream);
 int attn_fault_word(int *word);       // 0, and the device's fault word
 int attn_bwd_fault_word(int *word);
+int attn_decode_fault_word(int *word);
 // Backward: the rows' statistics, then dk and dv, then dq.
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream);
 

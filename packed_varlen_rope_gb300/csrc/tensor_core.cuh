@@ -12,6 +12,8 @@
 
 #include <cstdint>
 
+#include "fastdiv.cuh"
+
 namespace pvr {
 
 // Waits are bounded: after kWaitLimit tries (each of them suspends for a while) the waiter raises the
@@ -300,7 +302,7 @@ struct TileSlot {
 // Called by a whole warp.  Whatever cu holds, start and end stay in [0, T].  Short packs
 // take one round of loads, the entries of `used` with them.
 __device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, const int32_t *__restrict__ used, int n,
-                                              int T, int tile_tokens, int slot)
+                                              int T, FastDiv tile, int slot)
 {
     const int lane = threadIdx.x & 31;
     auto bound = [&](int s) {                      // first token of stretch s, s in [0, n + 2]
@@ -322,7 +324,7 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, co
 #pragma unroll
         for (int j = 0; j < kShort; ++j) {
             const int s = lane + 32 * j;
-            count += __popc(__ballot_sync(0xffffffffu, s <= n + 1 && b[j] / tile_tokens + s <= slot));
+            count += __popc(__ballot_sync(0xffffffffu, s <= n + 1 && static_cast<int>(fast_div(b[j], tile)) + s <= slot));
         }
         lo = max(count - 1, 0);
         r.start = r.end = r.used = 0;
@@ -342,7 +344,7 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, co
         while (len > 1) {
             const int step = (len + 31) >> 5;
             const int s = lo + lane * step;
-            const bool below = s < lo + len && bound(s) / tile_tokens + s <= slot;
+            const bool below = s < lo + len && static_cast<int>(fast_div(bound(s), tile)) + s <= slot;
             const uint32_t vote = __ballot_sync(0xffffffffu, below);
             const int hit = vote == 0xffffffffu ? 31 : __ffs(~vote) - 2;   // last of the leading run
             const int at = lo + max(hit, 0) * step;
@@ -355,7 +357,7 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t *__restrict__ cu, co
     }
     r.sample = lo - 1;
     r.end = max(r.end, r.start);
-    r.tile = slot - (r.start / tile_tokens + lo);
+    r.tile = slot - (static_cast<int>(fast_div(r.start, tile)) + lo);
     if (used == nullptr && lo >= 1 && lo <= n) r.used = r.end - r.start;
     return r;
 }
