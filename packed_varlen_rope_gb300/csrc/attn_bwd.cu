@@ -37,7 +37,6 @@ namespace pvr {
 namespace {
 
 constexpr int kThreads = 384;              // two softmax warpgroups, one for products and loads
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;   // 2 * 224 + 56 = 3 * 168, the launch's
 constexpr int kX = 128, kY = 64;           // rows of the resident and the streamed tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -143,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     constexpr uint32_t kColS = 0, kColP = 128, kCol1 = 256, kCol2 = 256 + DP;
 
     if (warp >= 8) {
-        regs_shrink<kRegsOther>();
         if (warp == 9) {
             // -------------------------------------------------------- loads
             int issued = 0;
@@ -175,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 if (s_abort != 0) {     // copies in flight land before the memory is given back
                     for (int t = max(0, issued - kStages); t < issued; ++t) {
                         if (KEYS) mbar_arrive(y_full + 8 * (t % kStages));   // for the statistics that may not come
-                        for (int w = 0; w < kWaitLimit && !mbar_try(y_full + 8 * (t % kStages), (t / kStages) & 1); ++w) {}
+                        mbar_drain(y_full + 8 * (t % kStages), (t / kStages) & 1);
                     }
-                    for (int w = 0; w < kWaitLimit && !mbar_try(x_full, 0); ++w) {}
+                    mbar_drain(x_full, 0);
                 }
             }
             __syncwarp();
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             }
             if (!ok) {                  // products in flight finish before tensor memory is freed
                 if (lane == 0) tc_commit(drain);
-                for (int w = 0; w < kWaitLimit && !mbar_try(drain, 0); ++w) {}
+                mbar_drain(drain, 0);
             }
             __syncwarp();
         } else if (KEYS && warp == 10) {
@@ -285,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         }
     } else {
         // ---------------------------------------------------------- softmax
-        regs_grow<kRegsSoftmax>();
         const int w = warp >> 2;
         const int row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -313,45 +310,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 to = min(rows, a.causal ? xi + 1 : rows) - y0;
             }
             const bool masked = KEYS ? a.causal && y0 < first + kX : y0 + kY > (a.causal ? min(rows, first + 1) : rows);
-            uint32_t s[64], p[64];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                tmem_ld32(t_s + 32 * j, reinterpret_cast<uint32_t(&)[32]>(s[32 * j]));
-                tmem_ld32(t_p + 32 * j, reinterpret_cast<uint32_t(&)[32]>(p[32 * j]));
-            }
-            tc_wait_ld(reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32]));
-            tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(p[0]));
-            tmem_loaded(reinterpret_cast<uint32_t(&)[32]>(p[32]));
+            for (int half = 0; half < 2; ++half) {
+                uint32_t s[32], p[32], sp[16], sd[16];
+                tmem_ld32(t_s + 32 * half, s);
+                tmem_ld32(t_p + 32 * half, p);
+                tc_wait_ld(s);
+                tmem_loaded(p);
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                float4 nl, nd;
-                if (KEYS) {
-                    nl = *reinterpret_cast<const float4 *>(st + j);
-                    nd = *reinterpret_cast<const float4 *>(st + kY + j);
-                } else {
-                    nl = make_float4(mine.x, mine.x, mine.x, mine.x);
-                    nd = make_float4(mine.y, mine.y, mine.y, mine.y);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = j + 2 * h;
-                    float2 pr = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2,
-                                     h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w));
-                    pr.x = ex2(pr.x);
-                    pr.y = ex2(pr.y);
-                    if (masked) {
-                        if (e < from || e >= to) pr.x = 0.0f;
-                        if (e + 1 < from || e + 1 >= to) pr.y = 0.0f;
+                for (int j = 0; j < 32; j += 4) {
+                    float4 nl, nd;
+                    if (KEYS) {
+                        nl = *reinterpret_cast<const float4 *>(st + 32 * half + j);
+                        nd = *reinterpret_cast<const float4 *>(st + kY + 32 * half + j);
+                    } else {
+                        nl = make_float4(mine.x, mine.x, mine.x, mine.x);
+                        nd = make_float4(mine.y, mine.y, mine.y, mine.y);
                     }
-                    const float2 ds = mul2(pr, add2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])),
-                                                    h == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w)));
-                    s[e / 2] = pack_bf16(pr.x, pr.y);
-                    p[e / 2] = pack_bf16(ds.x, ds.y);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = j + 2 * h, col = 32 * half + e;
+                        float2 pr = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2,
+                                         h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w));
+                        pr.x = ex2(pr.x);
+                        pr.y = ex2(pr.y);
+                        if (masked) {
+                            if (col < from || col >= to) pr.x = 0.0f;
+                            if (col + 1 < from || col + 1 >= to) pr.y = 0.0f;
+                        }
+                        const float2 ds = mul2(pr, add2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])),
+                                                        h == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w)));
+                        sp[e / 2] = pack_bf16(pr.x, pr.y);
+                        sd[e / 2] = pack_bf16(ds.x, ds.y);
+                    }
                 }
+                // P and dS take half the columns: what they overwrite has been read
+                if (KEYS) tmem_st16(t_s + 16 * half, sp);
+                tmem_st16(t_p + 16 * half, sd);
             }
-            if (KEYS) tmem_st32(t_s, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-            tmem_st32(t_p, reinterpret_cast<uint32_t(&)[32]>(p[0]));
             tc_wait_st();
             tc_fence_before();
             __syncwarp();

@@ -62,6 +62,7 @@ struct Shared {
     static constexpr int kWarpBytes = kStages * kChunkBytes;
     static constexpr int kOffQ = WARPS * kWarpBytes;
     static constexpr int kBytes = kOffQ + kRows * kRowBytes + 1024;    // + alignment slack
+    static_assert(kStages <= 5, "the first round of loads is four chunks of eight lanes");
     // after the loop the same memory holds each warp's o (binary32)
     static_assert(kWarpBytes >= kRows * DP * 4, "o of a warp fits its ring");
 };
@@ -217,10 +218,7 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
     const int mi = lane >> 3, mr = lane & 7;
     bool ok = true;
     auto wait = [&](uint32_t bar, int phase) {
-        for (int i = 0; i < kWaitLimit; ++i)
-            if (__all_sync(0xffffffffu, mbar_try(bar, phase & 1))) return true;
-        if (lane == 0) atomicExch(&g_attn_decode_fault, 1);
-        return false;
+        return warp_wait(bar, phase & 1, nullptr, &g_attn_decode_fault);
     };
     // queries as the A operand: 16 x 16 per k step (rows past the tile's hold anything: they
     // see no key)
@@ -331,9 +329,7 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
         }
     }
     if (!ok) {                          // copies in flight land before the memory is used again
-        for (int s = 0; s < kStages; ++s)
-            for (int t = 0; t < 2; ++t)
-                for (int i = 0; i < kWaitLimit / 64 && !mbar_try(full + 8 * s, t); ++i) {}
+        for (int s = 0; s < kStages; ++s) mbar_drain(full + 8 * s, (turn + (s < stage ? 1 : 0)) & 1);
     }
     __syncwarp();
 

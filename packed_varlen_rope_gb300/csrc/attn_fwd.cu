@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         if (s_abort != 0) {             // copies in flight land before the memory is given back
             for (int t = max(0, issued - kStages); t < issued; ++t)
-                for (int w = 0; w < kWaitLimit && !mbar_try(kv_full + 8 * (t % kStages), (t / kStages) & 1); ++w) {}
+                mbar_drain(kv_full + 8 * (t % kStages), (t / kStages) & 1);
             for (int x = 0; x < 2; ++x)
                 if (count[x] > 0)
-                    for (int w = 0; w < kWaitLimit && !mbar_try(q_full + 8 * x, 0); ++w) {}
+                    mbar_drain(q_full + 8 * x, 0);
         }
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         if (!ok) {                      // products in flight finish before tensor memory is freed
             if (lane == 0) tc_commit(drain);
-            for (int w = 0; w < kWaitLimit && !mbar_try(drain, 0); ++w) {}
+            mbar_drain(drain, 0);
         }
         __syncwarp();
     }

@@ -16,10 +16,18 @@
 
 namespace pvr {
 
-// Waits are bounded: after kWaitLimit tries (each of them suspends for a while) the waiter raises the
-// CTA's abort flag and the device's fault word, every other wait of the CTA then ends too,
-// and the kernel drains its copies, frees its tensor memory and returns.
-constexpr int kWaitLimit = 1 << 22;
+// Waits are bounded in time: after kWaitNs the waiter raises the CTA's abort flag and the
+// device's fault word, every other wait that is still open ends when it sees either, and the
+// kernel drains its copies, frees its tensor memory and returns.
+constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 20000000ull;
+
+__device__ __forceinline__ unsigned long long now_ns()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
 {
@@ -54,22 +62,38 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 }
 
 // One thread waits for the phase of the given parity; false when the CTA gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
 {
-    for (int i = 0; i < kWaitLimit; ++i) {
+    const unsigned long long start = now_ns();
+    for (int i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
-        if (*abort_flag != 0) return false;
+        if (abort_flag != nullptr && *abort_flag != 0) return false;
+        if ((i & 63) == 0 && (now_ns() - start > kWaitNs || *static_cast<volatile int *>(fault) != 0)) break;
     }
-    *abort_flag = 1;
+    if (abort_flag != nullptr) *abort_flag = 1;
     atomicExch(fault, 1);
     return false;
+}
+
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
+{
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try(bar, parity)) return true;
+    return mbar_wait_slow(bar, parity, abort_flag, fault);
+}
+
+// After an abort: waits a little for copies or products in flight.
+static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long start = now_ns();
+    while (!mbar_try(bar, parity) && now_ns() - start < kDrainNs) {}
 }
 
 // A converged warp waits; the result is the same in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *fault)
 {
-    const bool ok = mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, fault);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, fault));
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
@@ -222,12 +246,6 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32])
 {
     asm volatile("" : PVR_RW8(r, 0), PVR_RW8(r, 8), PVR_RW8(r, 16), PVR_RW8(r, 24)::"memory");
 }
-
-// This warpgroup's registers a thread from here on (its share of the block's at launch).
-template <int N>
-__device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // 2^x from the special-function unit (subnormal results flush to zero).
 __device__ __forceinline__ float ex2(float x)
