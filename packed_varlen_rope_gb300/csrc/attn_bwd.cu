@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const uint32_t base = smem_addr(smem);
     const uint32_t bars = base + Sh::kOffBars;
     const uint32_t x_full = bars, s_full = bars + 16, p_full = bars + 32, done = bars + 48, drain = bars + 56,
-                   y_full = bars + 64, y_empty = y_full + 8 * kStages;
+                   acc_done = bars + 72, y_full = bars + 88, y_empty = y_full + 8 * kStages;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
@@ -85,8 +85,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         mbar_init(x_full, 1);
         mbar_init(done, 1);
-        mbar_init(drain, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(drain + 8 * i, 1);
+            mbar_init(acc_done + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 4);
         }
@@ -179,78 +180,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 }
             }
             __syncwarp();
-        } else if (warp == 8) {
-            // ----------------------------------------------------- products
-            constexpr uint32_t kDescS = mma_desc(kX, kY, false);
-            constexpr uint32_t kDescA = mma_desc(kX, DP, true);
+        } else if (warp == 8 || warp == 11) {
+            // ------- products: S and dP by warp 8, those with P and dS by warp 11
             bool ok = true;
             auto wait = [&](uint32_t bar, int phase) {
                 if (ok) ok = warp_wait(bar, phase & 1, &s_abort, &g_attn_bwd_fault);
             };
             const uint32_t ubase = uniform(base), utmem = uniform(tmem);
-            const uint32_t d_x = desc_lo(ubase, 0), d_y = desc_lo(ubase + Sh::kOffY, 0),
-                           d_ymn = desc_lo(ubase + Sh::kOffY, kYBox);
-            // S and dP of tile t
-            auto scores = [&](int t) {
-                const int stage = t % kStages, b = t & 1;
-                const uint32_t y = Sh::kOffY + stage * Sh::kStageBytes;
-                wait(y_full + 8 * stage, t / kStages);
-                // streamed rows past the sample's end (another sample's, or anything) are
-                // cleared: their weights are zero, but zero times NaN is not
-                const int valid = rows - (y_lo + t % per_pass) * kY;
-                if (ok && valid < kY) {
-                    for (int r = valid + (lane >> 3); r < kY; r += 4)
-                        for (int i = 0; i < 2 * Sh::kBoxes; ++i)
-                            *reinterpret_cast<uint4 *>(smem + y + i * kYBox + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
+            if (warp == 8) {
+                constexpr uint32_t kDescS = mma_desc(kX, kY, false);
+                const uint32_t d_x = desc_lo(ubase, 0), d_y = desc_lo(ubase + Sh::kOffY, 0);
+                if (n_tiles > 0) wait(x_full, 0);
+                for (int t = 0; ok && t < n_tiles; ++t) {
+                    const int stage = t % kStages, b = t & 1;
+                    wait(y_full + 8 * stage, t / kStages);
+                    // streamed rows past the sample's end (another sample's, or anything) are
+                    // cleared: their weights are zero, but zero times NaN is not
+                    const int valid = rows - (y_lo + t % per_pass) * kY;
+                    if (ok && valid < kY) {
+                        uint8_t *y = smem + Sh::kOffY + stage * Sh::kStageBytes;
+                        for (int r = valid + (lane >> 3); r < kY; r += 4)
+                            for (int i = 0; i < 2 * Sh::kBoxes; ++i)
+                                *reinterpret_cast<uint4 *>(y + i * kYBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    // the buffer's P and dS have been used
+                    if (t >= 2) wait(acc_done + 8 * b, (t >> 1) - 1);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        const uint32_t yd = d_y + stage * (Sh::kStageBytes >> 4);
+#pragma unroll
+                        for (int s = 0; s < DP / 16; ++s) {
+                            const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
+                            mma_ss(utmem + kColS + b * kY, d_x + ax, yd + ay, kDescS, s > 0);
+                        }
+#pragma unroll
+                        for (int s = 0; s < DP / 16; ++s) {
+                            const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
+                            mma_ss(utmem + kColP + b * kY, d_x + (Sh::kXBytes >> 4) + ax, yd + (Sh::kYBytes >> 4) + ay,
+                                   kDescS, s > 0);
+                        }
+                        tc_commit(s_full + 8 * b);
+                    }
                     __syncwarp();
                 }
-                if (ok && elect_one()) {
-                    const uint32_t yd = d_y + stage * (Sh::kStageBytes >> 4);
+            } else {
+                constexpr uint32_t kDescA = mma_desc(kX, DP, true);
+                const uint32_t d_y = desc_lo(ubase + Sh::kOffY, kYBox);
+                for (int t = 0; ok && t < n_tiles; ++t) {
+                    const int stage = t % kStages, b = t & 1;
+                    const uint32_t y = d_y + stage * (Sh::kStageBytes >> 4);
+                    wait(p_full + 8 * b, t >> 1);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        if (KEYS) {
 #pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
-                        mma_ss(utmem + kColS + b * kY, d_x + ax, yd + ay, kDescS, s > 0);
-                    }
-#pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
-                        mma_ss(utmem + kColP + b * kY, d_x + (Sh::kXBytes >> 4) + ax, yd + (Sh::kYBytes >> 4) + ay, kDescS,
-                               s > 0);
-                    }
-                    tc_commit(s_full + 8 * b);
-                }
-                __syncwarp();
-            };
-            if (n_tiles > 0) {
-                wait(x_full, 0);
-                scores(0);
-            }
-            for (int t = 0; ok && t < n_tiles; ++t) {
-                if (t + 1 < n_tiles) scores(t + 1);
-                const int stage = t % kStages, b = t & 1;
-                const uint32_t y = d_ymn + stage * (Sh::kStageBytes >> 4);
-                wait(p_full + 8 * b, t >> 1);
-                tc_fence_after();
-                if (ok && elect_one()) {
-                    if (KEYS) {
+                            for (int s = 0; s < kY / 16; ++s)
+                                mma_ts(utmem + kCol2, utmem + kColS + b * kY + s * 8,
+                                       y + (Sh::kYBytes >> 4) + s * (2048 >> 4), kDescA, t > 0 || s > 0);
+                        }
 #pragma unroll
                         for (int s = 0; s < kY / 16; ++s)
-                            mma_ts(utmem + kCol2, utmem + kColS + b * kY + s * 8,
-                                   y + (Sh::kYBytes >> 4) + s * (2048 >> 4), kDescA, t > 0 || s > 0);
+                            mma_ts(utmem + kCol1, utmem + kColP + b * kY + s * 8, y + s * (2048 >> 4), kDescA, t > 0 || s > 0);
+                        tc_commit(acc_done + 8 * b);
+                        tc_commit(y_empty + 8 * stage);
+                        if (t + 1 == n_tiles) tc_commit(done);
                     }
-#pragma unroll
-                    for (int s = 0; s < kY / 16; ++s)
-                        mma_ts(utmem + kCol1, utmem + kColP + b * kY + s * 8, y + s * (2048 >> 4), kDescA, t > 0 || s > 0);
-                    tc_commit(y_empty + 8 * stage);
-                    if (t + 1 == n_tiles) tc_commit(done);
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (!ok) {                  // products in flight finish before tensor memory is freed
-                if (lane == 0) tc_commit(drain);
-                mbar_drain(drain, 0);
+                const uint32_t mine = drain + (warp == 8 ? 0 : 8);
+                if (lane == 0) tc_commit(mine);
+                mbar_drain(mine, 0);
             }
             __syncwarp();
         } else if (KEYS && warp == 10) {
