@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const uint32_t base = smem_addr(smem);
     const uint32_t bars = base + Sh::kOffBars;
     const uint32_t x_full = bars, s_full = bars + 16, p_full = bars + 32, done = bars + 48, drain = bars + 56,
-                   acc_done = bars + 72, y_full = bars + 88, y_empty = y_full + 8 * kStages;
+                   acc_done = bars + 72, x_ready = bars + 88, y_full = bars + 96,
+                   y_empty = y_full + 8 * kStages;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(x_full, 1);
+        mbar_init(x_ready, 8);
         mbar_init(done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(drain + 8 * i, 1);
@@ -140,7 +142,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     }
     const int per_pass = y_hi - y_lo;
     const int n_tiles = per_pass * (KEYS ? a.group : 1);
+    // tensor memory: S and dP twice, the accumulators, and, where there is room, X as bf16: an
+    // operand read from there leaves shared memory to the other one, and 64-wide products run
+    // at the tensor core's rate (32 cycles a k step) instead of shared memory's (48)
     constexpr uint32_t kColS = 0, kColP = 128, kCol1 = 256, kCol2 = 256 + DP;
+    constexpr bool kXInTmem = !KEYS || DP == 64;
+    constexpr uint32_t kColX = KEYS ? 256 + 2 * DP : 256 + DP;
 
     if (warp >= 8) {
         if (warp == 9) {
@@ -190,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (warp == 8) {
                 constexpr uint32_t kDescS = mma_desc(kX, kY, false);
                 const uint32_t d_x = desc_lo(ubase, 0), d_y = desc_lo(ubase + Sh::kOffY, 0);
-                if (n_tiles > 0) wait(x_full, 0);
+                if (n_tiles > 0) wait(kXInTmem ? x_ready : x_full, 0);
+                tc_fence_after();
                 for (int t = 0; ok && t < n_tiles; ++t) {
                     const int stage = t % kStages, b = t & 1;
                     wait(y_full + 8 * stage, t / kStages);
@@ -213,13 +221,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 #pragma unroll
                         for (int s = 0; s < DP / 16; ++s) {
                             const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
-                            mma_ss(utmem + kColS + b * kY, d_x + ax, yd + ay, kDescS, s > 0);
+                            if (kXInTmem) mma_ts(utmem + kColS + b * kY, utmem + kColX + 8 * s, yd + ay, kDescS, s > 0);
+                            else mma_ss(utmem + kColS + b * kY, d_x + ax, yd + ay, kDescS, s > 0);
                         }
 #pragma unroll
                         for (int s = 0; s < DP / 16; ++s) {
                             const uint32_t ax = ((s / 4) * kXBox + (s % 4) * 32) >> 4, ay = ((s / 4) * kYBox + (s % 4) * 32) >> 4;
-                            mma_ss(utmem + kColP + b * kY, d_x + (Sh::kXBytes >> 4) + ax, yd + (Sh::kYBytes >> 4) + ay,
-                                   kDescS, s > 0);
+                            if (kXInTmem)
+                                mma_ts(utmem + kColP + b * kY, utmem + kColX + DP / 2 + 8 * s, yd + (Sh::kYBytes >> 4) + ay,
+                                       kDescS, s > 0);
+                            else
+                                mma_ss(utmem + kColP + b * kY, d_x + (Sh::kXBytes >> 4) + ax, yd + (Sh::kYBytes >> 4) + ay,
+                                       kDescS, s > 0);
                         }
                         tc_commit(s_full + 8 * b);
                     }
@@ -297,14 +310,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             mine = __ldg(a.stats + static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi);
         const float2 c2 = make_float2(c, c);
         bool ok = true;
-        for (int t = w; t < n_tiles; t += 2) {
+        if (kXInTmem && n_tiles > 0) {          // X1 by one group, X2 by the other, a row a thread
+            ok = warp_wait(x_full, 0, &s_abort, &g_attn_bwd_fault);
+            const uint32_t src = base + w * Sh::kXBytes + row * 128;
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j) {              // 32 of d: four 16-byte columns, swizzled
+                uint32_t r[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = 4 * j + e;
+                    const float4 v = smem_load4(src + (col >> 3) * kXBox + (((col & 7) ^ (row & 7)) << 4));
+                    r[4 * e] = __float_as_uint(v.x);
+                    r[4 * e + 1] = __float_as_uint(v.y);
+                    r[4 * e + 2] = __float_as_uint(v.z);
+                    r[4 * e + 3] = __float_as_uint(v.w);
+                }
+                tmem_st16(tmem + lanes + kColX + w * (DP / 2) + 16 * j, r);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_ready);
+        }
+        for (int t = w; ok && t < n_tiles; t += 2) {
             const int y0 = (y_lo + t % per_pass) * kY;
             const int stage = t % kStages;
             ok = warp_wait(s_full + 8 * w, (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
             if (KEYS && ok) ok = warp_wait(y_full + 8 * stage, (t / kStages) & 1, &s_abort, &g_attn_bwd_fault);
             if (!ok) break;
             tc_fence_after();
-            const float *st = reinterpret_cast<const float *>(smem + Sh::kOffY + stage * Sh::kStageBytes + 2 * Sh::kYBytes);
+            const uint32_t st = base + Sh::kOffY + stage * Sh::kStageBytes + 2 * Sh::kYBytes;
             // columns [from, to) are visible: keys of a query row, or queries of a key row
             int from = 0, to = kY;
             if (KEYS) {
@@ -324,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 for (int j = 0; j < 32; j += 4) {
                     float4 nl, nd;
                     if (KEYS) {
-                        nl = *reinterpret_cast<const float4 *>(st + 32 * half + j);
-                        nd = *reinterpret_cast<const float4 *>(st + kY + 32 * half + j);
+                        nl = smem_load4(st + 4 * (32 * half + j));
+                        nd = smem_load4(st + 4 * (kY + 32 * half + j));
                     } else {
                         nl = make_float4(mine.x, mine.x, mine.x, mine.x);
                         nd = make_float4(mine.y, mine.y, mine.y, mine.y);

@@ -274,6 +274,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Four floats at a shared-memory address.
+__device__ __forceinline__ float4 smem_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
 // Both halves of a pair through one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
