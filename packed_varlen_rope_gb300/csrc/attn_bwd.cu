@@ -39,7 +39,8 @@ namespace pvr {
 namespace {
 
 constexpr int kThreads = 640;              // four softmax warpgroups, one for products and loads
-constexpr int kMmaWarp = 16, kStatsWarp = 17, kLoadWarp = 18;   // loads: one warp for Y1 (and X), one for Y2
+constexpr int kMmaWarp = 16, kWatchWarp = 17;
+constexpr int kLoadWarp = 18;              // loads: one warp for X, Y1 and its statistics, one for Y2
 constexpr int kTile = 128;                 // rows of the resident and of the streamed tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -89,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const uint32_t base = smem_addr(smem);
     const uint32_t bars = base + Sh::kOffBars;
     const uint32_t x_full = bars, s_full = bars + 8, p_full = bars + 16, ds_full = bars + 24, done = bars + 32,
-                   drain = bars + 40, dp_full = bars + 48, st_full = bars + 64, st_empty = bars + 80, y_full = bars + 96,
+                   drain = bars + 40, dp_full = bars + 48, st_full = bars + 64, st_empty = bars + 80, first_full = bars + 96,
+                   y_full = bars + 104,
                    y_empty = y_full + 8 * (Sh::kY1 + Sh::kY2);
     Rest &rest = *reinterpret_cast<Rest *>(smem + Sh::kOffRest);
     volatile int &s_abort = rest.abort;
@@ -101,10 +103,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         mbar_init(x_full, 1);
         mbar_init(s_full, 1);
-        mbar_init(p_full, 16);
+        mbar_init(p_full, 17);
         mbar_init(ds_full, 16);
         mbar_init(done, 1);
         mbar_init(drain, 1);
+        mbar_init(first_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(dp_full + 8 * i, 1);
             mbar_init(st_full + 8 * i, 1);
@@ -160,37 +163,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 
     if (warp >= kLoadWarp) {
         // ------------------------------------------------------------ loads
-        if (lane == 0 && n_tiles > 0) {
-            const int which = warp - kLoadWarp;
-            if (which == 0) {
-                mbar_expect_tx(x_full, 2 * Sh::kTileBytes);
-                for (int b = 0; b < Sh::kBoxes; ++b) {
-                    tma_load_3d(base + b * kBox, &a.x1, 64 * b, where.start + first, xhead, x_full);
-                    tma_load_3d(base + Sh::kTileBytes + b * kBox, &a.x2, 64 * b, where.start + first, xhead, x_full);
+        const int which = warp - kLoadWarp;
+        if (which == 0 && lane == 0 && n_tiles > 0) {
+            mbar_expect_tx(x_full, 2 * Sh::kTileBytes);
+            for (int b = 0; b < Sh::kBoxes; ++b) {
+                tma_load_3d(base + b * kBox, &a.x1, 64 * b, where.start + first, xhead, x_full);
+                tma_load_3d(base + Sh::kTileBytes + b * kBox, &a.x2, 64 * b, where.start + first, xhead, x_full);
+            }
+        }
+        const CUtensorMap *map = which == 0 ? &a.y1 : &a.y2;
+        const int places = which == 0 ? Sh::kY1 : Sh::kY2, place0 = which == 0 ? 0 : Sh::kY1;
+        int g = 0, y = y_lo, at = 0, before = 0, issued = 0;
+        for (int t = 0; t < n_tiles; ++t) {
+            const uint32_t bar = y_full + 8 * (place0 + at);
+            const int yhead = KEYS ? xhead * a.group + g : xhead / a.group;
+            float2 v[4];
+            if (KEYS && which == 0) {
+                const float2 *src = a.stats + static_cast<int64_t>(yhead) * a.n_tokens + where.start;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = y * kTile + lane + 32 * i;
+                    v[i] = r < rows ? __ldg(src + r) : make_float2(-INFINITY, 0.0f);
                 }
             }
-            const CUtensorMap *map = which == 0 ? &a.y1 : &a.y2;
-            const int places = which == 0 ? Sh::kY1 : Sh::kY2, place0 = which == 0 ? 0 : Sh::kY1;
-            int g = 0, y = y_lo, at = 0, before = 0, issued = 0;
-            for (int t = 0; t < n_tiles; ++t) {
-                const uint32_t bar = y_full + 8 * (place0 + at);
-                if (before > 0 && !mbar_wait(y_empty + 8 * (place0 + at), (before - 1) & 1, &s_abort, &g_attn_bwd_fault))
-                    break;
+            if (before > 0 && !warp_wait(y_empty + 8 * (place0 + at), (before - 1) & 1, &s_abort, &g_attn_bwd_fault)) break;
+            if (lane == 0) {
                 const uint32_t dst = base + Sh::kOffY + (place0 + at) * Sh::kTileBytes;
-                const int yhead = KEYS ? xhead * a.group + g : xhead / a.group;
                 mbar_expect_tx(bar, Sh::kTileBytes);
                 for (int b = 0; b < Sh::kBoxes; ++b)
                     tma_load_3d(dst + b * kBox, map, 64 * b, where.start + y * kTile, yhead, bar);
-                ++issued;
-                if (++y == y_hi) {
-                    y = y_lo;
-                    ++g;
-                }
-                if (++at == places) {
-                    at = 0;
-                    ++before;
-                }
             }
+            ++issued;
+            if (KEYS && which == 0) {   // the statistics of Y1's rows
+                if (t >= 2 && !warp_wait(st_empty + 8 * (t & 1), ((t >> 1) - 1) & 1, &s_abort, &g_attn_bwd_fault)) break;
+                float *dst = reinterpret_cast<float *>(smem + Sh::kOffStats + (t & 1) * 2 * kTile * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dst[lane + 32 * i] = v[i].x;
+                    dst[kTile + lane + 32 * i] = v[i].y;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(st_full + 8 * (t & 1));
+            }
+            if (++y == y_hi) {
+                y = y_lo;
+                ++g;
+            }
+            if (++at == places) {
+                at = 0;
+                ++before;
+            }
+        }
+        if (n_tiles > 0) {
             if (s_abort != 0) {         // copies in flight land before the memory is given back
                 for (int t = max(0, issued - places); t < issued; ++t)
                     mbar_drain(y_full + 8 * place(t, which), turn(t, which) & 1);
@@ -198,6 +222,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             }
         }
         __syncwarp();
+    } else if (warp == kWatchWarp) {
+        // ------ the arrival of Y: the products wait for it and for P at one barrier, as every
+        // wait costs a few hundred cycles while the tensor core reads shared memory
+        bool ok = n_tiles > 0 && warp_wait(x_full, 0, &s_abort, &g_attn_bwd_fault);
+        int y = y_lo;
+        for (int t = 0; ok && t <= n_tiles; ++t) {
+            if (t < n_tiles) {
+                ok = warp_wait(y_full + 8 * place(t, 0), turn(t, 0) & 1, &s_abort, &g_attn_bwd_fault) &&
+                     warp_wait(y_full + 8 * place(t, 1), turn(t, 1) & 1, &s_abort, &g_attn_bwd_fault);
+                if (!ok) break;
+                // streamed rows past the sample's end (another sample's, or anything) are
+                // cleared: their weights are zero, but zero times NaN is not
+                const int valid = rows - y * kTile;
+                if (++y == y_hi) y = y_lo;
+                if (valid < kTile) {
+                    for (int which = 0; which < 2; ++which) {
+                        uint8_t *tile = smem + Sh::kOffY + place(t, which) * Sh::kTileBytes;
+                        for (int r = valid + (lane >> 3); r < kTile; r += 4)
+                            for (int i = 0; i < Sh::kBoxes; ++i)
+                                *reinterpret_cast<uint4 *>(tile + i * kBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+            }
+            // tile t counts towards phase t - 1 of the barrier, once the phase before is over
+            if (t >= 2) ok = warp_wait(p_full, (t - 2) & 1, &s_abort, &g_attn_bwd_fault);
+            if (ok && lane == 0) mbar_arrive(t == 0 ? first_full : p_full);
+            __syncwarp();
+        }
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         constexpr uint32_t kDescS = mma_desc(kTile, kTile, false), kDescA = mma_desc(kTile, DP, true);
@@ -208,106 +262,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
             if (ok) ok = warp_wait(bar, phase & 1, &s_abort, &g_attn_bwd_fault);
-        };
-        int y_at[2] = {y_lo, y_lo};
-        // S(t) (which = 0) or dP(t) (1)
-        auto scores = [&](int t, int which) {
-            const int at = place(t, which);
-            wait(y_full + 8 * at, turn(t, which));
-            // streamed rows past the sample's end (another sample's, or anything) are
-            // cleared: their weights are zero, but zero times NaN is not
-            const int valid = rows - y_at[which] * kTile;
-            if (++y_at[which] == y_hi) y_at[which] = y_lo;
-            if (ok && valid < kTile) {
-                uint8_t *y = smem + Sh::kOffY + at * Sh::kTileBytes;
-                for (int r = valid + (lane >> 3); r < kTile; r += 4)
-                    for (int i = 0; i < Sh::kBoxes; ++i)
-                        *reinterpret_cast<uint4 *>(y + i * kBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (ok && elect_one()) {
-                const uint32_t d = utmem + (which == 0 ? kColS : kColP + (t & 1) * kNextP);
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const uint32_t off = ((s / 4) * kBox + (s % 4) * 32) >> 4;
-                    mma_ss(d, d_x + which * kStep + off, d_y + at * kStep + off, kDescS, s > 0);
-                }
-                // (queries: dP of the next tile may be complete before every warp has seen this one)
-                tc_commit(which == 0 ? s_full : dp_full + 8 * (t & 1));
-                if (!KEYS && which == 1) tc_commit(y_empty + 8 * at);
-            }
-            __syncwarp();
-        };
-        // acc1 += dS Y1 (which = 0) or acc2 += P Y2 (1)
-        auto accumulate = [&](int t, int which) {
-            const int at = place(t, which);
-            wait(which == 0 ? ds_full : p_full, t);
             tc_fence_after();
-            if (ok && elect_one()) {
-                const uint32_t d = utmem + (which == 0 ? kCol1 : kCol2);
-                const uint32_t from = utmem + (which == 0 ? kColP + (t & 1) * kNextP : kColS);
+        };
+        // S(t) (which = 0) or dP(t) (1); one elected thread
+        auto scores = [&](int t, int which) {
+            const uint32_t d = utmem + (which == 0 ? kColS : kColP + (t & 1) * kNextP);
+            const uint32_t y = d_y + place(t, which) * kStep;
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(d, from + 32 * (s / 2) + 8 * (s % 2), d_ymn + at * kStep + s * (2048 >> 4), kDescA, t > 0 || s > 0);
-                tc_commit(y_empty + 8 * at);
-                if (KEYS && which == 0) tc_commit(st_empty + 8 * (t & 1));
-                if (which == 0 && t + 1 == n_tiles) tc_commit(done);
+            for (int s = 0; s < DP / 16; ++s) {
+                const uint32_t off = ((s / 4) * kBox + (s % 4) * 32) >> 4;
+                mma_ss(d, d_x + which * kStep + off, y + off, kDescS, s > 0);
             }
-            __syncwarp();
+            // (queries: dP of the next tile may be complete before every warp has seen this one)
+            tc_commit(which == 0 ? s_full : dp_full + 8 * (t & 1));
+            if (!KEYS && which == 1) tc_commit(y_empty + 8 * place(t, which));
+        };
+        // acc1 += dS Y1 (which = 0) or acc2 += P Y2 (1); one elected thread
+        auto accumulate = [&](int t, int which) {
+            const uint32_t d = utmem + (which == 0 ? kCol1 : kCol2);
+            const uint32_t from = utmem + (which == 0 ? kColP + (t & 1) * kNextP : kColS);
+            const uint32_t y = d_ymn + place(t, which) * kStep;
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+                mma_ts(d, from + 32 * (s / 2) + 8 * (s % 2), y + s * (2048 >> 4), kDescA, t > 0 || s > 0);
+            tc_commit(y_empty + 8 * place(t, which));
+            if (KEYS && which == 0) tc_commit(st_empty + 8 * (t & 1));
+            if (which == 0 && t + 1 == n_tiles) tc_commit(done);
         };
         if (n_tiles > 0) {
-            wait(x_full, 0);
-            scores(0, 0);
-            scores(0, 1);
+            wait(first_full, 0);
+            if (ok && elect_one()) {
+                scores(0, 0);
+                scores(0, 1);
+            }
+            __syncwarp();
         }
         for (int t = 0; ok && t < n_tiles; ++t) {
             const bool more = t + 1 < n_tiles;
-            if (KEYS) {
-                accumulate(t, 1);
+            if (KEYS || more) wait(p_full, t);
+            if (ok && elect_one()) {
+                if (KEYS) accumulate(t, 1);
                 if (more) scores(t + 1, 0);
-                accumulate(t, 0);
-                if (more) scores(t + 1, 1);
-            } else {
-                if (more) {
-                    wait(p_full, t);                         // S(t) has been read
-                    tc_fence_after();
-                    scores(t + 1, 0);
-                    scores(t + 1, 1);
-                }
-                accumulate(t, 0);
+                if (!KEYS && more) scores(t + 1, 1);
             }
+            __syncwarp();
+            wait(ds_full, t);
+            if (ok && elect_one()) {
+                accumulate(t, 0);
+                if (KEYS && more) scores(t + 1, 1);
+            }
+            __syncwarp();
         }
         if (!ok) {                      // products in flight finish before tensor memory is freed
             if (lane == 0) tc_commit(drain);
             mbar_drain(drain, 0);
         }
         __syncwarp();
-    } else if (KEYS && warp == kStatsWarp) {
-        // ------------------------- statistics of the streamed rows, per tile
-        int g = 0, y = y_lo;
-        for (int t = 0; t < n_tiles; ++t) {
-            const float2 *src = a.stats + static_cast<int64_t>(xhead * a.group + g) * a.n_tokens + where.start;
-            float2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = y * kTile + lane + 32 * i;
-                v[i] = r < rows ? __ldg(src + r) : make_float2(-INFINITY, 0.0f);
-            }
-            if (t >= 2 && !warp_wait(st_empty + 8 * (t & 1), ((t >> 1) - 1) & 1, &s_abort, &g_attn_bwd_fault)) break;
-            float *dst = reinterpret_cast<float *>(smem + Sh::kOffStats + (t & 1) * 2 * kTile * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dst[lane + 32 * i] = v[i].x;
-                dst[kTile + lane + 32 * i] = v[i].y;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(st_full + 8 * (t & 1));
-            if (++y == y_hi) {
-                y = y_lo;
-                ++g;
-            }
-        }
     }
     if (warp < kMmaWarp) {
         // ---------------------------------------------------------- softmax
