@@ -39,7 +39,7 @@ namespace {
 __device__ int g_attn_fault;            // a bounded wait ran out
 
 constexpr int kThreads = 640;           // four softmax warpgroups, one for products and loads
-constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kWatchWarp = 18;
 constexpr int kRows = 128;              // rows of a row tile
 constexpr int kKeys = 128;              // keys of a key tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const uint32_t base = smem_addr(smem);
     const uint32_t bars = base + Sh::kOffBars;
     const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_done = bars + 48, kv_full = bars + 64,
-                   kv_empty = kv_full + 8 * kStages, drain = kv_empty + 8 * kStages;
+                   kv_empty = kv_full + 8 * kStages, first_full = kv_empty + 8 * kStages, drain = first_full + 8;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ TileSlot s_slot;
@@ -95,13 +95,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 8);
+            mbar_init(p_full + 8 * i, 9);
             mbar_init(o_done + 8 * i, 1);
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(kv_full + 8 * i, 1);
             mbar_init(kv_empty + 8 * i, 1);
         }
+        mbar_init(first_full, 1);
         mbar_init(drain, 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -170,7 +171,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
     constexpr uint32_t kColS = 0, kColO = 256;
 
-    if (warp >= kMmaWarp) {
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
@@ -222,6 +222,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (count[x] > 0)
                     mbar_drain(q_full + 8 * x, 0);
         }
+    } else if (warp == kWatchWarp) {
+        // ------ the arrival of keys and values: the products wait for them and for P at one
+        // barrier, as every wait costs a few hundred cycles while the tensor core reads
+        // shared memory
+        auto full = [&](int t) {
+            return warp_wait(kv_full + 8 * (t % kStages), (t / kStages) & 1, &s_abort, &g_attn_fault);
+        };
+        bool ok = n_tiles > 0 && full(0);
+        for (int x = 0; x < 2; ++x)
+            if (ok && count[x] > 0) ok = warp_wait(q_full + 8 * x, 0, &s_abort, &g_attn_fault);
+        if (ok && lane == 0) mbar_arrive(first_full);
+        __syncwarp();
+        for (int i = 0; ok && i < n_tiles; ++i) {
+            const int t = 2 * i + 1;
+            ok = full(t);
+            // value rows past the last key (another sample's, or stale) are cleared: their
+            // weights are zero, but zero times NaN is not
+            const int valid = keys - (lo_tile + i) * kKeys;
+            if (ok && valid < kKeys) {
+                uint8_t *v = smem + Sh::kOffKV + (t % kStages) * Sh::kTileBytes;
+                for (int r = valid + (lane >> 3); r < kKeys; r += 4)
+                    for (int b = 0; b < Sh::kBoxes; ++b)
+                        *reinterpret_cast<uint4 *>(v + b * kBoxBytes + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (ok && i + 1 < n_tiles) ok = full(t + 1);
+            for (int x = 0; x < 2; ++x) {
+                if (i >= count[x]) continue;
+                // counts towards phase i, once the phase before is over
+                if (ok && i > 0) ok = warp_wait(p_full + 8 * x, (i - 1) & 1, &s_abort, &g_attn_fault);
+                if (ok && lane == 0) mbar_arrive(p_full + 8 * x);
+                __syncwarp();
+            }
+        }
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         constexpr uint32_t kDescS = mma_desc(kRows, kKeys, false);
@@ -229,66 +264,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const uint32_t ubase = uniform(base), utmem = uniform(tmem);
         const uint32_t d_q = desc_lo(ubase, 0), d_k = desc_lo(ubase + Sh::kOffKV, 0),
                        d_v = desc_lo(ubase + Sh::kOffKV, kBoxBytes);
-        auto scores = [&](int x, int stage) {
-            const uint32_t q = d_q + x * (Sh::kTileBytes >> 4), k = d_k + stage * (Sh::kTileBytes >> 4);
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const uint32_t at = ((s / 4) * kBoxBytes + (s % 4) * 32) >> 4;
-                    mma_ss(utmem + kColS + x * kKeys, q + at, k + at, kDescS, s > 0);
-                }
-                tc_commit(s_full + 8 * x);
-            }
-            __syncwarp();
-        };
+        constexpr uint32_t kStep = Sh::kTileBytes >> 4;
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
             if (ok) ok = warp_wait(bar, phase & 1, &s_abort, &g_attn_fault);
+            tc_fence_after();
+        };
+        // S of row tile x; one elected thread
+        auto scores = [&](int x, int stage) {
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s) {
+                const uint32_t at = ((s / 4) * kBoxBytes + (s % 4) * 32) >> 4;
+                mma_ss(utmem + kColS + x * kKeys, d_q + x * kStep + at, d_k + stage * kStep + at, kDescS, s > 0);
+            }
+            tc_commit(s_full + 8 * x);
         };
         if (n_tiles > 0) {
-            wait(kv_full, 0);
-            for (int x = 0; x < 2; ++x) {
-                if (count[x] == 0) continue;
-                wait(q_full + 8 * x, 0);
-                if (ok) scores(x, 0);
+            wait(first_full, 0);
+            if (ok && elect_one()) {
+                for (int x = 0; x < 2; ++x)
+                    if (count[x] > 0) scores(x, 0);
+                tc_commit(kv_empty);
             }
-            if (ok && elect_one()) tc_commit(kv_empty);
             __syncwarp();
         }
         for (int i = 0; ok && i < n_tiles; ++i) {
-            const int tv = 2 * i + 1, sv = tv % kStages, tk = 2 * i + 2, sk = tk % kStages;
-            wait(kv_full + 8 * sv, tv / kStages);
-            // value rows past the last key (another sample's, or stale) are cleared: their
-            // weights are zero, but zero times NaN is not
-            const int valid = keys - (lo_tile + i) * kKeys;
-            if (ok && valid < kKeys) {
-                for (int r = valid + (lane >> 3); r < kKeys; r += 4)
-                    for (int b = 0; b < Sh::kBoxes; ++b)
-                        *reinterpret_cast<uint4 *>(smem + Sh::kOffKV + sv * Sh::kTileBytes + b * kBoxBytes + r * 128 + (lane & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (i + 1 < n_tiles) wait(kv_full + 8 * sk, tk / kStages);
+            const int sv = (2 * i + 1) % kStages, sk = (2 * i + 2) % kStages;
             for (int x = 0; x < 2; ++x) {
                 if (i >= count[x]) continue;
                 wait(p_full + 8 * x, i);
-                tc_fence_after();
                 if (ok && elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kKeys / 16; ++s)
-                        mma_ts(utmem + kColO + x * DP, utmem + kColS + x * kKeys + s * 8,
-                               d_v + sv * (Sh::kTileBytes >> 4) + s * (2048 >> 4), kDescO, i > 0 || s > 0);
+                        mma_ts(utmem + kColO + x * DP, utmem + kColS + x * kKeys + s * 8, d_v + sv * kStep + s * (2048 >> 4),
+                               kDescO, i > 0 || s > 0);
                     if (i + 1 == count[x]) tc_commit(o_done + 8 * x);
+                    else scores(x, sk);
+                    if (x == 1 || i >= count[1]) {           // the last to read these stages
+                        tc_commit(kv_empty + 8 * sv);
+                        if (i + 1 < n_tiles) tc_commit(kv_empty + 8 * sk);
+                    }
                 }
                 __syncwarp();
-                if (ok && i + 1 < count[x]) scores(x, sk);
             }
-            if (ok && elect_one()) {
-                tc_commit(kv_empty + 8 * sv);
-                if (i + 1 < n_tiles) tc_commit(kv_empty + 8 * sk);
-            }
-            __syncwarp();
         }
         if (!ok) {                      // products in flight finish before tensor memory is freed
             if (lane == 0) tc_commit(drain);
@@ -296,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         __syncwarp();
     }
-    } else {
+    if (warp < kMmaWarp) {
         // ---------------------------------------------------------- softmax
         // a row is two threads', 64 of a tile's keys each
         const int x = warp >> 3, half = (warp >> 2) & 1;
