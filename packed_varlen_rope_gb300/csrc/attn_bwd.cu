@@ -50,7 +50,7 @@ struct BwdArgs {
     CUtensorMap x1, x2, y1, y2;
     __nv_bfloat16 *out1, *out2;            // dk, dv, or dq
     int64_t o1_ts, o1_hs, o2_ts, o2_hs;
-    const float2 *stats;                   // [hq, T]: (-lse log2(e), -D); -infinity first for rows not in use
+    float2 *stats;                         // [hq, T]: (-lse log2(e), -D); -infinity first for rows not in use
     const int32_t *cu, *used;
     int32_t n_tokens, n_seqs, hq, hkv, group, d, causal, n_slots;
     FastDiv div_tile;                      // by kTile
@@ -330,8 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         const float c = a.scale * kLog2e;
         float2 mine = make_float2(-INFINITY, 0.0f);
         if (!KEYS && live && xi < rows)
-            mine = __ldg(a.stats + static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi);
+            mine = a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi];
         const float2 c2 = make_float2(c, c);
+        // The D that comes in is dout . o with o rounded to bf16.  Against the few keys of a
+        // sample's first rows that error is as large as the rounding of ds; where all keys of
+        // the rows are in one tile, D is taken from them instead, D = sum_j p dP, and kept for
+        // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).
+        const bool single = !KEYS && n_tiles == 1;
         bool ok = true;
         int y = y_lo;
         for (int t = 0; t < n_tiles; ++t) {
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             }
             ok = warp_wait(s_full, t & 1, &s_abort, &g_attn_bwd_fault);
             if (KEYS && ok) ok = warp_wait(st_full + 8 * (t & 1), (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
-            if (!ok) break;
+            if (!ok && !single) break;         // (a single tile's warps meet below in any case)
             tc_fence_after();
             uint32_t s[32], packed[16];
             tmem_ld32(t_s, s);
@@ -387,13 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
             }
-            ok = warp_wait(dp_full + 8 * (t & 1), (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
-            if (!ok) break;
+            if (ok) ok = warp_wait(dp_full + 8 * (t & 1), (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
+            if (!ok && !single) break;
             tc_fence_after();
             const uint32_t t_dp = t_p + (t & 1) * kNextP;
             uint32_t dp[32];
             tmem_ld32(t_dp, dp);
             tc_wait_ld(dp);
+            if (single) {
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sum[e & 1] = fmaf(__uint_as_float(s[e]), __uint_as_float(dp[e]), sum[e & 1]);
+                float *swap = reinterpret_cast<float *>(smem + Sh::kOffStats);   // [quarter][row]
+                swap[quarter * kTile + row] = sum[0] + sum[1];
+                named_barrier(1 + (warp & 3), 128);
+                mine.y = -((swap[row] + swap[kTile + row]) + (swap[2 * kTile + row] + swap[3 * kTile + row]));
+                if (quarter == 0 && live && xi < rows)
+                    a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y;
+            }
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 nd = KEYS ? smem_load4(st + 4 * (kTile + j)) : make_float4(mine.y, mine.y, mine.y, mine.y);
@@ -530,7 +546,7 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
     a.out2 = p.dv.p;
     a.o2_ts = p.dv.ts;
     a.o2_hs = p.dv.hs;
-    a.stats = reinterpret_cast<const float2 *>(p.stats);
+    a.stats = reinterpret_cast<float2 *>(p.stats);
     a.cu = p.cu;
     a.used = p.used;
     a.n_tokens = p.n_tokens;
@@ -563,9 +579,10 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream)
                                          static_cast<const float *>(p.lse), reinterpret_cast<float2 *>(p.stats),
                                          static_cast<int>(p.n_tokens), static_cast<int>(p.hq), static_cast<int>(p.d));
     if (err != cudaSuccess) return err;
-    err = p.d <= 64 ? launch_pass<64, true>(p, stream) : launch_pass<128, true>(p, stream);
+    // dq first: it improves the statistics that the pass over the keys reads
+    err = p.d <= 64 ? launch_pass<64, false>(p, stream) : launch_pass<128, false>(p, stream);
     if (err != cudaSuccess) return err;
-    return p.d <= 64 ? launch_pass<64, false>(p, stream) : launch_pass<128, false>(p, stream);
+    return p.d <= 64 ? launch_pass<64, true>(p, stream) : launch_pass<128, true>(p, stream);
 }
 
 int attn_bwd_fault_word(int *word)
