@@ -433,36 +433,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             tc_fence_after();
         }
         // epilogue: dk and dv by two groups each, or a quarter of dq's columns a group
-        const bool mine_row = live && xi < len;
         const bool in_use = xi < rows && n_tiles > 0;
         const bool second = KEYS && quarter >= 2;
         const float mult = second ? 1.0f : a.scale;
-        __nv_bfloat16 *dst = (second ? a.out2 : a.out1) + (where.start + xi) * (second ? a.o2_ts : a.o1_ts) +
-                             xhead * (second ? a.o2_hs : a.o1_hs);
         constexpr int kCols = KEYS ? DP / 2 : DP / 4;
         const int col0 = (KEYS ? quarter & 1 : quarter) * kCols;
         const uint32_t acc = tmem + lanes + (second ? kCol2 : kCol1) + col0;
+        uint32_t v[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j) {
             uint32_t o[16];
             __syncwarp();
-            if (ok && n_tiles > 0) {
+            if (n_tiles > 0) {
                 tmem_ld16(acc + 16 * j, o);
                 tc_wait_ld16(o);
             }
-            if (!ok || !mine_row) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = col0 + 16 * j + 8 * e;
-                if (col >= a.d) continue;
-                uint32_t q[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    q[f] = in_use ? pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * mult,
-                                              __uint_as_float(o[8 * e + 2 * f + 1]) * mult) : 0u;
-                *reinterpret_cast<uint4 *>(dst + col) = make_uint4(q[0], q[1], q[2], q[3]);
-            }
+            for (int e = 0; e < 8; ++e)
+                v[8 * j + e] = in_use ? pack_bf16(__uint_as_float(o[2 * e]) * mult, __uint_as_float(o[2 * e + 1]) * mult) : 0u;
         }
+        // X is no longer read: its tiles become the warps' scratch
+        __nv_bfloat16 *out = second ? a.out2 : a.out1;
+        const int64_t ts = second ? a.o2_ts : a.o1_ts, hs = second ? a.o2_hs : a.o1_hs;
+        const int row0 = first + 32 * (warp & 3);
+        if (ok && live)
+            warp_store_rows<kCols>(base + warp * (64 * kCols), v, a.d - col0, [&](int r) {
+                if (row0 + r >= len) return static_cast<__nv_bfloat16 *>(nullptr);
+                return out + (where.start + row0 + r) * ts + xhead * hs + col0;
+            });
         tc_fence_before();
     }
     __syncthreads();

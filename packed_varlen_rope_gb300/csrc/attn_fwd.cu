@@ -59,7 +59,7 @@ struct FwdArgs {
     int32_t max_pages, page_size, n_pages, box_rows;
     int32_t n_tokens, n_seqs, hq, hkv, group, tile_tokens, d, causal;   // tile_tokens: of one row tile
     int32_t n_slots, splits;
-    FastDiv div_cta;                    // by the CTA's tokens
+    FastDiv div_cta, div_group;         // by the CTA's tokens, by group
     float scale;
 };
 
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             n[x] = live && last >= first + x * a.tile_tokens ? (limit(last) + kKeys - 1) / kKeys : 0;
         }
         const int all = max(n[0], n[1]);
-        const int chunk = (all + a.splits - 1) / a.splits;
+        const int chunk = a.splits == 1 ? all : (all + a.splits - 1) / a.splits;
         lo_tile = split * chunk;
         const int hi = min(all, lo_tile + chunk);
 #pragma unroll
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const uint32_t t_p = tmem + lanes + kColS + x * kKeys + half * 32;
         const uint32_t t_o = tmem + lanes + kColO + x * DP + half * (DP / 2);
         const int tok0 = first + x * a.tile_tokens;                    // of the sample
-        const int i_tok = tok0 + row / a.group;
+        const int i_tok = tok0 + static_cast<int>(fast_div(row, a.div_group));
         const bool mine = live && row < a.group * a.tile_tokens && i_tok < len;
         const int lim = mine ? limit(i_tok) : 0;
         // from the CTA's first key on: keys that every row of the tile sees, and that this
@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 high = fmaxf(high, highest(s));
                 if (folded) sum += weights(s, p + 16 * h, mc);
             }
+            // rows that see no key may hold anything: they take no part in the warp's decisions
+            if (lim == 0) high = -INFINITY;
             s_swap[i & 1][x][half][row] = high;
             // past the barrier both warps have read their scores, and P may overwrite them
             tc_fence_before();
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         // rows in use see whole are not masked, so such rows may have summed anything)
         if (lim == 0) l = 0.0f;
         const int tok = where.start + i_tok;
-        const int head = kvh * a.group + row % a.group;
+        const int head = kvh * a.group + (row - static_cast<int>(fast_div(row, a.div_group)) * a.group);
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const bool joined = PAGED && a.splits > 1;
         const int64_t at = static_cast<int64_t>(tok) * a.hq + head;
@@ -453,40 +455,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l > 0.0f ? m * a.scale + kLn2 * log2f(l) : -INFINITY;
             }
         }
+        const int col0 = half * (DP / 2);
+        if (joined) {
 #pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-            const int col = half * (DP / 2) + 32 * j;
-            uint32_t o[32];
-            __syncwarp();
-            if (count[x] > 0) {
-                tmem_ld32(t_o + 32 * j, o);
-                tc_wait_ld(o);
-            }
-            if (!ok || !mine) continue;
-            if (l == 0.0f) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0;
-            }
-            if (joined) {
+            for (int j = 0; j < DP / 64; ++j) {
+                const int col = col0 + 32 * j;
+                uint32_t o[32];
+                __syncwarp();
+                if (count[x] > 0) {
+                    tmem_ld32(t_o + 32 * j, o);
+                    tc_wait_ld(o);
+                }
+                if (!ok || !mine || !(l > 0.0f)) continue;
                 float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(split) * a.n_tokens * a.hq + at) *
                                                                         a.d + col);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (col + 4 * e < a.d && l > 0.0f)
+                    if (col + 4 * e < a.d)
                         dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-            } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(a.out + tok * a.out_ts + head * a.out_hs + col);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (col + 8 * e >= a.d) continue;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        w[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-                    dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
             }
+        } else {
+            uint32_t w[DP / 4];
+#pragma unroll
+            for (int j = 0; j < DP / 64; ++j) {
+                uint32_t o[32];
+                __syncwarp();
+                if (count[x] > 0) {
+                    tmem_ld32(t_o + 32 * j, o);
+                    tc_wait_ld(o);
+                }
+                if (count[x] == 0 || l == 0.0f) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    w[16 * j + e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            }
+            // Q is no longer read: its tile becomes the scratch of the eight warps
+            const int row0 = 32 * (warp & 3);
+            if (ok && live)
+                warp_store_rows<DP / 2>(base + x * Sh::kTileBytes + (warp & 7) * (32 * DP), w, a.d - col0, [&](int r) {
+                    const int tok_in = static_cast<int>(fast_div(row0 + r, a.div_group));
+                    const int to = tok0 + tok_in;
+                    if (row0 + r >= a.group * a.tile_tokens || to >= len) return static_cast<__nv_bfloat16 *>(nullptr);
+                    return a.out + (where.start + to) * a.out_ts +
+                           (kvh * a.group + row0 + r - tok_in * a.group) * a.out_hs + col0;
+                });
         }
         tc_fence_before();
     }
@@ -609,6 +625,7 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, 
     a.causal = p.causal;
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, 2 * tile);
     a.splits = splits;
+    a.div_group = make_fastdiv(static_cast<uint32_t>(p.group));
     a.div_cta = make_fastdiv(static_cast<uint32_t>(2 * tile));
     a.scale = p.scale;
     const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;

@@ -313,6 +313,34 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
+// A warp's 32 rows of COLS bf16, one row a lane, to global memory with whole lines a store: a
+// row a lane would touch 32 lines with every 16 bytes a lane, and that alone took 4,000 cycles
+// of an attention CTA.  `scratch`: 64 * COLS bytes of shared memory of the warp's own.
+// to(row) is where the row's columns go, or NULL; only the first `cols` of them are written.
+template <int COLS, typename To>
+__device__ __forceinline__ void warp_store_rows(uint32_t scratch, const uint32_t (&v)[COLS / 2], int cols, To to)
+{
+    constexpr int kChunks = COLS / 8;                        // of 16 bytes
+    const int lane = threadIdx.x & 31;
+    auto at = [&](int row, int chunk) {                      // spread over the banks
+        return scratch + row * (2 * COLS) + ((chunk ^ ((row / (8 / kChunks)) & (kChunks - 1))) << 4);
+    };
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, c)), "r"(v[4 * c]), "r"(v[4 * c + 1]),
+                     "r"(v[4 * c + 2]), "r"(v[4 * c + 3]) : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int index = 32 * i + lane, row = index / kChunks, chunk = index % kChunks;
+        uint4 x;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(row, chunk)));
+        __nv_bfloat16 *dst = to(row);
+        if (dst != nullptr && 8 * chunk < cols) *reinterpret_cast<uint4 *>(dst + 8 * chunk) = x;
+    }
+}
+
 // The sample a tile slot belongs to.  The token axis [0, T) is cut at cu[0..n] into n + 2
 // stretches (what lies before the pack, the samples, what lies after it), and stretch s
 // owns the slots from floor(start_s / tile) + s on: room for every one of its tiles,
