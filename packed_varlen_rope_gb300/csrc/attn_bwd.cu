@@ -161,7 +161,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     constexpr uint32_t kColS = 0, kColP = 128, kCol1 = KEYS ? 256 : 384, kCol2 = 256 + DP;
     constexpr uint32_t kNextP = KEYS ? 0 : 128;
 
-    if (warp >= kLoadWarp) {
+    if (n_tiles == 0) {
+        // rows outside the pack or not in use: zeros, without any of the rest
+        const int n_rows = live ? min(kTile, len - first) : 0;
+        for (int i = threadIdx.x; i < n_rows * (DP / 8); i += kThreads) {
+            const int64_t tok = where.start + first + i / (DP / 8);
+            const int col = 8 * (i % (DP / 8));
+            if (col >= a.d) continue;
+            *reinterpret_cast<uint4 *>(a.out1 + tok * a.o1_ts + xhead * a.o1_hs + col) = make_uint4(0, 0, 0, 0);
+            if (KEYS) *reinterpret_cast<uint4 *>(a.out2 + tok * a.o2_ts + xhead * a.o2_hs + col) = make_uint4(0, 0, 0, 0);
+        }
+    } else if (warp >= kLoadWarp) {
         // ------------------------------------------------------------ loads
         const int which = warp - kLoadWarp;
         if (which == 0 && lane == 0 && n_tiles > 0) {
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         }
         __syncwarp();
     }
-    if (warp < kMmaWarp) {
+    if (n_tiles > 0 && warp < kMmaWarp) {
         // ---------------------------------------------------------- softmax
         // a row of X is four threads', 32 of a tile's columns each
         const int quarter = warp >> 2;

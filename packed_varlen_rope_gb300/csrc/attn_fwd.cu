@@ -171,7 +171,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
     constexpr uint32_t kColS = 0, kColO = 256;
 
-    if (warp == kLoadWarp) {
+    if (n_tiles == 0) {
+        // no row of the CTA sees a key (padding, or keys of other splits): zeros, without any
+        // of the rest
+        const bool joined = PAGED && a.splits > 1;
+        const int n_rows = live ? min(cta_tokens, len - first) * a.group : 0;
+        for (int i = threadIdx.x; i < n_rows * (DP / 8); i += kThreads) {
+            const int r = i / (DP / 8), col = 8 * (i % (DP / 8));
+            const int tok_in = static_cast<int>(fast_div(r, a.div_group));
+            const int64_t tok = where.start + first + tok_in;
+            const int head = kvh * a.group + r - tok_in * a.group;
+            if (!joined && col < a.d)
+                *reinterpret_cast<uint4 *>(a.out + tok * a.out_ts + head * a.out_hs + col) = make_uint4(0, 0, 0, 0);
+            if (col == 0) {
+                if (joined) a.part_lse[(static_cast<int64_t>(split) * a.n_tokens + tok) * a.hq + head] = -INFINITY;
+                else if (a.lse != nullptr) a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = -INFINITY;
+            }
+        }
+    } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) {
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         __syncwarp();
     }
-    if (warp < kMmaWarp) {
+    if (n_tiles > 0 && warp < kMmaWarp) {
         // ---------------------------------------------------------- softmax
         // a row is two threads', 64 of a tile's keys each
         const int x = warp >> 3, half = (warp >> 2) & 1;

@@ -331,7 +331,7 @@ __device__ __forceinline__ void warp_store_rows(uint32_t scratch, const uint32_t
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, c)), "r"(v[4 * c]), "r"(v[4 * c + 1]),
                      "r"(v[4 * c + 2]), "r"(v[4 * c + 3]) : "memory");
     __syncwarp();
-#pragma unroll
+#pragma unroll 1                                             // run once a CTA: short code, few instruction fetches
     for (int i = 0; i < kChunks; ++i) {
         const int index = 32 * i + lane, row = index / kChunks, chunk = index % kChunks;
         uint4 x;
