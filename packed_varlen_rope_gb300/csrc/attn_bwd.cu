@@ -131,10 +131,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    // the CTAs of a cluster share the streamed tiles of one tile of keys
+    const int ranks = KEYS ? static_cast<int>(cluster_size()) : 1, rank = KEYS ? static_cast<int>(cluster_rank()) : 0;
+    const int unit = static_cast<int>(blockIdx.x) / ranks;
     const int heads = KEYS ? a.hkv : a.hq;
-    const int xhead = blockIdx.x % heads;
+    const int xhead = unit % heads;
     // with a causal mask early keys and late queries have the most work: they go first
-    const int order = static_cast<int>(blockIdx.x) / heads;
+    const int order = unit / heads;
     const int slot = KEYS ? order : a.n_slots - 1 - order;
     if (warp == 0) {
         const TileSlot f = find_slot(a.cu, a.used, a.n_seqs, a.n_tokens, a.div_tile, slot);
@@ -156,14 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         y_hi = ((!KEYS && a.causal ? min(rows, first + kTile) : rows) + kTile - 1) / kTile;
     }
     const int per_pass = y_hi - y_lo;
-    const int n_tiles = per_pass * (KEYS ? a.group : 1);
+    const int n_all = per_pass * (KEYS ? a.group : 1);       // the cluster's
+    int n_tiles = n_all, head0 = 0, y0_first = y_lo;
+    if (KEYS && ranks > 1 && n_all > 0) {
+        const int from = static_cast<int>(static_cast<int64_t>(n_all) * rank / ranks);
+        n_tiles = static_cast<int>(static_cast<int64_t>(n_all) * (rank + 1) / ranks) - from;
+        head0 = from / per_pass;
+        y0_first = y_lo + from - head0 * per_pass;
+    }
     // tensor memory; for queries dP is there twice
     constexpr uint32_t kColS = 0, kColP = 128, kCol1 = KEYS ? 256 : 384, kCol2 = 256 + DP;
     constexpr uint32_t kNextP = KEYS ? 0 : 128;
 
-    if (n_tiles == 0) {
+    bool ok_softmax = true;
+    if (n_all == 0) {
         // rows outside the pack or not in use: zeros, without any of the rest
-        const int n_rows = live ? min(kTile, len - first) : 0;
+        const int n_rows = live && rank == 0 ? min(kTile, len - first) : 0;
         for (int i = threadIdx.x; i < n_rows * (DP / 8); i += kThreads) {
             const int64_t tok = where.start + first + i / (DP / 8);
             const int col = 8 * (i % (DP / 8));
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         }
         const CUtensorMap *map = which == 0 ? &a.y1 : &a.y2;
         const int places = which == 0 ? Sh::kY1 : Sh::kY2, place0 = which == 0 ? 0 : Sh::kY1;
-        int g = 0, y = y_lo, at = 0, before = 0, issued = 0;
+        int g = head0, y = y0_first, at = 0, before = 0, issued = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const uint32_t bar = y_full + 8 * (place0 + at);
             const int yhead = KEYS ? xhead * a.group + g : xhead / a.group;
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // ------ the arrival of Y: the products wait for it and for P at one barrier, as every
         // wait costs a few hundred cycles while the tensor core reads shared memory
         bool ok = n_tiles > 0 && warp_wait(x_full, 0, &s_abort, &g_attn_bwd_fault);
-        int y = y_lo;
+        int y = y0_first;
         for (int t = 0; ok && t <= n_tiles; ++t) {
             if (t < n_tiles) {
                 ok = warp_wait(y_full + 8 * place(t, 0), turn(t, 0) & 1, &s_abort, &g_attn_bwd_fault) &&
@@ -347,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // the rows are in one tile, D is taken from them instead, D = sum_j p dP, and kept for
         // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).
         const bool single = !KEYS && n_tiles == 1;
-        bool ok = true;
-        int y = y_lo;
+        bool &ok = ok_softmax;
+        int y = y0_first;
         for (int t = 0; t < n_tiles; ++t) {
             const int y0 = y * kTile + 32 * quarter;                   // this thread's first column
             if (++y == y_hi) y = y_lo;
@@ -442,13 +453,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             ok = warp_wait(done, 0, &s_abort, &g_attn_bwd_fault);
             tc_fence_after();
         }
+    }
+    // A cluster's partial dk and dv: the 32-row slices of quarter q go to CTA q * ranks / 4,
+    // which adds them in the order of the CTAs.  Y's place takes them, [from][slice][column / 4][row][4].
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool second = KEYS && quarter >= 2;
+    constexpr int kCols = KEYS ? DP / 2 : DP / 4;
+    const int col0 = (KEYS ? quarter & 1 : quarter) * kCols;
+    const uint32_t acc = tmem + lanes + (second ? kCol2 : kCol1) + col0;
+    const int owner = KEYS ? quarter * ranks / 4 : 0, slices = 4 / ranks;
+    auto part = [&](int from) {
+        return base + Sh::kOffY + static_cast<uint32_t>(((from * slices + quarter % slices) * (kCols / 4)) * kTile + row) * 16;
+    };
+    if (KEYS && ranks > 1 && n_all > 0) {
+        cluster_arrive();
+        cluster_wait();                 // every CTA is through with its tiles
+        if (warp < kMmaWarp && owner != rank) {
+            const uint32_t to = part(rank);
+#pragma unroll 1
+            for (int j = 0; j < kCols / 16; ++j) {
+                uint32_t o[16];
+                if (n_tiles > 0) {
+                    tmem_ld16(acc + 16 * j, o);
+                    tc_wait_ld16(o);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (n_tiles > 0)
+                        x = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                    cluster_store4(to + (4 * j + e) * kTile * 16, owner, x);
+                }
+            }
+            __syncwarp();
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (n_all > 0 && warp < kMmaWarp && owner == rank) {
         // epilogue: dk and dv by two groups each, or a quarter of dq's columns a group
-        const bool in_use = xi < rows && n_tiles > 0;
-        const bool second = KEYS && quarter >= 2;
+        const int xi = first + row;
+        const bool in_use = xi < rows;
         const float mult = second ? 1.0f : a.scale;
-        constexpr int kCols = KEYS ? DP / 2 : DP / 4;
-        const int col0 = (KEYS ? quarter & 1 : quarter) * kCols;
-        const uint32_t acc = tmem + lanes + (second ? kCol2 : kCol1) + col0;
         uint32_t v[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j) {
@@ -457,6 +505,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (n_tiles > 0) {
                 tmem_ld16(acc + 16 * j, o);
                 tc_wait_ld16(o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = 0u;
+            }
+            if (KEYS && ranks > 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 own = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int r = 0; r < ranks; ++r) {
+                        const float4 x = r == rank ? own : smem_load4(part(r) + (4 * j + e) * kTile * 16);
+                        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+                    }
+                    o[4 * e] = __float_as_uint(sum.x);
+                    o[4 * e + 1] = __float_as_uint(sum.y);
+                    o[4 * e + 2] = __float_as_uint(sum.z);
+                    o[4 * e + 3] = __float_as_uint(sum.w);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -466,13 +533,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         __nv_bfloat16 *out = second ? a.out2 : a.out1;
         const int64_t ts = second ? a.o2_ts : a.o1_ts, hs = second ? a.o2_hs : a.o1_hs;
         const int row0 = first + 32 * (warp & 3);
-        if (ok && live)
+        if (ok_softmax && live)
             warp_store_rows<kCols>(base + warp * (64 * kCols), v, a.d - col0, [&](int r) {
                 if (row0 + r >= len) return static_cast<__nv_bfloat16 *>(nullptr);
                 return out + (where.start + row0 + r) * ts + xhead * hs + col0;
             });
-        tc_fence_before();
     }
+    tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
@@ -531,6 +598,19 @@ void plain_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned g
     cfg.numAttrs = 1;
 }
 
+// CTAs that share a tile of keys: up to 4 while all of them fit the SMs at once and each has a
+// few streamed tiles left.  (3,522 tokens, 10/2 heads of 80, 72 tiles of keys: 120 us alone,
+// in pairs 78 us, by four 155 us, as those take more than one round.)
+int key_cluster(const AttnProblem &p, int n_slots)
+{
+    const int64_t ctas = static_cast<int64_t>(n_slots) * p.hkv;
+    const int64_t mean = p.n_seqs > 0 ? p.n_tokens / p.n_seqs : 0;
+    const int64_t tiles = p.group * ((mean + kTile - 1) / kTile);
+    int ranks = 1;
+    while (ranks < 4 && ctas * ranks * 2 <= kSMs && tiles >= 4 * ranks) ranks *= 2;
+    return ranks;
+}
+
 template <int DP, bool KEYS>
 cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
 {
@@ -567,10 +647,17 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, kTile);
     a.scale = p.scale;
     a.div_tile = make_fastdiv(kTile);
+    const int ranks = KEYS ? key_cluster(p, a.n_slots) : 1;
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    plain_config(cfg, attr, static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(xh), kThreads, Shared<DP>::kBytes,
-                 stream);
+    cudaLaunchAttribute attr[2];
+    plain_config(cfg, attr[0], static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(xh * ranks), kThreads,
+                 Shared<DP>::kBytes, stream);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, attn_bwd_kernel<DP, KEYS>, a);
 }
 

@@ -85,41 +85,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Stores at this CTA's shared address `addr`, in CTA `rank` of the cluster.
-__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t rank, float v)
-{
-    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.f32 [p], %2;\n}"
-                 ::"r"(addr), "r"(rank), "f"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_store4(uint32_t addr, uint32_t rank, float4 v)
-{
-    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n"
-                 " st.shared::cluster.v4.f32 [p], {%2, %3, %4, %5};\n}"
-                 ::"r"(addr), "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
-
 template <int DP, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_constant__ DecodeArgs a)
 {

@@ -313,6 +313,42 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
+// Thread-block clusters.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores at this CTA's shared address `addr`, in CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t rank, float v)
+{
+    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.f32 [p], %2;\n}"
+                 ::"r"(addr), "r"(rank), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_store4(uint32_t addr, uint32_t rank, float4 v)
+{
+    asm volatile("{\n .reg .u32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n"
+                 " st.shared::cluster.v4.f32 [p], {%2, %3, %4, %5};\n}"
+                 ::"r"(addr), "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 // A warp's 32 rows of COLS bf16, one row a lane, to global memory with whole lines a store: a
 // row a lane would touch 32 lines with every 16 bytes a lane, and that alone took 4,000 cycles
 // of an attention CTA.  `scratch`: 64 * COLS bytes of shared memory of the warp's own.
