@@ -153,9 +153,10 @@ int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc);
 
 int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Nonzero when a bounded wait inside an attention kernel has run out on the current device
- * since the library was loaded (its results are then invalid).  Synchronises the device:
- * for tests and diagnosis. */
+/* 1 when a bounded wait inside an attention kernel has run out on the current device since
+ * the library was loaded or this was last called (results since then are invalid), else 0;
+ * ROPE_ERR_LAUNCH when the device cannot be read.  Synchronises the device: for tests and
+ * diagnosis. */
 int attn_fault(void);
 
 #ifdef __cplusplus

@@ -64,6 +64,7 @@ class AttnPagedDesc(ctypes.Structure):
 # A decoding step is a few microseconds on the GPU, so the calls below pack a descriptor in one
 # go (the structures above, as ``struct`` formats) and read each tensor's fields once.
 _VIEW = "Pqq"
+_KV_PACK = struct.Struct("@PqqqPqqqqiiii").pack
 _PAGED = "88s"
 _APPEND_PACK = struct.Struct("@" + 4 * _VIEW + _PAGED + "PPPqiiiiqddP").pack
 _VARLEN_PACK = struct.Struct("@" + 4 * _VIEW + "PPPqiiiiif").pack
@@ -136,20 +137,19 @@ class PagedKVCache:
 
     def __init__(self, k_pages, v_pages):
         torch = _torch or _load_torch()
-        ks, vs = k_pages.stride(), v_pages.stride()
-        for name, t, st in (("k_pages", k_pages, ks), ("v_pages", v_pages, vs)):
-            if t.dtype is not torch.bfloat16 or not t.is_cuda or len(st) != 4 or (st[3] != 1 and t.numel()):
-                raise ValueError("%s must be a CUDA bf16 [pages, page_size, kv_heads, head_dim] view with head_dim "
-                                 "contiguous" % name)
-        shape = k_pages.shape
-        if shape != v_pages.shape or k_pages.device != v_pages.device:
+        ks, vs, shape = k_pages.stride(), v_pages.stride(), k_pages.shape
+        bf16 = torch.bfloat16
+        if k_pages.dtype is not bf16 or v_pages.dtype is not bf16 or not k_pages.is_cuda or len(ks) != 4 or \
+                len(vs) != 4 or ((ks[3] != 1 or vs[3] != 1) and k_pages.numel()):
+            raise ValueError("k_pages and v_pages must be CUDA bf16 [pages, page_size, kv_heads, head_dim] views with "
+                             "head_dim contiguous")
+        dev = k_pages.get_device()
+        if shape != v_pages.shape or dev != v_pages.get_device():
             raise ValueError("k_pages and v_pages must share shape and device")
         self.k_pages, self.v_pages = k_pages, v_pages
-        n, page, heads, d = shape
-        self.desc = RopePagedKV(k_pages.data_ptr(), ks[0], ks[1], ks[2], v_pages.data_ptr(), vs[0], vs[1], vs[2],
-                                n, page, heads, d, 0)
-        self._packed = bytes(self.desc)
-        self._dev, self._heads, self._dim = k_pages.get_device(), heads, d
+        self._packed = _KV_PACK(k_pages.data_ptr(), ks[0], ks[1], ks[2], v_pages.data_ptr(), vs[0], vs[1], vs[2],
+                                *shape, 0)
+        self._dev, self._heads, self._dim = dev, shape[2], shape[3]
 
     @property
     def device(self):
@@ -157,19 +157,24 @@ class PagedKVCache:
 
     @property
     def n_pages(self) -> int:
-        return self.desc.n_pages
+        return self.k_pages.shape[0]
 
     @property
     def page_size(self) -> int:
-        return self.desc.page_size
+        return self.k_pages.shape[1]
 
     @property
     def n_kv_heads(self) -> int:
-        return self.desc.n_kv_heads
+        return self._heads
 
     @property
     def head_dim(self) -> int:
-        return self.desc.head_dim
+        return self._dim
+
+    @property
+    def desc(self) -> RopePagedKV:
+        """The C descriptor."""
+        return RopePagedKV.from_buffer_copy(self._packed)
 
 
 def new_paged_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda") -> PagedKVCache:
@@ -384,8 +389,12 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
 
 def attn_fault() -> bool:
     """Whether a bounded wait inside an attention kernel has run out on the current device
-    since the library was loaded.  Synchronises the device."""
-    return load_library().attn_fault() != 0
+    since the library was loaded or this was last called: results since then are invalid.
+    Synchronises the device."""
+    st = load_library().attn_fault()
+    if st < 0:
+        _check("attn_fault", st)
+    return st != 0
 
 
 _Attn = None

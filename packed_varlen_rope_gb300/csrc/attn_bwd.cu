@@ -682,7 +682,7 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream)
 
 int attn_bwd_fault_word(int *word)
 {
-    return cudaMemcpyFromSymbol(word, g_attn_bwd_fault, sizeof *word) == cudaSuccess ? 0 : -1;
+    return take_fault_word(word, g_attn_bwd_fault);
 }
 
 }  // namespace pvr

@@ -470,7 +470,7 @@ cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, flo
 
 int attn_decode_fault_word(int *word)
 {
-    return cudaMemcpyFromSymbol(word, g_attn_decode_fault, sizeof *word) == cudaSuccess ? 0 : -1;
+    return take_fault_word(word, g_attn_decode_fault);
 }
 
 }  // namespace pvr

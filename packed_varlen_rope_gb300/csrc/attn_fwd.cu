@@ -674,7 +674,7 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
 
 int attn_fault_word(int *word)
 {
-    return cudaMemcpyFromSymbol(word, g_attn_fault, sizeof *word) == cudaSuccess ? 0 : -1;
+    return take_fault_word(word, g_attn_fault);
 }
 
 }  // namespace pvr

@@ -17,8 +17,8 @@
 namespace pvr {
 
 // Waits are bounded in time: after kWaitNs the waiter raises the CTA's abort flag and the
-// device's fault word, every other wait that is still open ends when it sees either, and the
-// kernel drains its copies, frees its tensor memory and returns.
+// device's fault word, the CTA's other waits end when they see the flag, and the CTA drains
+// its copies and products, frees its tensor memory and returns.
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr unsigned long long kDrainNs = 20000000ull;
 
@@ -68,7 +68,7 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
     for (int i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
         if (abort_flag != nullptr && *abort_flag != 0) return false;
-        if ((i & 63) == 0 && (now_ns() - start > kWaitNs || *static_cast<volatile int *>(fault) != 0)) break;
+        if ((i & 63) == 0 && now_ns() - start > kWaitNs) break;
     }
     if (abort_flag != nullptr) *abort_flag = 1;
     atomicExch(fault, 1);

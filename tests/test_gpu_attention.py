@@ -450,3 +450,89 @@ def test_paged_workspace_and_stream(dev):
     junk = torch.full((max(need, 16) // 4 + 1,), 7.0, device=dev)
     s.synchronize()
     assert torch.equal(o, o2) and float(junk[0]) == 7.0
+
+
+def test_refusals(dev):
+    """What the binding refuses before the library sees it, and what the library refuses."""
+    m = pr()
+    x = normal((8, 8, 64), 1, dev)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    cu = torch.tensor([0, 8], dtype=torch.int32, device=dev)
+    o, lse = m.attn_varlen_fwd(q, k, v, cu, return_lse=True)
+    for args, kw in (((q.float(), k, v, cu), {}), ((q, k[:4], v, cu), {}), ((q, k, x[:, 5:], cu), {}),
+                     ((q, k, v, cu.long()), {}), ((q, k, v, cu.cpu()), {}), ((q, k, v, cu), dict(out=o[:4])),
+                     ((q, k, v, cu), dict(seq_used=torch.zeros(2, dtype=torch.int32, device=dev))),
+                     ((q.transpose(1, 2), k, v, cu), {})):
+        with pytest.raises(ValueError):
+            m.attn_varlen_fwd(*args, **kw)
+    for args in ((q, q, k, v, o, None, cu), (q[:4], q, k, v, o, lse, cu), (None, q, k, v, o, lse, cu),
+                 (q, q, k, v, o, lse.t(), cu)):
+        with pytest.raises(ValueError):
+            m.attn_varlen_bwd(*args)
+    for kw in (dict(scale=0.0), dict(out=q), dict(scale=float("inf"))):
+        with pytest.raises(m.RopeError):
+            m.attn_varlen_fwd(q, k, v, cu, **kw)
+    with pytest.raises(m.RopeError):                       # 4 query heads do not share 3 key heads
+        m.attn_varlen_fwd(q, x[:, :3].contiguous(), x[:, :3].contiguous(), cu)
+    with pytest.raises(m.RopeError):
+        m.attn_varlen_fwd(*(normal((8, 2, 256), 2, dev) for _ in range(3)), cu)
+    with pytest.raises(m.RopeError):
+        m.attn_varlen_bwd(o, q, k, v, o, lse, cu, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    cache, table, _, _ = make_paged(dev, [8], 16, 2, 64, 3)
+    lens = torch.tensor([8], dtype=torch.int32, device=dev)
+    for args in ((q.float(), cache, table, lens, cu), (q, None, table, lens, cu), (q, cache, table.long(), lens, cu),
+                 (q, cache, table, lens.long(), cu), (q, cache, table, lens, cu.cpu()),
+                 (normal((8, 4, 128), 4, dev), cache, table, lens, cu)):
+        with pytest.raises(ValueError):
+            m.attn_paged(*args)
+
+
+def test_results_do_not_depend_on_what_no_row_sees(dev):
+    """The same bits whatever lies in other samples, past seq_used and in stale cache slots."""
+    m = pr()
+    used = [77, 150, 1]
+    cu = torch.tensor([3, 103, 303, 310], dtype=torch.int32, device=dev)
+    su = torch.tensor(used, dtype=torch.int32, device=dev)
+    inside = torch.zeros(320, dtype=torch.bool, device=dev)
+    for a, n in zip([3, 103, 303], used):
+        inside[a:a + n] = True
+    base = [normal((320, h, 64), 5 + i, dev) for i, h in enumerate((6, 2, 2, 6))]
+    first = None
+    for fill in (0.0, 1e30, float("nan"), float("-inf")):
+        q, k, v, dout = (x.clone() for x in base)
+        for x in (q, k, v, dout):
+            x[~inside] = fill
+        o, lse = m.attn_varlen_fwd(q, k, v, cu, seq_used=su, return_lse=True)
+        now = (o, lse, *m.attn_varlen_bwd(dout, q, k, v, o, lse, cu, seq_used=su))
+        torch.cuda.synchronize()
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, now))
+        first = now
+    for new in (1, 40):
+        first = None
+        qn = normal((new, 6, 64), 9, dev)
+        for fill in (0.0, 1e30, float("nan"), float("inf")):
+            cache, table, _, _ = make_paged(dev, [203], 24, 2, 64, 6, fill=fill)
+            now = m.attn_paged(qn, cache, table, torch.tensor([203], dtype=torch.int32, device=dev),
+                               torch.tensor([0, new], dtype=torch.int32, device=dev))
+            assert first is None or torch.equal(first, now)
+            first = now
+
+
+def test_few_key_tiles_shared_by_a_cluster(dev):
+    """Backward of problems with few tiles of keys and many streamed ones."""
+    check_varlen(dev, [600], 16, 1, 64, True, seed=110)
+    check_varlen(dev, [1100], 8, 1, 128, False, seed=111)
+    check_varlen(dev, [400, 300], 12, 2, 128, True, seed=112, lead=3, tail=1)
+    check_varlen(dev, [500, 0, 260], 40, 1, 80, True, seed=113, used=[499, 0, 200])
+
+
+def test_example_runs(dev):
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, os.path.join(root, "examples", "attention_layer.py")], capture_output=True,
+                         text=True, timeout=300)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert "served in" in out.stdout
