@@ -96,6 +96,7 @@ PagedPlan plan_of(const attn_paged_desc &p)
     a.hq = p.n_q_heads;
     a.hkv = p.cache.n_kv_heads;
     a.group = a.hq / a.hkv;
+    a.d = p.cache.head_dim;
     int64_t keys = static_cast<int64_t>(p.max_pages) * p.cache.page_size;
     if (p.max_kv_len > 0 && p.max_kv_len < keys) keys = p.max_kv_len;
     plan.decode = attn_decode_plan(a, keys);

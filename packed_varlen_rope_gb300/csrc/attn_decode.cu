@@ -13,9 +13,9 @@
 // sequence's keys) through distributed shared memory; only where that leaves SMs idle do
 // further splits join through the workspace in a second launch.
 //
-// Bound by HBM: 4 G operations a byte of cache.  The 128-row tiles of the prompt kernel
-// would do for it too, but their tensor memory, barriers and tile maps cost a decoding
-// step more than its loads.
+// Bound by HBM: G operations a byte of cache (64 sequences of 500-16,000 tokens, 32/8 heads
+// of 128: 325 us for 2.2 GB, 6.77 TB/s, a copy's rate); a short sequence by the chain of its
+// dependent steps (one of 4,098 tokens 10.7 us, of which 2.5 us of loads).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -405,23 +405,33 @@ cudaError_t launch(const DecodeArgs &a, int cluster, int slots, cudaStream_t str
 DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv)
 {
     DecodePlan plan;
-    // few rows a sequence, on average; longer stretches still come out right, a tile at a time
-    plan.use = p.group <= kRows && static_cast<int64_t>(p.n_tokens) * p.group <= 2 * kRows * static_cast<int64_t>(p.n_seqs);
+    // at most one tile of rows a sequence, on average (longer stretches still come out right, a
+    // tile at a time).  16 sequences, 4,096 tokens cached, 32/8 heads of 128, this kernel and the
+    // 128-row one: 4 rows 50 and 55 us, 16 rows 53 and 56 us, 32 rows 87 and 55 us.
+    plan.use = p.group <= kRows && static_cast<int64_t>(p.n_tokens) * p.group <= kRows * static_cast<int64_t>(p.n_seqs);
     if (!plan.use) return plan;
     plan.slots = slot_count(p.n_tokens, p.n_seqs, kRows / p.group);
     // live CTAs of one rank: a sequence with new tokens fills at least one slot
     const int64_t ctas = static_cast<int64_t>(p.n_seqs < p.n_tokens ? p.n_seqs : p.n_tokens) * p.hkv;
     const int64_t chunks = (max_kv + kKeys - 1) / kKeys;
-    // a cluster of up to 8 CTAs a sequence: until the GPU is full, or, where sequences are long
-    // and may be uneven, until there are several rounds of CTAs
+    // CTAs of a cluster share a sequence's keys: while the SMs hold all CTAs at once (a CTA an
+    // SM; two of half the size with head_dim up to 64), and so that none has more than about
+    // 5,000 keys, as lengths are uneven.  32/8 heads of 128, one token each, by 1, 2, 4, 8 CTAs:
+    // 1 x 4,096 keys 17, 17, 15, 11 us; 16 x 1,024 14, 14, 19, 29; 64 x 4,096 156, 173, 178, 210;
+    // 64 x 500-16,000 389, 343, 321, -.
+    const int64_t room = p.d <= 64 ? 2 * kSMs : kSMs;
+    const int most = chunks > 512 ? 4 : kMaxCluster;      // clusters of 8 leave SMs of a GPC idle
     plan.cluster = 1;
-    while (plan.cluster < kMaxCluster && chunks > 16 * plan.cluster &&
-           (ctas * plan.cluster < 2 * kSMs || (chunks > 128 * plan.cluster && ctas * plan.cluster < 8 * kSMs)))
+    while (plan.cluster < most && chunks > 16 * plan.cluster &&
+           (ctas * plan.cluster * 2 <= room || chunks > 320 * plan.cluster))
         plan.cluster *= 2;
+    // and a second launch joins further splits of few long sequences (1 x 32,768 keys: 33 us as
+    // 4 splits of 4, 50 us as 2 of 8)
     plan.splits = 1;
     while (ctas * plan.cluster * plan.splits * 2 <= kSMs && chunks > 128 * plan.cluster * plan.splits && plan.splits < 64)
         plan.splits *= 2;
-    // one CTA an SM at most: eight warps each keep more loads in flight
+    // with a CTA an SM at most, eight warps each keep more loads in flight (1 x 4,096 keys:
+    // 10.7 us, 12.7 with four)
     plan.warps = ctas * plan.cluster * plan.splits <= kSMs ? 8 : 4;
     plan.use = static_cast<int64_t>(plan.slots) * p.hkv * plan.cluster * plan.splits <= INT32_MAX;
     return plan;
