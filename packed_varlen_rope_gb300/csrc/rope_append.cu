@@ -4,8 +4,9 @@
 // Q and K rows are rotated by the token's position in its sequence with the arithmetic of
 // the rotation kernel (y = x*cos + rotate_half(x)*sin, identical bits), V rows are copied;
 // Q goes back to where it was or to q_out, K and V to their page.  Every element is read
-// once and written once, about half a flop a byte: the bound is HBM for prompts (16,015 tokens
-// of 64/8 heads of 128: 109 us, 6.0 TB/s, 0.89 of a copy's rate) and the
+// once and written once, about half a flop a byte: the bound is HBM for prompts (16,384 tokens
+// of 64/8 heads of 128: 111 us, 6.05 TB/s, 104 us with a cos/sin cache; of 32/8 heads 68 and
+// 63 us), the evaluation of cos and sin where heads are few (8/2 heads: 3.7 TB/s), and the
 // chain of dependent loads (sequence, cache length, page) for a decoding step.  Against
 // that chain cu_seqlens and kv_lens are staged in one round of loads, the page lookup
 // overlaps the evaluation of cos and sin, and the first rows are loaded before any of it.
@@ -26,9 +27,9 @@ namespace {
 using namespace pvr;
 
 constexpr int kThreads = 128;
-// 16-byte pair units in flight per thread: with 5 a token of 80 heads of 128 is one batch
-// (16,015 tokens of them 108.7 us; 110.2 with 3, 111.2 with 4, 5.2-5.4 us a decoding step)
-constexpr int kUnits = 5;
+// 16-byte pair units in flight per thread.  16,384 tokens of 48 and of 80 heads of 128: 68 and
+// 111 us; with 2 71 and 110 us, with 5 84 and 110 us (fewer resident CTAs).
+constexpr int kUnits = 3;
 constexpr int kMaxTile = 16;            // tokens per tile
 constexpr int kMaxStaged = 256;         // sequences whose cu_seqlens and kv_lens are staged
 
