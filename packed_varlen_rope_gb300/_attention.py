@@ -71,13 +71,17 @@ _VARLEN_PACK = struct.Struct("@" + 4 * _VIEW + "PPPqiiiiif").pack
 _GRADS_PACK = struct.Struct("@" + 4 * _VIEW).pack
 _PAGED_PACK = struct.Struct("@" + 2 * _VIEW + _PAGED + "PPPqqqiiiifi").pack
 
-_torch = None
+_torch = _bf16 = _i32t = _f32t = _raw_stream = _current_device = None
 
 
 def _load_torch():
-    global _torch
+    """torch, imported at the first call, and what every call needs of it."""
+    global _torch, _bf16, _i32t, _f32t, _raw_stream, _current_device
     import torch
 
+    _bf16, _i32t, _f32t = torch.bfloat16, torch.int32, torch.float32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None)
     _torch = torch
     return torch
 
@@ -85,14 +89,14 @@ def _load_torch():
 def _view(t, name: str):
     """(pointer, token stride, head stride) of a bf16 CUDA [tokens, heads, head_dim] view."""
     st = t.stride()
-    if len(st) != 3 or st[2] != 1 or t.dtype is not _torch.bfloat16 or not t.is_cuda:
+    if len(st) != 3 or st[2] != 1 or t.dtype is not _bf16 or not t.is_cuda:
         raise ValueError("%s must be a CUDA bf16 [tokens, heads, head_dim] view with head_dim contiguous" % name)
     return t.data_ptr(), st[0], st[1]
 
 
 def _int32(t, dev: int, n: int, what: str) -> int:
     """Pointer of a contiguous int32 [n] tensor on CUDA device ``dev``."""
-    if t.dtype is not _torch.int32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not _i32t or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of %d values on the device of q" % (what, n))
     return t.data_ptr()
 
@@ -100,12 +104,11 @@ def _int32(t, dev: int, n: int, what: str) -> int:
 def _launch(fn, name: str, dev: int, stream, *args) -> None:
     """Call an entry point with device ``dev`` current, on ``stream`` (a torch stream or an int)
     or torch's current one of that device."""
-    c = _torch._C
     if stream is None:
-        stream = c._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if c._cuda_getDevice() == dev:
+    if _current_device() == dev:
         st = fn(*args, stream)
     else:
         with _torch.cuda.device(dev):
@@ -136,10 +139,9 @@ class PagedKVCache:
     two may be the halves of one pool).  page_size is a multiple of 8."""
 
     def __init__(self, k_pages, v_pages):
-        torch = _torch or _load_torch()
+        _torch or _load_torch()
         ks, vs, shape = k_pages.stride(), v_pages.stride(), k_pages.shape
-        bf16 = torch.bfloat16
-        if k_pages.dtype is not bf16 or v_pages.dtype is not bf16 or not k_pages.is_cuda or len(ks) != 4 or \
+        if k_pages.dtype is not _bf16 or v_pages.dtype is not _bf16 or not k_pages.is_cuda or len(ks) != 4 or \
                 len(vs) != 4 or ((ks[3] != 1 or vs[3] != 1) and k_pages.numel()):
             raise ValueError("k_pages and v_pages must be CUDA bf16 [pages, page_size, kv_heads, head_dim] views with "
                              "head_dim contiguous")
@@ -198,7 +200,7 @@ def _tables(cache, dev: int, page_table, kv_lens, cu_seqlens):
     cu = _int32(cu_seqlens, dev, n + 1, "cu_seqlens")
     kv = _int32(kv_lens, dev, n, "kv_lens")
     st, shape = page_table.stride(), page_table.shape
-    if page_table.dtype is not _torch.int32 or page_table.get_device() != dev or len(st) != 2 or shape[0] != n or \
+    if page_table.dtype is not _i32t or page_table.get_device() != dev or len(st) != 2 or shape[0] != n or \
             (st[1] != 1 and shape[1] > 1):
         raise ValueError("page_table must be an int32 [n_seqs, max_pages] tensor with contiguous rows on the "
                          "device of q")
@@ -317,7 +319,7 @@ def _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used):
         raise ValueError("out must have the shape and device of q")
     lp = 0
     if lse is not None:
-        if lse.dtype is not _torch.float32 or lse.get_device() != dev or tuple(lse.shape) != (hq, T) or \
+        if lse.dtype is not _f32t or lse.get_device() != dev or tuple(lse.shape) != (hq, T) or \
                 not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [heads, tokens] tensor on the device of q")
         lp = lse.data_ptr()
