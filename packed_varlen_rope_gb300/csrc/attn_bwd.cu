@@ -604,16 +604,28 @@ void plain_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned g
     cfg.numAttrs = 1;
 }
 
-// CTAs that share a tile of keys: up to 4 while all of them fit the SMs at once and each has a
-// few streamed tiles left.  (3,522 tokens, 10/2 heads of 80, 72 tiles of keys: 120 us alone,
-// in pairs 78 us, by four 155 us, as those take more than one round.)
-int key_cluster(const AttnProblem &p, int n_slots)
+// CTAs that share a tile of keys, up to 4.  While all fit the SMs at once, sharing pays from a
+// few streamed tiles each on.  Causal tiles of keys are uneven, so that sharing long ones pays
+// up to two and a half rounds as well; even ones would only wait for a second round.  CTAs are
+// counted by the tiles that samples of any lengths fill on average (slots may stay empty).
+// The whole backward by one, two and four a tile, heads of 128 unless stated, causal:
+//   one round   500 tokens, 32/8 heads 40.5, 35.5, 33.9 us; 2,000, 8/2 heads 123, 83, 66;
+//               8 x 128, 32/8 heads 32, 38, 58 (four tiles each: not shared)
+//   more        2,048, 32/8 heads 159, 130, 170; 4,000, 8/2 heads of 64 201, 123, 92;
+//               4 x 512, 64/8 heads 127, 134, 164; 4,096, 32/8 heads 379, 393, 482 (not shared)
+//   both directions: 3,522 tokens, 10/2 heads of 80 185, 131, 132; 3 x 900, 12/4 heads of 80
+//               77, 93, 108 (not shared)
+int key_cluster(const AttnProblem &p)
 {
-    const int64_t ctas = static_cast<int64_t>(n_slots) * p.hkv;
-    const int64_t mean = p.n_seqs > 0 ? p.n_tokens / p.n_seqs : 0;
-    const int64_t tiles = p.group * ((mean + kTile - 1) / kTile);
+    const int64_t n = p.n_seqs > 0 ? p.n_seqs : 1;
+    const int64_t ctas = (p.n_tokens + n * (kTile / 2) + kTile - 1) / kTile * p.hkv;
+    const int64_t tiles = p.group * ((p.n_tokens / n + kTile - 1) / kTile);
+    const auto pays = [&](int ranks) {
+        if (ctas * ranks <= kSMs) return tiles >= 4 * ranks;
+        return p.causal && 2 * ctas * ranks <= 5 * kSMs && tiles > 16 * ranks;
+    };
     int ranks = 1;
-    while (ranks < 4 && ctas * ranks * 2 <= kSMs && tiles >= 4 * ranks) ranks *= 2;
+    while (ranks < 4 && pays(2 * ranks)) ranks *= 2;
     return ranks;
 }
 
@@ -653,7 +665,7 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, kTile);
     a.scale = p.scale;
     a.div_tile = make_fastdiv(kTile);
-    const int ranks = KEYS ? key_cluster(p, a.n_slots) : 1;
+    const int ranks = KEYS ? key_cluster(p) : 1;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     plain_config(cfg, attr[0], static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(xh * ranks), kThreads,

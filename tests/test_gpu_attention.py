@@ -526,6 +526,13 @@ def test_few_key_tiles_shared_by_a_cluster(dev):
     check_varlen(dev, [500, 0, 260], 40, 1, 80, True, seed=113, used=[499, 0, 200])
 
 
+def test_key_tiles_shared_over_two_rounds(dev):
+    """More CTAs than SMs: causal samples of many tiles in pairs and by four, uneven and long."""
+    check_varlen(dev, [1500], 32, 8, 128, True, seed=114)
+    check_varlen(dev, [4000], 8, 2, 64, True, seed=115)
+    check_varlen(dev, [1, 3900, 2, 3301], 8, 1, 80, True, seed=116, used=[1, 3000, 0, 3301], lead=1, tail=2)
+
+
 def test_example_runs(dev):
     import os
     import subprocess
