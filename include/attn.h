@@ -77,8 +77,9 @@ typedef struct attn_varlen_desc {
                                       forward: written, or NULL; backward: read        */
     const int32_t *cu_seqlens;
     const int32_t *seq_used;       /* or NULL                                          */
-    int64_t total_tokens;          /* <= 2^24                                          */
-    int32_t n_seqs;
+    int64_t total_tokens;          /* <= 2^24; below 2^31 times n_q_heads              */
+    int32_t n_seqs;                /* (total_tokens / 128 + n_seqs + 2) * n_q_heads is
+                                      below 2^31 too, else ROPE_ERR_UNSUPPORTED        */
     int32_t n_q_heads;
     int32_t n_kv_heads;
     int32_t head_dim;
@@ -140,7 +141,7 @@ typedef struct attn_paged_desc {
     int64_t total_tokens;          /* new tokens, <= 2^24                              */
     int64_t max_kv_len;
     int32_t max_pages;
-    int32_t n_seqs;
+    int32_t n_seqs;                /* limits as for attn_varlen_desc                   */
     int32_t n_q_heads;
     int32_t causal;
     float scale;

@@ -23,6 +23,8 @@ int check_heads(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, f
     if (d < 16 || d > kMaxAttnDim || d % 16 != 0) return ROPE_ERR_HEAD_DIM;
     // (token, head) rows are counted in 32 bits
     if (hq / hkv > kMaxGroup || T > kMaxTokens || T * hq > INT32_MAX) return ROPE_ERR_UNSUPPORTED;
+    // and so are a launch's CTAs: a head's tiles of 128 rows, and a slot more for every sequence
+    if ((T / 128 + n_seqs + 2) * hq > INT32_MAX) return ROPE_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return ROPE_ERR_THETA;
     return ROPE_OK;
 }

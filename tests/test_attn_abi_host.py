@@ -232,6 +232,17 @@ def test_paged_refusals(lib, kw, want):
     assert lib.attn_paged(ctypes.byref(paged(**kw)), None, 1 << 30, None) == want
 
 
+def test_more_tiles_than_a_launch_counts(lib):
+    """Tile slots times heads past 2^31: every sequence, empty or not, adds a slot."""
+    ref, n = ctypes.byref, 1 << 24
+    a = varlen(hq=256, hkv=256, n_seqs=n)
+    assert lib.attn_varlen_fwd(ref(a), None) == ERR_UNSUPPORTED
+    assert lib.attn_varlen_bwd(ref(a), ref(grads(hq=256, hkv=256)), BASE + (1 << 38), 1 << 20, None) == ERR_UNSUPPORTED
+    p = paged(dict(heads=256), hq=256, n_seqs=n)
+    assert lib.attn_paged(ref(p), BASE + (1 << 38), 1 << 40, None) == ERR_UNSUPPORTED
+    assert lib.attn_paged_workspace_bytes(ref(p)) == ERR_UNSUPPORTED
+
+
 def test_paged_head_dims(lib):
     """The cache holds head_dim up to 256; attention takes up to 128."""
     for d, want in ((144, ERR_HEAD_DIM), (256, ERR_HEAD_DIM), (20, ERR_HEAD_DIM)):
