@@ -77,7 +77,7 @@ typedef struct attn_varlen_desc {
                                       forward: written, or NULL; backward: read        */
     const int32_t *cu_seqlens;
     const int32_t *seq_used;       /* or NULL                                          */
-    int64_t total_tokens;          /* <= 2^24; below 2^31 times n_q_heads              */
+    int64_t total_tokens;          /* <= 2^24; times n_q_heads below 2^31              */
     int32_t n_seqs;                /* (total_tokens / 128 + n_seqs + 2) * n_q_heads is
                                       below 2^31 too, else ROPE_ERR_UNSUPPORTED        */
     int32_t n_q_heads;
