@@ -25,7 +25,10 @@
  * the cache beyond a sequence's length may hold anything, NaN and infinities among it, and
  * reach no result.  Within a sample, a key that a causal row does not see has weight zero
  * in it, but its value row is a factor of the product: keys, values and output gradients
- * of a sample's own rows are expected to be finite.
+ * of a sample's own rows are expected to be finite, and queries in the backward.  A NaN or a
+ * score above binary32's range, from a query or from a key that the row sees, makes the
+ * row's out and lse NaN, however the keys are split; scores that are all -infinity weigh
+ * nothing, as if the row saw no key.
  *
  * Layout.  q, k, v, out and the gradients are bf16 views [total_tokens, heads, head_dim],
  * head_dim contiguous, with token and head strides in elements (multiples of 8, pointers

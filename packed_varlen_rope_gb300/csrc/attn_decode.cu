@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
         const int tok_in = static_cast<int>(fast_div(row, a.div_group));
         const int head = kvh * a.group + row - tok_in * a.group;
         const int tok = f.start + first + tok_in;
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        // no weight is sum == 0, not !(sum > 0): a NaN score makes the sum NaN, and that must come out
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
         if (a.splits == 1) {
             *reinterpret_cast<uint2 *>(a.out + tok * a.out_ts + head * a.out_hs + e) =
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
         } else {
             const int64_t to = static_cast<int64_t>(split) * a.n_tokens * a.hq + static_cast<int64_t>(tok) * a.hq + head;
             *reinterpret_cast<float4 *>(a.part_o + to * a.d + e) = x;
-            if (e == 0) a.part_lse[to] = sum > 0.0f ? top * c + log2f(sum) : -INFINITY;
+            if (e == 0) a.part_lse[to] = sum == 0.0f ? -INFINITY : top * c + log2f(sum);
         }
     }
 }

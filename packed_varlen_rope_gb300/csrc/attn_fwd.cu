@@ -466,19 +466,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             l += s_swap[count[x] & 1][x][half ^ 1][row];
         }
         // epilogue: rows outside the pack, and rows that see no key, are zero (tiles that all
-        // rows in use see whole are not masked, so such rows may have summed anything)
+        // rows in use see whole are not masked, so such rows may have summed anything).  No
+        // weight is l == 0, not !(l > 0): a NaN score makes l NaN, and that must come out
         if (lim == 0) l = 0.0f;
         const int tok = where.start + i_tok;
         const int head = kvh * a.group + (row - static_cast<int>(fast_div(row, a.div_group)) * a.group);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const bool joined = PAGED && a.splits > 1;
         const int64_t at = static_cast<int64_t>(tok) * a.hq + head;
         if (ok && mine && half == 0) {
             if (joined) {
                 a.part_lse[static_cast<int64_t>(split) * a.n_tokens * a.hq + at] =
-                    l > 0.0f ? m * c + log2f(l) : -INFINITY;
+                    l == 0.0f ? -INFINITY : m * c + log2f(l);
             } else if (a.lse != nullptr) {
-                a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l > 0.0f ? m * a.scale + kLn2 * log2f(l) : -INFINITY;
+                a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l == 0.0f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
             }
         }
         const int col0 = half * (DP / 2);
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     tmem_ld32(t_o + 32 * j, o);
                     tc_wait_ld(o);
                 }
-                if (!ok || !mine || !(l > 0.0f)) continue;
+                if (!ok || !mine || l == 0.0f) continue;
                 float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(split) * a.n_tokens * a.hq + at) *
                                                                         a.d + col);
 #pragma unroll
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 }
 
 // Joins the partial results of the splits: o = sum_i w_i o_i, w_i = 2^(lse_i - lse).  One
-// warp a row, 4 elements a lane.
+// warp a row, 4 elements a lane.  A part whose lse is -infinity holds no weight and nothing
+// was written for it; one of NaN (which the maximum passes over) makes the row NaN.
 __global__ void __launch_bounds__(128) attn_join_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
                                                         __nv_bfloat16 *__restrict__ out, int64_t out_ts, int64_t out_hs,
                                                         int n_rows, int hq, int d, int splits)
@@ -554,26 +556,24 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const float *__restrict_
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.0f;
-    if (m > -INFINITY) {
-        for (int i0 = 0; i0 < splits; i0 += 32) {
-            const float mine = i0 + lane < splits ? part_lse[static_cast<int64_t>(i0 + lane) * n_rows + row] : -INFINITY;
-            const int n = min(32, splits - i0);
+    for (int i0 = 0; i0 < splits; i0 += 32) {
+        const float mine = i0 + lane < splits ? part_lse[static_cast<int64_t>(i0 + lane) * n_rows + row] : -INFINITY;
+        const int n = min(32, splits - i0);
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float lse = __shfl_sync(0xffffffffu, mine, i);
-                if (lse == -INFINITY) continue;            // nothing was written there
-                const float w = exp2f(lse - m);
-                l += w;
-                if (4 * lane < d) {
-                    const float4 o = *reinterpret_cast<const float4 *>(
-                        part_o + (static_cast<int64_t>(i0 + i) * n_rows + row) * d + 4 * lane);
-                    acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w;
-                }
+        for (int i = 0; i < n; ++i) {
+            const float lse = __shfl_sync(0xffffffffu, mine, i);
+            if (lse == -INFINITY) continue;
+            const float w = exp2f(lse - m);
+            l += w;
+            if (4 * lane < d) {
+                const float4 o = *reinterpret_cast<const float4 *>(
+                    part_o + (static_cast<int64_t>(i0 + i) * n_rows + row) * d + 4 * lane);
+                acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w;
             }
         }
     }
     if (4 * lane >= d) return;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int tok = row / hq, head = row % hq;
     *reinterpret_cast<uint2 *>(out + tok * out_ts + head * out_hs + 4 * lane) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
