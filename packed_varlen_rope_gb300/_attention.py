@@ -207,17 +207,19 @@ def _tables(cache, dev: int, page_table, kv_lens, cu_seqlens):
     return cu, kv, page_table.data_ptr(), st[0], shape[1], n
 
 
-def _keep_for(stream, *tensors):
-    """Tensors allocated here, on torch's current stream, and used on ``stream``: their
-    memory is not given to others before that stream has passed this point."""
-    import torch
-
+def _empty(shape, dtype, device, stream, returned=True):
+    """A new tensor for a call on ``stream`` (a torch stream, an int, or None: torch's current
+    one).  Its memory comes from that stream's pool: a block of another stream's may still be
+    in use by what is queued there.  ``returned``: the caller's current stream will use it too,
+    so its memory is not given to others before that stream has passed the tensor's end."""
     if stream is None:
-        return
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    for t in tensors:
-        if t is not None and t.numel():
-            t.record_stream(s)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    current = _torch.cuda.current_stream(device)
+    with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.numel():
+        t.record_stream(current)
+    return t
 
 
 def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, theta: float, q_out=None,
@@ -261,27 +263,23 @@ def attn_paged(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, causal: 
     caches; 0: what the page table's width allows).  ``workspace``: a CUDA tensor for
     partial results (``attn_paged_workspace_bytes``); allocated through torch unless given.
     Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
-    torch = _torch or _load_torch()
-    made = out is None
-    if made:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _torch or _load_torch()
+    if out is None:
+        out = _empty(q.shape, _bf16, q.device, stream)
     elif out.shape != q.shape or out.get_device() != q.get_device():
         raise ValueError("out must have the shape and device of q")
     desc, dev = _paged_desc(q, out, cache, page_table, kv_lens, cu_seqlens, causal, scale, max_kv_len)
     lib = load_library()
-    own = None
     if workspace is None:
         nbytes = lib.attn_paged_workspace_bytes(desc)
         if nbytes > 0:
-            own = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        ws = None if own is None else own.data_ptr()
+            workspace = _empty(nbytes, _torch.uint8, q.device, stream, returned=False)
+        ws = None if workspace is None else workspace.data_ptr()
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(lib.attn_paged, "attn_paged", dev, stream, desc, ws, nbytes)
-    if stream is not None:
-        _keep_for(stream, own, out if made else None)
     return out
 
 
@@ -341,15 +339,12 @@ def attn_varlen_fwd(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[fl
     ``scale``: 1/sqrt(d) unless given.  Returns out [T, Hq, d] (a new tensor unless given;
     rows that see no key are 0), with ``return_lse`` (out, lse): lse float32 [Hq, T], the
     natural logarithm of each row's sum, which the backward takes."""
-    torch = _torch or _load_torch()
-    made = out is None
-    if made:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if return_lse else None
+    _torch or _load_torch()
+    if out is None:
+        out = _empty(q.shape, _bf16, q.device, stream)
+    lse = _empty((q.shape[1], q.shape[0]), _f32t, q.device, stream) if return_lse else None
     desc, dev = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
     _launch(load_library().attn_varlen_fwd, "attn_varlen_fwd", dev, stream, desc)
-    if stream is not None:
-        _keep_for(stream, out if made else None, lse)
     return (out, lse) if return_lse else out
 
 
@@ -360,17 +355,16 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
     arguments.  dq, dk and dv are written whole (new tensors unless given; rows of no sample
     get 0).  ``workspace``: a CUDA tensor of at least 8 * T * Hq bytes; allocated through
     torch unless given."""
-    torch = _torch or _load_torch()
+    _torch or _load_torch()
     if lse is None:
         raise ValueError("the backward needs the forward's lse (return_lse=True)")
     if dout is None:
         raise ValueError("dout is required")
     desc, dev = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
-    made, grads, packed = [], [], []
+    grads, packed = [], []
     for name, t, like in (("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is None:
-            t = torch.empty(like.shape, dtype=torch.bfloat16, device=q.device)
-            made.append(t)
+            t = _empty(like.shape, _bf16, q.device, stream)
         elif t.shape != like.shape or t.get_device() != dev:
             raise ValueError("%s must have shape %s on %s" % (name, tuple(like.shape), q.device))
         packed += _view(t, name)
@@ -378,14 +372,11 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
     lib = load_library()
     if workspace is None:
         need = lib.attn_varlen_bwd_workspace_bytes(q.shape[0], q.shape[1])
-        workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=q.device)
-        made.append(workspace)
+        workspace = _empty(max(need, 0), _torch.uint8, q.device, stream, returned=False)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
     _launch(lib.attn_varlen_bwd, "attn_varlen_bwd", dev, stream, desc, _GRADS_PACK(*packed), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
-    if stream is not None:
-        _keep_for(stream, *made)
     return tuple(grads[1:])
 
 
