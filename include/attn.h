@@ -159,8 +159,8 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
 
 /* 1 when a bounded wait inside an attention kernel has run out on the current device since
  * the library was loaded or this was last called (results since then are invalid), else 0;
- * ROPE_ERR_LAUNCH when the device cannot be read.  Synchronises the device: for tests and
- * diagnosis. */
+ * ROPE_ERR_LAUNCH when the device cannot be read.  Waits for the work of every stream of the
+ * device first: for tests and diagnosis, and not while a stream is captured. */
 int attn_fault(void);
 
 #ifdef __cplusplus

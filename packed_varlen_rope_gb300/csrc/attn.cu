@@ -2,6 +2,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -225,10 +226,20 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
 
 int attn_fault(void)
 {
-    int fwd = 0, bwd = 0, dec = 0;
-    if (attn_fault_word(&fwd) != 0 || attn_bwd_fault_word(&bwd) != 0 || attn_decode_fault_word(&dec) != 0)
+    static std::atomic<int> reported[64][3];                 // of each device's counts
+    int dev = 0, now[3] = {0, 0, 0};
+    // the copies below wait for the default stream alone, and kernels run on any
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return ROPE_ERR_LAUNCH;
+    if (attn_fault_word(&now[0]) != 0 || attn_bwd_fault_word(&now[1]) != 0 || attn_decode_fault_word(&now[2]) != 0)
         return ROPE_ERR_LAUNCH;
-    return fwd != 0 || bwd != 0 || dec != 0 ? 1 : 0;
+    int raised = 0;
+    for (int i = 0; i < 3; ++i) {
+        std::atomic<int> &known = reported[dev & 63][i];
+        int before = known.load();
+        while (before < now[i] && !known.compare_exchange_weak(before, now[i])) {}
+        if (before < now[i]) raised = 1;
+    }
+    return raised;
 }
 
 }  // extern "C"

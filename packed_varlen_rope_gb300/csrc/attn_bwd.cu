@@ -50,7 +50,7 @@ constexpr int kLoadWarp = 18;              // loads: one warp for X, Y1 and its 
 constexpr int kTile = 128;                 // rows of the resident and of the streamed tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ int g_attn_bwd_fault;           // a bounded wait ran out
+__device__ int g_attn_bwd_fault;           // bounded waits that ran out
 
 struct BwdArgs {
     CUtensorMap x1, x2, y1, y2;
@@ -700,7 +700,7 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream)
 
 int attn_bwd_fault_word(int *word)
 {
-    return take_fault_word(word, g_attn_bwd_fault);
+    return read_fault_word(word, g_attn_bwd_fault);
 }
 
 }  // namespace pvr

@@ -38,7 +38,7 @@ constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 30.0f;          // log2 growth of the maximum that triggers a rescale
 
-__device__ int g_attn_decode_fault;     // a bounded wait ran out
+__device__ int g_attn_decode_fault;     // bounded waits that ran out
 
 struct DecodeArgs {
     CUtensorMap q, k, v;
@@ -483,7 +483,7 @@ cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, flo
 
 int attn_decode_fault_word(int *word)
 {
-    return take_fault_word(word, g_attn_decode_fault);
+    return read_fault_word(word, g_attn_decode_fault);
 }
 
 }  // namespace pvr

@@ -45,7 +45,7 @@
 namespace pvr {
 namespace {
 
-__device__ int g_attn_fault;            // a bounded wait ran out
+__device__ int g_attn_fault;            // bounded waits that ran out
 
 constexpr int kThreads = 640;           // four softmax warpgroups, one for products and loads
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kWatchWarp = 18;
@@ -683,7 +683,7 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
 
 int attn_fault_word(int *word)
 {
-    return take_fault_word(word, g_attn_fault);
+    return read_fault_word(word, g_attn_fault);
 }
 
 }  // namespace pvr

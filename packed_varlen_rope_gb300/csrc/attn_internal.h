@@ -55,7 +55,8 @@ DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv);
 cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream);
 cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
                              cudaStream_t stream);
-// The device's fault word, which is cleared; 0 on success.
+// The kernels' counts of waits that ran out on the current device; 0 on success.  Nothing
+// clears them, so that none is lost between two looks.
 int attn_fault_word(int *word);
 int attn_bwd_fault_word(int *word);
 int attn_decode_fault_word(int *word);
@@ -63,11 +64,9 @@ int attn_decode_fault_word(int *word);
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream);
 
 template <typename Symbol>
-int take_fault_word(int *word, const Symbol &symbol)
+int read_fault_word(int *word, const Symbol &symbol)
 {
-    const int none = 0;
-    if (cudaMemcpyFromSymbol(word, symbol, sizeof *word) != cudaSuccess) return -1;
-    return *word == 0 || cudaMemcpyToSymbol(symbol, &none, sizeof none) == cudaSuccess ? 0 : -1;
+    return cudaMemcpyFromSymbol(word, symbol, sizeof *word) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace pvr

@@ -16,8 +16,8 @@
 
 namespace pvr {
 
-// Waits are bounded in time: after kWaitNs the waiter raises the CTA's abort flag and the
-// device's fault word, the CTA's other waits end when they see the flag, and the CTA drains
+// Waits are bounded in time: after kWaitNs the waiter raises the CTA's abort flag and counts
+// one in the device's fault word, the CTA's other waits end when they see the flag, and the CTA drains
 // its copies and products, frees its tensor memory and returns.
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr unsigned long long kDrainNs = 20000000ull;
@@ -71,7 +71,7 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
         if ((i & 63) == 0 && now_ns() - start > kWaitNs) break;
     }
     if (abort_flag != nullptr) *abort_flag = 1;
-    atomicExch(fault, 1);
+    atomicAdd(fault, 1);
     return false;
 }
 

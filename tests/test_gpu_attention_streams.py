@@ -98,3 +98,21 @@ def test_results_dropped_behind_queued_work_are_left_alone(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(want, copies)), name
         assert all(bool((x == 5.0).all()) for x in again)
+
+
+def test_fault_report_waits_for_every_stream(dev):
+    """What attn_fault answers holds for kernels still running on a stream that the default
+    stream does not wait for."""
+    m = pr()
+    T, hq, d = 32768, 16, 128
+    q, k, v = qkv_views(T, hq, hq, d, 210, dev, "plain")
+    cu = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    out = torch.empty_like(q)
+    s = torch.cuda.Stream()
+    assert m.attn_fault() is False                       # (loads what it reads)
+    torch.cuda.synchronize()
+    for _ in range(40):                                  # about 100 ms
+        m.attn_varlen_fwd(q, k, v, cu, out=out, stream=s)
+    assert not s.query()
+    assert m.attn_fault() is False
+    assert s.query()
