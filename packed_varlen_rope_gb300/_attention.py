@@ -407,6 +407,7 @@ def _attn_function():
             return out
 
         @staticmethod
+        @torch.autograd.function.once_differentiable       # the kernels have no second derivative
         def backward(ctx, dout):
             q, k, v, out, lse, cu_seqlens, seq_used = ctx.saved_tensors
             dq, dk, dv = attn_varlen_bwd(_rows(dout), q, k, v, out, lse, cu_seqlens, *ctx.args, seq_used=seq_used)
@@ -426,7 +427,8 @@ def _rows(t):
 def apply_attn(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] = None, seq_used=None):
     """Differentiable attention within each sample of a pack: ``attn_varlen_fwd`` with the
     gradients of ``attn_varlen_bwd``.  q, k, v may be any bf16 CUDA [T, heads, d] tensors;
-    those that the kernels cannot address (broadcast ones) are copied."""
+    those that the kernels cannot address (broadcast ones) are copied.  Differentiable once: a
+    second derivative raises an error."""
     global _Attn
     if _Attn is None:
         _Attn = _attn_function()
