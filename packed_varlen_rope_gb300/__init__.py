@@ -82,6 +82,7 @@ def _autograd_function():
             return q, k
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dq, dk):
             cu_seqlens, position_ids, seq_used = ctx.saved_tensors
             theta, token_offset, position_scale, cache, segments = ctx.args
@@ -109,7 +110,7 @@ def apply_rope_qk(q, k, cu_seqlens, theta: float, cos_sin_cache=None, position_i
     ``cu_seqlens`` (row r is token ``token_offset + r``, or as ``segments`` map it);
     with ``seq_used`` (int32 [n_seqs]) only the first seq_used[s] rows of sample s are
     rotated and the rest (a padded batch's pad rows) are left as they are, in the
-    forward and in the gradient."""
+    forward and in the gradient.  Differentiable once: a second derivative raises."""
     global _RopeQK
     if _RopeQK is None:
         _RopeQK = _autograd_function()
@@ -132,6 +133,7 @@ def _glu_function():
             return glu_fwd(kind, e, g)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dh):
             e, g = ctx.saved_tensors
             de, dg = glu_bwd(ctx.kind, dh.contiguous(), e, g)
@@ -146,7 +148,8 @@ _GLU = None
 def apply_glu(kind: str, e, g):
     """Differentiable h = act(e) * g for bf16 CUDA [rows, cols] views with contiguous rows
     (e.g. the gate and up halves of one fused projection output): ``kind`` "swiglu"
-    (SiLU), "geglu" (GELU, erf form) or "geglu_tanh" (GELU, tanh form)."""
+    (SiLU), "geglu" (GELU, erf form) or "geglu_tanh" (GELU, tanh form).  Differentiable once:
+    a second derivative raises."""
     global _GLU
     if kind not in GLU_KINDS:
         raise ValueError("kind must be one of %s" % sorted(GLU_KINDS))
