@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = y * kTile + lane + 32 * i;
-                    v[i] = r < rows ? __ldg(src + r) : make_float2(-INFINITY, 0.0f);
+                    v[i] = r < rows ? src[r] : make_float2(-INFINITY, 0.0f);
                 }
             }
             if (before > 0 && !warp_wait(y_empty + 8 * (place0 + at), (before - 1) & 1, &s_abort, &g_attn_bwd_fault)) break;
@@ -554,11 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 }
 
 // (-lse log2(e), -D) of every (head, token) row, D = dout . out.  Eight lanes a row, 16
-// elements each (head_dim <= 128); HBM-bound.
-__global__ void __launch_bounds__(256) attn_stats_kernel(const __nv_bfloat16 *__restrict__ dout, int64_t g_ts, int64_t g_hs,
-                                                         const __nv_bfloat16 *__restrict__ out, int64_t o_ts, int64_t o_hs,
-                                                         const float *__restrict__ lse, float2 *__restrict__ stats,
-                                                         int n_tokens, int hq, int d)
+// elements each (head_dim <= 128); HBM-bound.  The grid is resident while the kernel that
+// writes out and lse ends, so they are no read-only data: no __ldg and no __restrict__, here
+// and where the passes read the statistics.
+__global__ void __launch_bounds__(256) attn_stats_kernel(const __nv_bfloat16 *dout, int64_t g_ts, int64_t g_hs,
+                                                         const __nv_bfloat16 *out, int64_t o_ts, int64_t o_hs,
+                                                         const float *lse, float2 *stats, int n_tokens, int hq, int d)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -571,8 +572,8 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const __nv_bfloat16 *__
     for (int i = 0; i < 2; ++i) {
         const int col = 8 * (part + 8 * i);
         if (!in || col >= d) continue;
-        const uint4 g = __ldg(reinterpret_cast<const uint4 *>(dout + tok * g_ts + head * g_hs + col));
-        const uint4 o = __ldg(reinterpret_cast<const uint4 *>(out + tok * o_ts + head * o_hs + col));
+        const uint4 g = *reinterpret_cast<const uint4 *>(dout + tok * g_ts + head * g_hs + col);
+        const uint4 o = *reinterpret_cast<const uint4 *>(out + tok * o_ts + head * o_hs + col);
         const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

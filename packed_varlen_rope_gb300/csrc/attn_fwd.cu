@@ -542,9 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
 // Joins the partial results of the splits: o = sum_i w_i o_i, w_i = 2^(lse_i - lse).  One
 // warp a row, 4 elements a lane.  A part whose lse is -infinity holds no weight and nothing
-// was written for it; one of NaN (which the maximum passes over) makes the row NaN.
-__global__ void __launch_bounds__(128) attn_join_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
-                                                        __nv_bfloat16 *__restrict__ out, int64_t out_ts, int64_t out_hs,
+// was written for it; one of NaN (which the maximum passes over) makes the row NaN.  The grid
+// is resident while the kernel that writes the parts ends: no __ldg and no __restrict__.
+__global__ void __launch_bounds__(128) attn_join_kernel(const float *part_o, const float *part_lse,
+                                                        __nv_bfloat16 *out, int64_t out_ts, int64_t out_hs,
                                                         int n_rows, int hq, int d, int splits)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
