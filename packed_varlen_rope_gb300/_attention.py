@@ -136,7 +136,8 @@ def _declare(lib):
 class PagedKVCache:
     """Keys and values in pages: ``k_pages`` and ``v_pages`` are bf16 CUDA views
     [n_pages, page_size, n_kv_heads, head_dim], head_dim contiguous, any other strides (the
-    two may be the halves of one pool).  page_size is a multiple of 8."""
+    two may be the halves of one pool).  page_size is a multiple of 8.  Other pages are another
+    PagedKVCache: the descriptor that the calls use holds these tensors' addresses."""
 
     def __init__(self, k_pages, v_pages):
         _torch or _load_torch()
@@ -148,22 +149,30 @@ class PagedKVCache:
         dev = k_pages.get_device()
         if shape != v_pages.shape or dev != v_pages.get_device():
             raise ValueError("k_pages and v_pages must share shape and device")
-        self.k_pages, self.v_pages = k_pages, v_pages
+        self._k_pages, self._v_pages = k_pages, v_pages
         self._packed = _KV_PACK(k_pages.data_ptr(), ks[0], ks[1], ks[2], v_pages.data_ptr(), vs[0], vs[1], vs[2],
                                 *shape, 0)
         self._dev, self._heads, self._dim = dev, shape[2], shape[3]
 
     @property
+    def k_pages(self):
+        return self._k_pages
+
+    @property
+    def v_pages(self):
+        return self._v_pages
+
+    @property
     def device(self):
-        return self.k_pages.device
+        return self._k_pages.device
 
     @property
     def n_pages(self) -> int:
-        return self.k_pages.shape[0]
+        return self._k_pages.shape[0]
 
     @property
     def page_size(self) -> int:
-        return self.k_pages.shape[1]
+        return self._k_pages.shape[1]
 
     @property
     def n_kv_heads(self) -> int:
