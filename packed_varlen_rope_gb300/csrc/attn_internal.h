@@ -60,7 +60,8 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
 int attn_fault_word(int *word);
 int attn_bwd_fault_word(int *word);
 int attn_decode_fault_word(int *word);
-// Backward: the rows' statistics, then dk and dv, then dq.
+// Backward: the rows' statistics, then dq, then dk and dv.  dq goes first: where all keys of a
+// row are in one tile it rewrites the row's D, which the pass over the keys then reads.
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream);
 
 template <typename Symbol>
