@@ -16,10 +16,13 @@
  * where dk and dv sum over the G query heads of their key head too.
  *
  * Arithmetic.  bf16 in, bf16 out, one rounding to nearest even at the end.  Products
- * accumulate in binary32; scores, maxima, sums, lse and D stay in
- * binary32.  The weights p (forward and dv) and the ds (dq, dk) are rounded to bf16 once
- * where they enter a product: relative error at most 2^-8 of each term, as the final
- * rounding.  Results do not depend on launch timing: no atomics, the same bits each run.
+ * accumulate in binary32; scores, maxima, sums, lse and D stay in binary32.  The weights p
+ * (forward and dv) and the ds (dq, dk) are rounded to bf16 once where they enter a product:
+ * relative error at most 2^-8 of each term, as the final rounding.  D is taken from out as it
+ * was rounded, except where all keys of a row are in one tile of 128.  The backward has p from
+ * lse, and lse is binary32: p is off by up to |lse| 2^-22 of itself, which stays below its
+ * rounding to bf16 while |lse| does below 2^14.  Results do not depend on launch timing: no
+ * atomics, the same bits each run.
  *
  * Values.  Rows of other samples, rows beyond seq_used or outside the pack, and slots of
  * the cache beyond a sequence's length may hold anything, NaN and infinities among it, and
@@ -124,10 +127,13 @@ int attn_varlen_bwd(const attn_varlen_desc *desc, const attn_varlen_grads *grads
  * positions past max_pages * page_size are not read.  A row with a negative position, or
  * of no sequence, sees no key.
  *
- * One token per sequence up to whole prompts.  Where rows are few, the keys are split over
- * several CTAs, partial results go to the workspace and a second launch joins them.  The
- * split depends on the sizes on the host alone: max_kv_len, an upper bound on kv_lens[s]
- * (0: max_pages * page_size), tunes it and never cuts keys off.
+ * One token per sequence up to whole prompts.  Where rows are few, a sequence's keys are
+ * shared by the CTAs of a cluster, which join their results on the chip; only where that
+ * leaves SMs idle are they split further, with partial results in the workspace and a second
+ * launch that joins them.  All of it depends on the sizes on the host alone: max_kv_len, an
+ * upper bound on kv_lens[s] (0: max_pages * page_size), tunes it and never cuts keys off.  A
+ * page table much wider than the sequences, without that bound, is planned for as if they
+ * were that long.
  */
 typedef struct attn_paged_desc {
     const void *q;                 /* [total_tokens, n_q_heads, head_dim]              */

@@ -27,8 +27,9 @@
 // memory.
 //
 // Bound by the tensor core: 2048 cycles a 128x128 tile for dk and dv, 1536 for dq.  32/8 heads
-// of 128, causal: one sample of 32,768 tokens 19.7 ms, 1,118 TFLOP/s by the five products it
-// needs, 1,565 by the seven it runs (the library's sustain 1,705); 8,192 tokens 1.28 ms.
+// of 128, causal: one sample of 32,768 tokens 19.7-19.9 ms, 1,108-1,118 TFLOP/s by the five
+// products it needs, 1,551-1,565 by the seven it runs, and 20.0 ms over 0.8 s under the power
+// limit (the library's sustain 1,705); 8,192 tokens 1.30 and 1.35 ms.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -14,8 +14,8 @@
 // further splits join through the workspace in a second launch.
 //
 // Bound by HBM: G operations a byte of cache (64 sequences of 500-16,000 tokens, 32/8 heads
-// of 128: 325 us for 2.2 GB, 6.77 TB/s, a copy's rate); a short sequence by the chain of its
-// dependent steps (one of 4,098 tokens 10.7 us, of which 2.5 us of loads).
+// of 128: 325-330 us for 2.2 GB, 6.7-6.8 TB/s, a copy's rate); a short sequence by the chain of
+// its dependent steps (one of 4,098 tokens 10.7 us, of which 2.5 us of loads).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

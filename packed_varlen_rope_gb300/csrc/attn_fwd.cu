@@ -19,16 +19,18 @@
 // row tile's softmax runs the tensor core works for the other.
 //
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
-// elected lane of a converged warp (from one diverged lane each cost 100 cycles).  No register
-// spills in the softmax loop: with 200 KB of shared memory local memory misses to L2.  One
-// wait per row tile for the issuing warp: a wait costs some 200 cycles while the tensor core
+// elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
+// register spill (none in the packed instances, one of 4 bytes in the paged ones): with 200 KB
+// of shared memory local memory misses to L2, and the softmax loop waits for it.  One wait per
+// row tile for the issuing warp: a wait costs some 200 cycles while the tensor core
 // reads shared memory, so the arrival of K and V is folded into the barrier of P.
 //
 // The bound is the tensor core: 1024 cycles a row tile and key tile.  32/8 heads of 128,
-// causal: one sample of 32,768 tokens 5.34 ms, 1,647 TFLOP/s (the library's products sustain
-// 1,705 under the power limit); 8,192 tokens 380 us; packs of short samples are held back by
+// causal: one sample of 32,768 tokens 5.34-5.48 ms, 1,605-1,647 TFLOP/s, over 0.1 s and 5.70
+// ms, 1,544, over 0.9 s under the power limit (the library's products sustain 1,705; from pages
+// of 128 tokens 5.74 ms); 8,192 tokens 379 and 392 us; packs of short samples are held back by
 // the 6,000 cycles before a CTA's first softmax and the 4,000 after its last (16,384 tokens in
-// samples of 32-8,192: 470 us, 1,250 TFLOP/s).
+// samples of 32-8,192: 474 us, 1,237 TFLOP/s).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

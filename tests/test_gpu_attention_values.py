@@ -92,3 +92,34 @@ def test_packed_nan_query(dev, d):
     assert bool(lse.t()[spoiled].isnan().all())
     err = (lse.double() - ref["lse"]).abs().t()[~spoiled]
     assert float(err.max()) <= 2.0 ** -11 * (1 + float(ref["lse"].abs().max()))
+
+
+@pytest.mark.parametrize("level", [0.0, 2.0 ** 10, -2.0 ** 12, 2.0 ** 14])
+@pytest.mark.parametrize("n,causal", [(100, True), (300, False)])
+def test_gradients_of_large_scores(dev, level, n, causal):
+    """Scores level + x with x of a few units, exact in binary32: what the backward loses is its
+    exponent's rounding against lse, at most |lse| 2^-22 of a weight (lse's own two roundings, that
+    of lse log2(e) and that of scale log2(e), 2^-24 of |lse| each)."""
+    m = pr()
+    d = 64
+    q, k = torch.zeros((n, 1, d), device=dev), torch.zeros((n, 1, d), device=dev)
+    gen = torch.Generator(device=dev).manual_seed(60)
+    q[..., :2], k[..., 0] = 1.0, level
+    k[..., 1] = torch.randint(-64, 65, (n, 1), generator=gen, device=dev) / 32
+    q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+    v, dout = normal((n, 1, d), 61, dev), normal((n, 1, d), 62, dev)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    seen = causal_mask(n, n, causal, dev)
+    ref = sample_reference(q, k, v, 1.0, seen, dout)
+    o, lse = m.attn_varlen_fwd(q, k, v, cu, causal=causal, scale=1.0, return_lse=True)
+    got = m.attn_varlen_bwd(dout, q, k, v, o, lse, cu, causal=causal, scale=1.0)
+    rel = float(ref["lse"].abs().max()) * 2.0 ** -22
+    Q, K, V, G = (x[:, 0].double() for x in (q, k, v, dout))
+    p = torch.where(seen, torch.exp(Q @ K.t() - ref["lse"][0][:, None]), 0.0)
+    dP, D = G @ V.t(), (G * (p @ V)).sum(1, keepdim=True)
+    ds = p * (dP.abs() + 2 * D.abs())              # a row's weights are off by one factor, and D with them
+    assert_within(o, *ref["o"], "o")
+    assert float((lse.double() - ref["lse"]).abs().max()) <= float(ref["lse"].abs().max()) * 2.0 ** -23 + 2.0 ** -18
+    for x, name, more in zip(got, ("dq", "dk", "dv"), (ds @ K.abs(), ds.t() @ Q.abs(), p.t() @ G.abs())):
+        value, bound = ref[name]
+        assert_within(x, value, bound + rel * more[:, None], name)
