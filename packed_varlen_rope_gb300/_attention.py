@@ -6,7 +6,7 @@ import ctypes
 import struct
 from typing import Optional
 
-from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, load_library
+from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, _empty, load_library
 
 ATTN_EXPORTS = ("attn_varlen_fwd", "attn_varlen_bwd", "attn_varlen_bwd_workspace_bytes", "attn_paged",
                 "attn_paged_workspace_bytes", "attn_fault")
@@ -214,21 +214,6 @@ def _tables(cache, dev: int, page_table, kv_lens, cu_seqlens):
         raise ValueError("page_table must be an int32 [n_seqs, max_pages] tensor with contiguous rows on the "
                          "device of q")
     return cu, kv, page_table.data_ptr(), st[0], shape[1], n
-
-
-def _empty(shape, dtype, device, stream, returned=True):
-    """A new tensor for a call on ``stream`` (a torch stream, an int, or None: torch's current
-    one).  Its memory comes from that stream's pool: a block of another stream's may still be
-    in use by what is queued there.  ``returned``: the caller's current stream will use it too,
-    so its memory is not given to others before that stream has passed the tensor's end."""
-    if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    current = _torch.cuda.current_stream(device)
-    with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
-        t = _torch.empty(shape, dtype=dtype, device=device)
-    if returned and t.numel():
-        t.record_stream(current)
-    return t
 
 
 def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, theta: float, q_out=None,

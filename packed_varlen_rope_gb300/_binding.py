@@ -206,6 +206,23 @@ def _stream(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, returned=True):
+    """A new tensor for a call on ``stream`` (a torch stream, an int, or None: torch's current
+    one).  Its memory comes from that stream's pool: a block of another stream's may still be
+    in use by what is queued there.  ``returned``: the caller's current stream will use it too,
+    so its memory is not given to others before that stream has passed the tensor's end."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.numel():
+        t.record_stream(current)
+    return t
+
+
 def _on(device, fn, *args):
     """Call library entry point ``fn`` with ``device`` current: the library launches on
     the calling thread's current device, and the stream passed belongs to ``device``.
@@ -315,7 +332,7 @@ def new_cos_sin_cache(rows: int, head_dim: int, theta: float, device="cuda", str
     """Allocate (through torch) and build a cos/sin cache of ``rows`` positions."""
     import torch
 
-    data = torch.empty((rows, 4, head_dim // 16, 4), dtype=torch.float32, device=device)
+    data = _empty((rows, 4, head_dim // 16, 4), torch.float32, device, stream)
     return rope_cos_sin_cache_build(data, theta, stream, position_scale)
 
 
@@ -331,7 +348,7 @@ def rope_qk_positions(cu_seqlens, total_tokens: int, pos_out=None, stream=None):
     import torch
 
     if pos_out is None:
-        pos_out = torch.empty(int(total_tokens), dtype=torch.int32, device=cu_seqlens.device)
+        pos_out = _empty(int(total_tokens), torch.int32, cu_seqlens.device, stream)
     _check_cu(cu_seqlens, pos_out.device)
     st = _on(cu_seqlens.device, load_library().rope_qk_positions, _ptr(cu_seqlens), cu_seqlens.numel() - 1,
              int(total_tokens), _ptr(pos_out), _stream(stream, cu_seqlens.device))
@@ -344,7 +361,7 @@ def rope_validate_cu_seqlens(cu_seqlens, total_tokens: int, err_word=None, strea
     import torch
 
     if err_word is None:
-        err_word = torch.empty(1, dtype=torch.int32, device=cu_seqlens.device)
+        err_word = _empty(1, torch.int32, cu_seqlens.device, stream)
     st = _on(cu_seqlens.device, load_library().rope_validate_cu_seqlens, _ptr(cu_seqlens),
              cu_seqlens.numel() - 1, int(total_tokens), _ptr(err_word), _stream(stream, cu_seqlens.device))
     _check("rope_validate_cu_seqlens", st)
@@ -362,7 +379,7 @@ def rope_cos_sin_eval(phi, mode: str = "as_rotation", stream=None):
 
     if phi.dtype != torch.float32 or not phi.is_cuda or not phi.is_contiguous():
         raise ValueError("phi must be a contiguous float32 CUDA tensor")
-    c, s = torch.empty_like(phi), torch.empty_like(phi)
+    c, s = (_empty(phi.shape, torch.float32, phi.device, stream) for _ in range(2))
     st = _on(phi.device, load_library().rope_cos_sin_eval, _ptr(phi), _ptr(c), _ptr(s), phi.numel(),
              COS_SIN_MODES[mode], _stream(stream, phi.device))
     _check("rope_cos_sin_eval", st)
@@ -520,7 +537,7 @@ def glu_fwd(kind: str, e, g, h=None, stream=None):
 
     shape = tuple(e.shape)
     if h is None:
-        h = torch.empty(shape, dtype=torch.bfloat16, device=e.device)
+        h = _empty(shape, torch.bfloat16, e.device, stream)
     ep, es = _mat_args(e, "e", shape, e.device)
     gp, gs = _mat_args(g, "g", shape, e.device)
     hp, hs = _mat_args(h, "h", shape, e.device)
@@ -537,9 +554,9 @@ def glu_bwd(kind: str, dh, e, g, de=None, dg=None, stream=None):
 
     shape = tuple(e.shape)
     if de is None:
-        de = torch.empty(shape, dtype=torch.bfloat16, device=e.device)
+        de = _empty(shape, torch.bfloat16, e.device, stream)
     if dg is None:
-        dg = torch.empty(shape, dtype=torch.bfloat16, device=e.device)
+        dg = _empty(shape, torch.bfloat16, e.device, stream)
     args = []
     for name, t in (("dh", dh), ("e", e), ("g", g), ("de", de), ("dg", dg)):
         args += list(_mat_args(t, name, shape, e.device))

@@ -61,12 +61,28 @@ def calls(dev):
             ("paged", lambda s: (m.attn_paged(qn, cache, table, lens, cun, stream=s),), [qn.numel() * 2, need])]
 
 
+def other_calls(dev):
+    """The same of the rotation's helpers and the GLU."""
+    m = pr()
+    e, g, dh = (normal((2000, 1024), 220 + i, dev) for i in range(3))
+    cu = torch.tensor([0, 300000, 600000], dtype=torch.int32, device=dev)
+    phi = torch.rand(600000, generator=torch.Generator(device=dev).manual_seed(223), device=dev) * 1e4
+    n = e.numel() * 2
+    return [("glu", lambda s: (m.glu_fwd("swiglu", e, g, stream=s),), [n]),
+            ("glu backward", lambda s: m.glu_bwd("geglu", dh, e, g, stream=s), [n, n]),
+            ("positions", lambda s: (m.rope_qk_positions(cu, 600000, stream=s),), [2400000]),
+            ("validation", lambda s: (m.rope_validate_cu_seqlens(cu, 600000, stream=s),), [4]),
+            ("cos and sin", lambda s: m.rope_cos_sin_eval(phi, stream=s), [2400000, 2400000]),
+            ("cache", lambda s: (m.new_cos_sin_cache(8192, 128, 1e6, device=dev, stream=s).data,), [8192 * 128 * 4])]
+
+
+@pytest.mark.parametrize("which", [calls, other_calls])
 @pytest.mark.parametrize("as_int", [False, True])
-def test_memory_freed_behind_queued_work_is_left_alone(dev, as_int):
+def test_memory_freed_behind_queued_work_is_left_alone(dev, as_int, which):
     """Tensors of the very sizes that the call needs, dropped while the current stream has yet to
     read them: their values arrive, and the call's results are right."""
     s, busy = torch.cuda.Stream(), Busy(dev)
-    for name, call, sizes in calls(dev):
+    for name, call, sizes in which(dev):
         want = call(None)
         torch.cuda.synchronize()
         olds = [torch.full((n // 4,), 7.0 + i, device=dev) for i, n in enumerate(sizes)]
@@ -80,11 +96,12 @@ def test_memory_freed_behind_queued_work_is_left_alone(dev, as_int):
         assert all(bool((x == 7.0 + i).all()) for i, x in enumerate(copies)), name
 
 
-def test_results_dropped_behind_queued_work_are_left_alone(dev):
+@pytest.mark.parametrize("which", [calls, other_calls])
+def test_results_dropped_behind_queued_work_are_left_alone(dev, which):
     """Results of a call on another stream, dropped while the current stream has yet to read them,
     keep their values there although that stream then wants the same sizes."""
     s, busy = torch.cuda.Stream(), Busy(dev)
-    for name, call, _ in calls(dev):
+    for name, call, _ in which(dev):
         want = call(None)
         torch.cuda.synchronize()
         got = call(s)
