@@ -74,7 +74,7 @@ struct Shared {
     static constexpr int kOffY = 2 * kTileBytes;                      // Y1 tiles, then Y2 tiles
     static constexpr int kOffStats = kOffY + (kY1 + kY2) * kTileBytes;   // of even and odd tiles: -lse, then -D
     static constexpr int kOffBars = kOffStats + 2 * 2 * kTile * 4;
-    static constexpr int kOffRest = kOffBars + 192;
+    static constexpr int kOffRest = kOffBars + 208;
     static constexpr int kBytes = kOffRest + 64;
 };
 
@@ -94,12 +94,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     // all of the shared memory there is: tiles on 1024-byte boundaries with no slack
     extern __shared__ __align__(1024) uint8_t smem[];
     static_assert(sizeof(Rest) <= 64 && Sh::kBytes <= 227 * 1024, "shared memory");
+    static_assert(104 + 8 * (2 * (Sh::kY1 + Sh::kY2) + 2) <= Sh::kOffRest - Sh::kOffBars, "barriers");
     const uint32_t base = smem_addr(smem);
     const uint32_t bars = base + Sh::kOffBars;
-    const uint32_t x_full = bars, s_full = bars + 8, p_full = bars + 16, ds_full = bars + 24, done = bars + 32,
+    const uint32_t x_full = bars, s_full = bars + 8, p_full = bars + 16, done = bars + 32,
                    drain = bars + 40, dp_full = bars + 48, st_full = bars + 64, st_empty = bars + 80, first_full = bars + 96,
                    y_full = bars + 104,
-                   y_empty = y_full + 8 * (Sh::kY1 + Sh::kY2);
+                   y_empty = y_full + 8 * (Sh::kY1 + Sh::kY2),
+                   // of even and odd tiles: for queries S(t + 1) is there before every warp has stored
+                   // dS(t), and a warp that is a tile ahead must not arrive in another's place
+                   ds_full = y_empty + 8 * (Sh::kY1 + Sh::kY2);
     Rest &rest = *reinterpret_cast<Rest *>(smem + Sh::kOffRest);
     volatile int &s_abort = rest.abort;
     // where tile t of Y1 (0) or Y2 (1) is, and how often that place was used before
@@ -111,11 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         mbar_init(x_full, 1);
         mbar_init(s_full, 1);
         mbar_init(p_full, 17);
-        mbar_init(ds_full, 16);
         mbar_init(done, 1);
         mbar_init(drain, 1);
         mbar_init(first_full, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(ds_full + 8 * i, 16);
             mbar_init(dp_full + 8 * i, 1);
             mbar_init(st_full + 8 * i, 1);
             mbar_init(st_empty + 8 * i, 1);
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 if (!KEYS && more) scores(t + 1, 1);
             }
             __syncwarp();
-            wait(ds_full, t);
+            wait(ds_full + 8 * (t & 1), t >> 1);
             if (ok && elect_one()) {
                 accumulate(t, 0);
                 if (KEYS && more) scores(t + 1, 1);
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(ds_full);
+            if (lane == 0) mbar_arrive(ds_full + 8 * (t & 1));
         }
         if (ok && n_tiles > 0) {
             ok = warp_wait(done, 0, &s_abort, &g_attn_bwd_fault);
