@@ -60,6 +60,23 @@ from ._attention import (  # noqa: F401
     new_paged_kv_cache,
     rope_kv_append,
 )
+from ._axes import (  # noqa: F401
+    ROPE_MAX_AXES,
+    RopeAxesDesc,
+    apply_rope_axes,
+    check_sections,
+    rope_axes_apply,
+)
+from ._step import (  # noqa: F401
+    PAGED_EXPORTS,
+    STEP_NEGATIVE_LENGTH,
+    STEP_NO_PAGES,
+    STEP_STACK_FULL,
+    STEP_TABLE_FULL,
+    STEP_TOKENS_PAST_END,
+    PagedKVStepDesc,
+    paged_kv_step,
+)
 from .shards import cp_shards, shard_rows, shard_segments, ulysses_heads  # noqa: F401
 
 
@@ -178,16 +195,28 @@ class RotaryEmbedding:
 
         >>> rope = RotaryEmbedding(128, 1e6)
         >>> q, k = rope(q, k, cu_seqlens=cu)          # in place, differentiable
+
+    With ``sections`` the positions have several axes (``rope_axes_apply``) and are always
+    explicit:
+
+        >>> rope = RotaryEmbedding(128, 1e6, sections=(16, 24, 24))
+        >>> q, k = rope(q, k, position_ids=ids)       # [3, T]: time, height, width
     """
 
-    def __init__(self, head_dim: int, theta: float, position_scale: float = 1.0, use_cache: bool = True):
+    def __init__(self, head_dim: int, theta: float, position_scale: float = 1.0, use_cache: bool = True,
+                 sections=None, interleaved: bool = False, own_frequencies: bool = False):
         """``use_cache=False``: no table at all, cos/sin evaluated in the kernel (the same
         bits; as fast on large packs, a few % slower on small ones, and no memory: the
         table of a 1,048,576-token sequence with head_dim 128 takes 512 MiB)."""
         if head_dim % 16 != 0 or not 16 <= head_dim <= 256:
             raise ValueError("head_dim must be a multiple of 16 in [16, 256]")
         self.head_dim, self.theta, self.position_scale = int(head_dim), float(theta), float(position_scale)
-        self.use_cache = bool(use_cache)
+        # a cache holds the frequencies that the axes share
+        self.use_cache = bool(use_cache) and not own_frequencies
+        if sections is None and (interleaved or own_frequencies):
+            raise ValueError("interleaved and own_frequencies need sections")
+        self.sections = None if sections is None else check_sections(sections, self.head_dim)
+        self.interleaved, self.own_frequencies = bool(interleaved), bool(own_frequencies)
         self._caches = {}
 
     def cache(self, device, rows: int):
@@ -224,6 +253,13 @@ class RotaryEmbedding:
             rows = int(token_offset) + T
         rows = max(rows, int(max_position) + 1 if max_position else 0)
         cache = self.cache(q.device, max(rows, 1)) if self.use_cache else None
+        if self.sections is not None:
+            if position_ids is None or cu_seqlens is not None or token_offset or segments is not None or \
+                    seq_used is not None:
+                raise ValueError("a rotation by several axes takes its positions from position_ids [axes, tokens] alone")
+            return apply_rope_axes(q, k, self.theta, self.sections, position_ids, cos_sin_cache=cache,
+                                   position_scale=self.position_scale, interleaved=self.interleaved,
+                                   own_frequencies=self.own_frequencies)
         return apply_rope_qk(q, k, cu_seqlens, self.theta, cos_sin_cache=cache, position_ids=position_ids,
                              token_offset=token_offset, position_scale=self.position_scale, segments=segments,
                              seq_used=seq_used)

@@ -6,6 +6,7 @@ import ctypes
 import struct
 from typing import Optional
 
+from ._axes import pack_axes
 from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, _empty, load_library
 
 ATTN_EXPORTS = ("attn_varlen_fwd", "attn_varlen_bwd", "attn_varlen_bwd_workspace_bytes", "attn_paged",
@@ -217,13 +218,16 @@ def _tables(cache, dev: int, page_table, kv_lens, cu_seqlens):
 
 
 def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, theta: float, q_out=None,
-                   position_scale: float = 1.0, cos_sin_cache=None, stream=None):
+                   position_scale: float = 1.0, cos_sin_cache=None, stream=None, position_ids=None, sections=None,
+                   interleaved: bool = False, own_frequencies: bool = False):
     """Rotate the new tokens' q [T, Hq, d] (in place, or into ``q_out``) and k [T, Hkv, d] by
     their positions and write k and v [T, Hkv, d] into the pages of ``cache`` (C entry point
     ``rope_kv_append``).  ``cu_seqlens`` (int32 [n + 1]) delimits the new tokens of each
     sequence, ``kv_lens`` (int32 [n]) counts its tokens in the cache with the new ones,
     ``page_table`` (int32 [n, max_pages]) names its pages; all on the device.  k and v are
-    only read.  Returns the rotated q."""
+    only read.  With ``position_ids`` ([axes, T]) and ``sections`` the angles come from several
+    position axes as in ``rope_axes_apply`` (C entry point ``rope_kv_append_axes``), the places in
+    the cache from the lengths as before.  Returns the rotated q."""
     _torch or _load_torch()
     qv, kv, vv = _view(q, "q"), _view(k, "k"), _view(v, "v")
     dev = q.get_device()
@@ -244,7 +248,13 @@ def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens
         ref = _cache_arg(cos_sin_cache, d, q.device)
     desc = _APPEND_PACK(*qv, *kv, *vv, *ov, cache._packed, cu, lens, table, stride, width, n, hq, 0, T, float(theta),
                         float(position_scale), 0 if ref is None else ctypes.addressof(ref.contents))
-    _launch(load_library().rope_kv_append, "rope_kv_append", dev, stream, desc)
+    if position_ids is None and sections is None:
+        if interleaved or own_frequencies:
+            raise ValueError("interleaved and own_frequencies need position_ids and sections")
+        _launch(load_library().rope_kv_append, "rope_kv_append", dev, stream, desc)
+    else:
+        axes = pack_axes(position_ids, sections, T, dev, interleaved, own_frequencies)
+        _launch(load_library().rope_kv_append_axes, "rope_kv_append_axes", dev, stream, desc, axes)
     return q if q_out is None else q_out
 
 

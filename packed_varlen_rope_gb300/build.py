@@ -9,8 +9,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", n) for n in ("rope_qk.cu", "rope_host.cu", "glu.cu", "rope_append.cu",
+                                                 "rope_axes.cu", "paged_step.cu",
                                                  "attn.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu")]
-HEADERS = [os.path.join(ROOT, "include", n) for n in ("rope_qk.h", "glu.h", "paged_kv.h", "attn.h")] + \
+HEADERS = [os.path.join(ROOT, "include", n) for n in ("rope_qk.h", "glu.h", "paged_kv.h", "attn.h", "rope_axes.h",
+                                                       "paged_step.h")] + \
           [os.path.join(HERE, "csrc", n) for n in ("fastdiv.cuh", "cos_sin.cuh", "rope_core.cuh", "host_checks.h",
                                                    "paged_checks.h", "attn_internal.h", "tensor_core.cuh", "tensor_map.h")]
 LIB_PATH = os.path.join(HERE, "librope_qk.so")

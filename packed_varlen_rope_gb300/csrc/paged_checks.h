@@ -73,4 +73,46 @@ inline int check_page_table(const int32_t *cu, const int32_t *kv_lens, const int
     return ROPE_OK;
 }
 
+// The views of an append's descriptor (q_out: q when it is rotated in place).
+struct AppendViews {
+    View q, k, v, q_out;
+};
+
+// Every check of an append; with no tokens nothing but sizes is checked, and no view filled.
+inline int check_append(const rope_kv_append_desc &p, AppendViews &w)
+{
+    const rope_paged_kv &c = p.cache;
+    const int64_t T = p.total_tokens;
+    if (T < 0 || p.n_q_heads < 1 || p.n_q_heads > (1 << 20)) return ROPE_ERR_SHAPE;
+    if (p.reserved != 0) return ROPE_ERR_UNSUPPORTED;
+    int rc;
+    if ((rc = check_paged(c)) != ROPE_OK) return rc;
+    if ((rc = check_theta(p.theta)) != ROPE_OK || (rc = check_scale(p.position_scale)) != ROPE_OK) return rc;
+    if ((rc = check_cache(p.cos_sin_cache, c.head_dim, p.theta, p.position_scale)) != ROPE_OK) return rc;
+    if (T > kMaxTokens) return ROPE_ERR_UNSUPPORTED;
+    if (T == 0) return ROPE_OK;
+    if ((rc = check_page_table(p.cu_seqlens, p.kv_lens, p.page_table, p.page_table_stride, p.max_pages,
+                               p.n_seqs)) != ROPE_OK)
+        return rc;
+    const int64_t d = c.head_dim;
+    w.q = View{p.q, T, p.n_q_heads, p.q_stride_token, p.q_stride_head, d};
+    w.k = View{p.k, T, c.n_kv_heads, p.k_stride_token, p.k_stride_head, d};
+    w.v = View{p.v, T, c.n_kv_heads, p.v_stride_token, p.v_stride_head, d};
+    const bool in_place = p.q_out == nullptr;
+    w.q_out = in_place ? w.q : View{p.q_out, T, p.n_q_heads, p.q_out_stride_token, p.q_out_stride_head, d};
+    for (const View *x : {&w.q, &w.k, &w.v, &w.q_out})
+        if ((rc = check_view(*x)) != ROPE_OK) return rc;
+    if (in_place && (!views_disjoint(w.q, w.k) || !views_disjoint(w.q, w.v))) return ROPE_ERR_OVERLAP;
+    auto in_pools = [&](const View &x) {
+        return c.n_pages > 0 && (overlap(c.k, 2 * k_span(c), x.base, x.bytes()) ||
+                                 overlap(c.v, 2 * v_span(c), x.base, x.bytes()));
+    };
+    for (const View *x : {&w.q, &w.k, &w.v}) {
+        if (!in_place && overlap(w.q_out.base, w.q_out.bytes(), x->base, x->bytes())) return ROPE_ERR_OVERLAP;
+        if (in_pools(*x)) return ROPE_ERR_OVERLAP;
+    }
+    if (!in_place && in_pools(w.q_out)) return ROPE_ERR_OVERLAP;
+    return check_cache_device(p.cos_sin_cache);
+}
+
 }  // namespace pvr

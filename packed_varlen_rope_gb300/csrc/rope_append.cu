@@ -217,36 +217,12 @@ extern "C" int rope_kv_append(const rope_kv_append_desc *dp, void *stream)
     const rope_kv_append_desc &p = *dp;
     const rope_paged_kv &c = p.cache;
     const int64_t T = p.total_tokens;
-    if (T < 0 || p.n_q_heads < 1 || p.n_q_heads > (1 << 20)) return ROPE_ERR_SHAPE;
-    if (p.reserved != 0) return ROPE_ERR_UNSUPPORTED;
-    int rc;
-    if ((rc = check_paged(c)) != ROPE_OK) return rc;
-    if ((rc = check_theta(p.theta)) != ROPE_OK || (rc = check_scale(p.position_scale)) != ROPE_OK) return rc;
-    if ((rc = check_cache(p.cos_sin_cache, c.head_dim, p.theta, p.position_scale)) != ROPE_OK) return rc;
-    if (T > kMaxTokens) return ROPE_ERR_UNSUPPORTED;
-    if (T == 0) return ROPE_OK;
-    if ((rc = check_page_table(p.cu_seqlens, p.kv_lens, p.page_table, p.page_table_stride, p.max_pages,
-                               p.n_seqs)) != ROPE_OK)
-        return rc;
+    AppendViews w;
+    const int rc = check_append(p, w);
+    if (rc != ROPE_OK || T == 0) return rc;
     const int64_t d = c.head_dim;
-    const View q{p.q, T, p.n_q_heads, p.q_stride_token, p.q_stride_head, d};
-    const View k{p.k, T, c.n_kv_heads, p.k_stride_token, p.k_stride_head, d};
-    const View v{p.v, T, c.n_kv_heads, p.v_stride_token, p.v_stride_head, d};
+    const View &q = w.q, &k = w.k, &v = w.v, &qo = w.q_out;
     const bool in_place = p.q_out == nullptr;
-    const View qo = in_place ? q : View{p.q_out, T, p.n_q_heads, p.q_out_stride_token, p.q_out_stride_head, d};
-    for (const View *x : {&q, &k, &v, &qo})
-        if ((rc = check_view(*x)) != ROPE_OK) return rc;
-    if (in_place && (!views_disjoint(q, k) || !views_disjoint(q, v))) return ROPE_ERR_OVERLAP;
-    for (const View *x : {&q, &k, &v}) {
-        if (!in_place && overlap(qo.base, qo.bytes(), x->base, x->bytes())) return ROPE_ERR_OVERLAP;
-        if (c.n_pages > 0 && (overlap(c.k, 2 * k_span(c), x->base, x->bytes()) ||
-                              overlap(c.v, 2 * v_span(c), x->base, x->bytes())))
-            return ROPE_ERR_OVERLAP;
-    }
-    if (!in_place && c.n_pages > 0 && (overlap(c.k, 2 * k_span(c), qo.base, qo.bytes()) ||
-                                       overlap(c.v, 2 * v_span(c), qo.base, qo.bytes())))
-        return ROPE_ERR_OVERLAP;
-    if ((rc = check_cache_device(p.cos_sin_cache)) != ROPE_OK) return rc;
 
     AppendArgs a{};
     a.q = static_cast<const __nv_bfloat16 *>(p.q);
