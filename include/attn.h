@@ -163,6 +163,36 @@ int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc);
 
 int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * Rules on the scores, for the three operations above.  With u_ij = scale * q_i . k_j,
+ *
+ *     s_ij = cap * tanh(u_ij / cap) - slopes[h] * |i - j|
+ *
+ * in place of u_ij, where i and j are positions in the sequence and h is the query head; and a
+ * causal row also sees the keys below prefix[s], whatever its own position (an image, or a
+ * document that the whole sequence is about).  The backward has ds_ij (1 - tanh^2(u_ij / cap)) in
+ * place of ds_ij where it sums dq and dk; slopes are constants of the model and get no gradient.
+ *
+ * A cap moves a score by less than 8e-6 of its distance from 0, computed in binary32.  A score of
+ * +-infinity is capped like any other; a NaN comes out in its row.
+ */
+typedef struct attn_score_rule {
+    const float *slopes;           /* device float [n_q_heads], finite; or NULL: no bias   */
+    const int32_t *prefix;         /* device int32 [n_seqs], keys that all rows of the
+                                      sequence see (cut to its keys, negative as 0); needs
+                                      causal (else ROPE_ERR_UNSUPPORTED); or NULL          */
+    float cap;                     /* 0: none; else > 0; cap, 1.45 cap, scale / cap and
+                                      2.9 scale / cap normal in binary32 (else ROPE_ERR_THETA) */
+    int32_t reserved;              /* 0 */
+} attn_score_rule;
+
+/* attn_varlen_fwd, attn_varlen_bwd and attn_paged under a rule (NULL: none). */
+int attn_varlen_fwd_rule(const attn_varlen_desc *desc, const attn_score_rule *rule, void *stream);
+int attn_varlen_bwd_rule(const attn_varlen_desc *desc, const attn_varlen_grads *grads, const attn_score_rule *rule,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+int attn_paged_rule(const attn_paged_desc *desc, const attn_score_rule *rule, void *workspace,
+                    int64_t workspace_bytes, void *stream);
+
 /* 1 when a bounded wait inside an attention kernel has run out on the current device since
  * the library was loaded or this was last called (results since then are invalid), else 0;
  * ROPE_ERR_LAUNCH when the device cannot be read.  Waits for the work of every stream of the

@@ -46,6 +46,7 @@ from ._binding import (  # noqa: F401
 from ._attention import (  # noqa: F401
     ATTN_EXPORTS,
     AttnPagedDesc,
+    AttnScoreRule,
     AttnVarlenDesc,
     AttnVarlenGrads,
     PagedKVCache,

@@ -10,7 +10,7 @@ from ._axes import pack_axes
 from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, _empty, load_library
 
 ATTN_EXPORTS = ("attn_varlen_fwd", "attn_varlen_bwd", "attn_varlen_bwd_workspace_bytes", "attn_paged",
-                "attn_paged_workspace_bytes", "attn_fault")
+                "attn_paged_workspace_bytes", "attn_fault", "attn_varlen_fwd_rule", "attn_varlen_bwd_rule", "attn_paged_rule")
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -62,6 +62,12 @@ class AttnPagedDesc(ctypes.Structure):
                 ("causal", _i32), ("scale", ctypes.c_float), ("reserved", _i32)]
 
 
+class AttnScoreRule(ctypes.Structure):
+    """Mirror of ``attn_score_rule``."""
+
+    _fields_ = [("slopes", _vp), ("prefix", _vp), ("cap", ctypes.c_float), ("reserved", _i32)]
+
+
 # A decoding step is a few microseconds on the GPU, so the calls below pack a descriptor in one
 # go (the structures above, as ``struct`` formats) and read each tensor's fields once.
 _VIEW = "Pqq"
@@ -70,6 +76,7 @@ _PAGED = "88s"
 _APPEND_PACK = struct.Struct("@" + 4 * _VIEW + _PAGED + "PPPqiiiiqddP").pack
 _VARLEN_PACK = struct.Struct("@" + 4 * _VIEW + "PPPqiiiiif").pack
 _GRADS_PACK = struct.Struct("@" + 4 * _VIEW).pack
+_RULE_PACK = struct.Struct("@PPfi").pack
 _PAGED_PACK = struct.Struct("@" + 2 * _VIEW + _PAGED + "PPPqqqiiiifi").pack
 
 _torch = _bf16 = _i32t = _f32t = _raw_stream = _current_device = None
@@ -102,6 +109,23 @@ def _int32(t, dev: int, n: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _rule(score_cap, distance_slopes, prefix_lens, q, dev: int, n: int):
+    """The packed rule on the scores, None without one."""
+    if score_cap == 0 and distance_slopes is None and prefix_lens is None:
+        return None
+    slopes = prefix = 0
+    if distance_slopes is not None:
+        if distance_slopes.requires_grad and _torch.is_grad_enabled():
+            raise ValueError("distance_slopes are constants: they get no gradient")
+        if distance_slopes.dtype is not _f32t or tuple(distance_slopes.shape) != (q.shape[1],) or \
+                distance_slopes.get_device() != dev or not distance_slopes.is_contiguous():
+            raise ValueError("distance_slopes must be a contiguous float32 tensor of one value a query head on the device of q")
+        slopes = distance_slopes.data_ptr()
+    if prefix_lens is not None:
+        prefix = _int32(prefix_lens, dev, n, "prefix_lens")
+    return _RULE_PACK(slopes, prefix, score_cap, 0)
+
+
 def _launch(fn, name: str, dev: int, stream, *args) -> None:
     """Call an entry point with device ``dev`` current, on ``stream`` (a torch stream or an int)
     or torch's current one of that device."""
@@ -130,7 +154,11 @@ def _declare(lib):
     lib.attn_paged_workspace_bytes.argtypes = [_vp]
     lib.attn_paged_workspace_bytes.restype = _i64
     lib.attn_fault.argtypes = []
-    for name in ("rope_kv_append", "attn_varlen_fwd", "attn_varlen_bwd", "attn_paged", "attn_fault"):
+    lib.attn_varlen_fwd_rule.argtypes = [_vp, _vp, _vp]
+    lib.attn_varlen_bwd_rule.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp]
+    lib.attn_paged_rule.argtypes = [_vp, _vp, _vp, _i64, _vp]
+    for name in ("rope_kv_append", "attn_varlen_fwd", "attn_varlen_bwd", "attn_paged", "attn_fault",
+                 "attn_varlen_fwd_rule", "attn_varlen_bwd_rule", "attn_paged_rule"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -259,14 +287,16 @@ def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens
 
 
 def attn_paged(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, causal: bool = True,
-               scale: Optional[float] = None, out=None, max_kv_len: int = 0, workspace=None, stream=None):
+               scale: Optional[float] = None, out=None, max_kv_len: int = 0, workspace=None, stream=None,
+               score_cap: float = 0.0, distance_slopes=None, prefix_lens=None):
     """Attention of the new tokens' q [T, Hq, d] over the pages of ``cache`` (C entry point
     ``attn_paged``), the new tokens' own keys and values among them (``rope_kv_append``
     first).  Arrays as for ``rope_kv_append``.  ``scale``: 1/sqrt(d) unless given.
     ``max_kv_len``: an upper bound on ``kv_lens`` known on the host (tunes the split of long
     caches; 0: what the page table's width allows).  ``workspace``: a CUDA tensor for
     partial results (``attn_paged_workspace_bytes``); allocated through torch unless given.
-    Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
+    ``score_cap``, ``distance_slopes`` and ``prefix_lens``: rules on the scores, as in
+    ``attn_varlen_fwd`` (C entry point ``attn_paged_rule``).  Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
     _torch or _load_torch()
     if out is None:
         out = _empty(q.shape, _bf16, q.device, stream)
@@ -283,7 +313,11 @@ def attn_paged(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, causal: 
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(lib.attn_paged, "attn_paged", dev, stream, desc, ws, nbytes)
+    rule = _rule(score_cap, distance_slopes, prefix_lens, q, dev, kv_lens.numel())
+    if rule is None:
+        _launch(lib.attn_paged, "attn_paged", dev, stream, desc, ws, nbytes)
+    else:
+        _launch(lib.attn_paged_rule, "attn_paged_rule", dev, stream, desc, rule, ws, nbytes)
     return out
 
 
@@ -335,30 +369,41 @@ def _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used):
 
 
 def attn_varlen_fwd(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] = None, seq_used=None, out=None,
-                    return_lse: bool = False, stream=None):
+                    return_lse: bool = False, stream=None, score_cap: float = 0.0, distance_slopes=None, prefix_lens=None):
     """Attention within each sample of a pack (C entry point ``attn_varlen_fwd``).  q
     [T, Hq, d], k and v [T, Hkv, d]: bf16 CUDA views, any token and head strides (the
     slices of one fused QKV output), Hq a multiple of Hkv, d a multiple of 16 up to 128.
     ``seq_used`` (int32 [n]): only the first seq_used[s] rows of sample s are rows and keys.
     ``scale``: 1/sqrt(d) unless given.  Returns out [T, Hq, d] (a new tensor unless given;
     rows that see no key are 0), with ``return_lse`` (out, lse): lse float32 [Hq, T], the
-    natural logarithm of each row's sum, which the backward takes."""
+    natural logarithm of each row's sum, which the backward takes.
+
+    Rules on the scores u = scale q.k (C entry point ``attn_varlen_fwd_rule``): ``score_cap`` (0:
+    none) makes them cap * tanh(u / cap); ``distance_slopes`` (float32 [Hq]) takes slope * |i - j|
+    off the score of row i and key j; with ``prefix_lens`` (int32 [n], with ``causal``) every row of
+    sample s also sees the sample's first prefix_lens[s] keys."""
     _torch or _load_torch()
     if out is None:
         out = _empty(q.shape, _bf16, q.device, stream)
     lse = _empty((q.shape[1], q.shape[0]), _f32t, q.device, stream) if return_lse else None
     desc, dev = _varlen_desc(q, k, v, out, lse, cu_seqlens, causal, scale, seq_used)
-    _launch(load_library().attn_varlen_fwd, "attn_varlen_fwd", dev, stream, desc)
+    rule = _rule(score_cap, distance_slopes, prefix_lens, q, dev, cu_seqlens.numel() - 1)
+    if rule is None:
+        _launch(load_library().attn_varlen_fwd, "attn_varlen_fwd", dev, stream, desc)
+    else:
+        _launch(load_library().attn_varlen_fwd_rule, "attn_varlen_fwd_rule", dev, stream, desc, rule)
     return (out, lse) if return_lse else out
 
 
 def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, scale: Optional[float] = None,
-                    seq_used=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+                    seq_used=None, dq=None, dk=None, dv=None, workspace=None, stream=None, score_cap: float = 0.0,
+                    distance_slopes=None, prefix_lens=None):
     """Gradients (dq, dk, dv) of ``attn_varlen_fwd`` for the output gradient ``dout`` (C entry
     point ``attn_varlen_bwd``), with the ``out`` and ``lse`` that it returned and its other
     arguments.  dq, dk and dv are written whole (new tensors unless given; rows of no sample
     get 0).  ``workspace``: a CUDA tensor of at least 8 * T * Hq bytes; allocated through
-    torch unless given."""
+    torch unless given.  Under the forward's rules on the scores (C entry point
+    ``attn_varlen_bwd_rule``) pass the same ones; the slopes get no gradient."""
     _torch or _load_torch()
     if lse is None:
         raise ValueError("the backward needs the forward's lse (return_lse=True)")
@@ -379,8 +424,12 @@ def attn_varlen_bwd(dout, q, k, v, out, lse, cu_seqlens, causal: bool = True, sc
         workspace = _empty(max(need, 0), _torch.uint8, q.device, stream, returned=False)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
-    _launch(lib.attn_varlen_bwd, "attn_varlen_bwd", dev, stream, desc, _GRADS_PACK(*packed), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    rule = _rule(score_cap, distance_slopes, prefix_lens, q, dev, cu_seqlens.numel() - 1)
+    ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if rule is None:
+        _launch(lib.attn_varlen_bwd, "attn_varlen_bwd", dev, stream, desc, _GRADS_PACK(*packed), ws, nbytes)
+    else:
+        _launch(lib.attn_varlen_bwd_rule, "attn_varlen_bwd_rule", dev, stream, desc, _GRADS_PACK(*packed), rule, ws, nbytes)
     return tuple(grads[1:])
 
 
@@ -404,18 +453,24 @@ def _attn_function():
         """Autograd wrapper of the packed attention: q, k, v, out and lse are saved."""
 
         @staticmethod
-        def forward(ctx, q, k, v, cu_seqlens, causal, scale, seq_used):
-            out, lse = attn_varlen_fwd(q, k, v, cu_seqlens, causal, scale, seq_used, return_lse=True)
-            ctx.save_for_backward(q, k, v, out, lse, cu_seqlens, seq_used)
+        def forward(ctx, q, k, v, cu_seqlens, causal, scale, seq_used, score_cap=0.0, distance_slopes=None,
+                    prefix_lens=None):
+            rule = {}                                          # of the scores, where there is one
+            if score_cap != 0 or distance_slopes is not None or prefix_lens is not None:
+                rule = dict(score_cap=score_cap, distance_slopes=distance_slopes, prefix_lens=prefix_lens)
+            out, lse = attn_varlen_fwd(q, k, v, cu_seqlens, causal, scale, seq_used, return_lse=True, **rule)
+            ctx.save_for_backward(q, k, v, out, lse, cu_seqlens, seq_used, distance_slopes, prefix_lens)
             ctx.args = (causal, scale)
+            ctx.score_cap = score_cap
             return out
 
         @staticmethod
         @torch.autograd.function.once_differentiable       # the kernels have no second derivative
         def backward(ctx, dout):
-            q, k, v, out, lse, cu_seqlens, seq_used = ctx.saved_tensors
-            dq, dk, dv = attn_varlen_bwd(_rows(dout), q, k, v, out, lse, cu_seqlens, *ctx.args, seq_used=seq_used)
-            return dq, dk, dv, None, None, None, None
+            q, k, v, out, lse, cu_seqlens, seq_used, slopes, prefix = ctx.saved_tensors
+            dq, dk, dv = attn_varlen_bwd(_rows(dout), q, k, v, out, lse, cu_seqlens, *ctx.args, seq_used=seq_used,
+                                         score_cap=ctx.score_cap, distance_slopes=slopes, prefix_lens=prefix)
+            return dq, dk, dv, None, None, None, None, None, None, None
 
     return Attn
 
@@ -428,12 +483,16 @@ def _rows(t):
     return t if ok else t.clone(memory_format=__import__("torch").contiguous_format)
 
 
-def apply_attn(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] = None, seq_used=None):
+def apply_attn(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] = None, seq_used=None,
+               score_cap: float = 0.0, distance_slopes=None, prefix_lens=None):
     """Differentiable attention within each sample of a pack: ``attn_varlen_fwd`` with the
     gradients of ``attn_varlen_bwd``.  q, k, v may be any bf16 CUDA [T, heads, d] tensors;
     those that the kernels cannot address (broadcast ones) are copied.  Differentiable once: a
-    second derivative raises an error."""
+    second derivative raises an error.  ``distance_slopes`` that require a gradient are refused."""
     global _Attn
     if _Attn is None:
         _Attn = _attn_function()
-    return _Attn.apply(_rows(q), _rows(k), _rows(v), cu_seqlens, bool(causal), scale, seq_used)
+    if distance_slopes is not None and distance_slopes.requires_grad:
+        raise ValueError("distance_slopes are constants: they get no gradient")
+    return _Attn.apply(_rows(q), _rows(k), _rows(v), cu_seqlens, bool(causal), scale, seq_used, score_cap,
+                       distance_slopes, prefix_lens)

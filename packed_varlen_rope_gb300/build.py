@@ -11,10 +11,12 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", n) for n in ("rope_qk.cu", "rope_host.cu", "glu.cu", "rope_append.cu",
                                                  "rope_axes.cu", "paged_step.cu",
                                                  "attn.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu")]
+# the attention kernels are compiled once for every rule on the scores (csrc/score_rule.cuh)
+RULES = {"attn_fwd.cu": (0, 1, 2, 4, 6), "attn_bwd.cu": (0, 1, 2, 4, 6), "attn_decode.cu": (0, 1, 2, 4, 6)}
 HEADERS = [os.path.join(ROOT, "include", n) for n in ("rope_qk.h", "glu.h", "paged_kv.h", "attn.h", "rope_axes.h",
                                                        "paged_step.h")] + \
           [os.path.join(HERE, "csrc", n) for n in ("fastdiv.cuh", "cos_sin.cuh", "rope_core.cuh", "host_checks.h",
-                                                   "paged_checks.h", "attn_internal.h", "tensor_core.cuh", "tensor_map.h")]
+                                                   "paged_checks.h", "attn_internal.h", "tensor_core.cuh", "tensor_map.h", "score_rule.cuh")]
 LIB_PATH = os.path.join(HERE, "librope_qk.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -45,14 +47,15 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile the CUDA library if it is missing or older than its sources."""
     if force or verbose_ptxas or stale():
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
-        # one compiler process per source, side by side, then the link
-        objs = [tmp + "." + os.path.basename(src) + ".o" for src in SOURCES]
-        jobs = [subprocess.Popen([nvcc(), *flags(verbose_ptxas), "-c", src, "-o", obj])
-                for src, obj in zip(SOURCES, objs)]
+        # one compiler process per source and rule, side by side, then the link
+        units = [(src, rule) for src in SOURCES for rule in RULES.get(os.path.basename(src), (0,))]
+        objs = [tmp + ".%s.%d.o" % (os.path.basename(src), rule) for src, rule in units]
+        jobs = [subprocess.Popen([nvcc(), *flags(verbose_ptxas), *(["-DPVR_SCORE_RULE=%d" % rule] if rule else []),
+                                  "-c", src, "-o", obj]) for (src, rule), obj in zip(units, objs)]
         try:
-            for job, src in zip(jobs, SOURCES):
+            for job, (src, rule) in zip(jobs, units):
                 if job.wait() != 0:
-                    raise subprocess.CalledProcessError(job.returncode, "nvcc -c " + src)
+                    raise subprocess.CalledProcessError(job.returncode, "nvcc -c %s (rule %d)" % (src, rule))
             subprocess.check_call([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp])
             os.replace(tmp, LIB_PATH)
         finally:

@@ -71,6 +71,25 @@ int varlen_problem(const attn_varlen_desc &p, AttnProblem &a, View (&in)[3], Vie
     return ROPE_OK;
 }
 
+// The rule of a call, NULL for none.
+int set_rule(const attn_score_rule *rule, AttnProblem &a)
+{
+    if (rule == nullptr) return ROPE_OK;
+    if (rule->reserved != 0) return ROPE_ERR_UNSUPPORTED;
+    if (rule->cap != 0.0f) {
+        const float ratio = 2.0f * 1.45f * (a.scale / rule->cap);
+        if (!(rule->cap > 0.0f) || !std::isnormal(rule->cap) || !std::isfinite(1.45f * rule->cap) || !std::isnormal(a.scale / rule->cap) ||
+            !std::isfinite(ratio))
+            return ROPE_ERR_THETA;
+    }
+    if (!aligned(rule->slopes, 4) || !aligned(rule->prefix, 4)) return ROPE_ERR_ALIGN;
+    if (rule->prefix != nullptr && !a.causal) return ROPE_ERR_UNSUPPORTED;
+    a.cap = rule->cap;
+    a.slopes = rule->slopes;
+    a.prefix = a.n_seqs > 0 ? rule->prefix : nullptr;
+    return ROPE_OK;
+}
+
 // Sizes of a paged call.
 int check_paged_sizes(const attn_paged_desc &p)
 {
@@ -111,13 +130,15 @@ PagedPlan plan_of(const attn_paged_desc &p)
 
 extern "C" {
 
-int attn_varlen_fwd(const attn_varlen_desc *desc, void *stream)
+int attn_varlen_fwd(const attn_varlen_desc *desc, void *stream) { return attn_varlen_fwd_rule(desc, nullptr, stream); }
+
+int attn_varlen_fwd_rule(const attn_varlen_desc *desc, const attn_score_rule *rule, void *stream)
 {
     if (desc == nullptr) return ROPE_ERR_NULL;
     AttnProblem a;
     View in[3], out;
-    const int rc = varlen_problem(*desc, a, in, out);
-    if (rc != ROPE_OK || desc->total_tokens == 0) return rc;
+    int rc = varlen_problem(*desc, a, in, out);
+    if (rc != ROPE_OK || desc->total_tokens == 0 || (rc = set_rule(rule, a)) != ROPE_OK) return rc;
     if (!aligned(a.lse, 4)) return ROPE_ERR_ALIGN;
     return status_of(launch_attn_fwd(a, 1, nullptr, static_cast<cudaStream_t>(stream)));
 }
@@ -131,12 +152,18 @@ int64_t attn_varlen_bwd_workspace_bytes(int64_t total_tokens, int32_t n_q_heads)
 int attn_varlen_bwd(const attn_varlen_desc *desc, const attn_varlen_grads *grads, void *workspace,
                     int64_t workspace_bytes, void *stream)
 {
+    return attn_varlen_bwd_rule(desc, grads, nullptr, workspace, workspace_bytes, stream);
+}
+
+int attn_varlen_bwd_rule(const attn_varlen_desc *desc, const attn_varlen_grads *grads, const attn_score_rule *rule,
+                         void *workspace, int64_t workspace_bytes, void *stream)
+{
     if (desc == nullptr || grads == nullptr) return ROPE_ERR_NULL;
     AttnProblem a;
     View in[5], out;
     View qkv[3];
     int rc = varlen_problem(*desc, a, qkv, out);
-    if (rc != ROPE_OK || desc->total_tokens == 0) return rc;
+    if (rc != ROPE_OK || desc->total_tokens == 0 || (rc = set_rule(rule, a)) != ROPE_OK) return rc;
     const int64_t T = desc->total_tokens, d = desc->head_dim;
     const attn_varlen_grads &g = *grads;
     for (int i = 0; i < 3; ++i) in[i] = qkv[i];
@@ -174,6 +201,12 @@ int64_t attn_paged_workspace_bytes(const attn_paged_desc *desc)
 }
 
 int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return attn_paged_rule(desc, nullptr, workspace, workspace_bytes, stream);
+}
+
+int attn_paged_rule(const attn_paged_desc *desc, const attn_score_rule *rule, void *workspace, int64_t workspace_bytes,
+                    void *stream)
 {
     if (desc == nullptr) return ROPE_ERR_NULL;
     const attn_paged_desc &p = *desc;
@@ -218,6 +251,7 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
     a.d = c.head_dim;
     a.causal = p.causal != 0;
     a.scale = p.scale;
+    if ((rc = set_rule(rule, a)) != ROPE_OK) return rc;
     float *ws = static_cast<float *>(workspace);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return status_of(plan.decode.use ? launch_attn_decode(a, plan.decode, ws, st)

@@ -37,8 +37,10 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_internal.h"
+#include "score_rule.cuh"
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
@@ -62,6 +64,7 @@ struct BwdArgs {
     int32_t n_tokens, n_seqs, hq, hkv, group, d, causal, n_slots;
     FastDiv div_tile;                      // by kTile
     float scale;
+    ScoreRule rule;
 };
 
 template <int DP>
@@ -164,10 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const bool live = where.tile >= 0 && first < len;
     const int rows = min(len, max(where.used, 0));           // rows (and keys) in use
     // streamed tiles [y_lo, y_hi) of each pass; a pass for every head of the group
+    const int prefix = prefix_of(a.rule, where.sample, a.n_seqs, rows);   // keys that all rows see
     int y_lo = 0, y_hi = 0;
     if (live && first < rows) {
-        if (KEYS && a.causal) y_lo = where.tile;
-        y_hi = ((!KEYS && a.causal ? min(rows, first + kTile) : rows) + kTile - 1) / kTile;
+        if (KEYS && a.causal && first >= prefix) y_lo = where.tile;
+        y_hi = ((!KEYS && a.causal ? max(min(rows, first + kTile), prefix) : rows) + kTile - 1) / kTile;
     }
     const int per_pass = y_hi - y_lo;
     const int n_all = per_pass * (KEYS ? a.group : 1);       // the cluster's
@@ -359,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + 32 * quarter, t_p = tmem + lanes + kColP + 32 * quarter;
         const int xi = first + row;                                    // key or query of the sample
-        const float c = a.scale * kLog2e;
+        const float c = kCap ? a.rule.k : a.scale * kLog2e;            // of a tanh, or of a score
+        int head = KEYS ? xhead * a.group + head0 : xhead;             // the query head of the tile
         float2 mine = make_float2(-INFINITY, 0.0f);
         if (!KEYS && live && xi < rows)
             mine = a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi];
@@ -373,23 +378,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         int y = y0_first;
         for (int t = 0; t < n_tiles; ++t) {
             const int y0 = y * kTile + 32 * quarter;                   // this thread's first column
-            if (++y == y_hi) y = y_lo;
+            const float slope2 = kBias ? a.rule.slopes[head] * kLog2e : 0.0f;
+            if (++y == y_hi) {
+                y = y_lo;
+                if (KEYS) ++head;
+            }
             const uint32_t st = base + Sh::kOffStats + (t & 1) * 2 * kTile * 4 + 128 * quarter;
             // of its columns, [from, to) are visible: keys of a query row, or queries of a key row
             int from = 0, to = 32;
             bool masked;
             if (KEYS) {
-                masked = a.causal && y0 < first + kTile;
-                if (a.causal) from = xi - y0;
+                masked = a.causal && y0 < first + kTile && first + kTile > prefix;
+                if (a.causal) from = xi < prefix ? 0 : xi - y0;
             } else {
-                masked = y0 + 32 > (a.causal ? min(rows, first + 1) : rows);
-                to = min(rows, a.causal ? xi + 1 : rows) - y0;
+                masked = y0 + 32 > (a.causal ? max(min(rows, first + 1), prefix) : rows);
+                to = min(rows, a.causal ? max(xi + 1, prefix) : rows) - y0;
             }
             ok = warp_wait(s_full, t & 1, &s_abort, &g_attn_bwd_fault);
             if (KEYS && ok) ok = warp_wait(st_full + 8 * (t & 1), (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
             if (!ok && !single) break;         // (a single tile's warps meet below in any case)
             tc_fence_after();
             uint32_t s[32], packed[16];
+            // how far the first column is from this row: the bias takes its magnitude
+            const float far = static_cast<float>(y0 - xi);
             tmem_ld32(t_s, s);
             tc_wait_ld(s);
             if (!KEYS) {                                               // S is free
@@ -397,25 +408,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
             }
+            // wide: capped scores past the fit of the tanh are among the warp's
+            auto weights = [&](auto wide) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = j + 2 * h;
-                    float2 p = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2,
-                                    h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w));
-                    p.x = ex2(p.x);
-                    p.y = ex2(p.y);
-                    if (masked) {
-                        if (e < from || e >= to) p.x = 0.0f;
-                        if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = j + 2 * h;
+                        const float2 n2 = h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w);
+                        float2 p = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), factor;
+                        if (kCap) p = tanh2<decltype(wide)::value>(a.rule, p, factor);
+                        if (kBias) {
+                            p = fma2(p, c2, bias2(slope2, make_float2(far + e, far + (e + 1))));
+                            p = add2(p, n2);
+                        } else {
+                            p = fma2(p, c2, n2);
+                        }
+                        p.x = ex2(p.x);
+                        p.y = ex2(p.y);
+                        if (masked) {
+                            if (e < from || e >= to) p.x = 0.0f;
+                            if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
+                        }
+                        packed[e / 2] = pack_bf16(p.x, p.y);
+                        if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2)
+                        s[e] = __float_as_uint(p.x);
+                        s[e + 1] = __float_as_uint(p.y);
                     }
-                    s[e] = __float_as_uint(p.x);
-                    s[e + 1] = __float_as_uint(p.y);
-                    packed[e / 2] = pack_bf16(p.x, p.y);
                 }
-            }
+            };
+            if (kCap && any_wide(a.rule, s)) weights(std::true_type{});
+            else weights(std::false_type{});
             // P and dS take the first half of the columns this thread has read
             if (KEYS) {
                 tmem_st16(t_s, packed);
@@ -433,8 +457,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             tc_wait_ld(dp);
             if (single) {
                 float sum[2] = {0.0f, 0.0f};
+                if (kCap) {
+                    // the weights again, from the scores: S is read for the last time
 #pragma unroll
-                for (int e = 0; e < 32; ++e) sum[e & 1] = fmaf(__uint_as_float(s[e]), __uint_as_float(dp[e]), sum[e & 1]);
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t again[16];
+                        tmem_ld16(t_s + 16 * j, again);
+                        tc_wait_ld16(again);
+                        shape_any(a.rule, again, slope2, far + 16 * j);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int col = 16 * j + e;
+                            float p = ex2(__uint_as_float(again[e]) + mine.x);
+                            if (masked && (col < from || col >= to)) p = 0.0f;
+                            sum[e & 1] = fmaf(p, __uint_as_float(dp[col]), sum[e & 1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[e & 1] = fmaf(__uint_as_float(s[e]), __uint_as_float(dp[e]), sum[e & 1]);
+                }
                 float *swap = reinterpret_cast<float *>(smem + Sh::kOffStats);   // [quarter][row]
                 swap[quarter * kTile + row] = sum[0] + sum[1];
                 named_barrier(1 + (warp & 3), 128);
@@ -558,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     }
 }
 
+#if PVR_SCORE_RULE == 0
 // (-lse log2(e), -D) of every (head, token) row, D = dout . out.  Eight lanes a row, 16
 // elements each (head_dim <= 128); HBM-bound.  The grid is resident while the kernel that
 // writes out and lse ends, so they are no read-only data: no __ldg and no __restrict__, here
@@ -595,6 +638,8 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const __nv_bfloat16 *do
         stats[at] = x == -INFINITY ? make_float2(-INFINITY, 0.0f) : make_float2(-x * kLog2e, -sum);
     }
 }
+
+#endif
 
 void plain_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned grid, unsigned threads, size_t smem,
                   cudaStream_t stream)
@@ -670,6 +715,7 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
     a.causal = p.causal;
     a.n_slots = slot_count(p.n_tokens, p.n_seqs, kTile);
     a.scale = p.scale;
+    a.rule = rule_of(p);
     a.div_tile = make_fastdiv(kTile);
     const int ranks = KEYS ? key_cluster(p) : 1;
     cudaLaunchConfig_t cfg;
@@ -687,6 +733,7 @@ cudaError_t launch_pass(const AttnProblem &p, cudaStream_t stream)
 
 }  // namespace
 
+#if PVR_SCORE_RULE == 0
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg;
@@ -698,13 +745,26 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t stream)
                                          static_cast<const float *>(p.lse), reinterpret_cast<float2 *>(p.stats),
                                          static_cast<int>(p.n_tokens), static_cast<int>(p.hq), static_cast<int>(p.d));
     if (err != cudaSuccess) return err;
+    return for_rule(p.rule(), [&](auto rule) { return launch_attn_bwd_rule<decltype(rule)::value>(p, stream); });
+}
+
+int attn_bwd_fault_word(int *word)
+{
+    return sum_fault_words(word, [](auto rule, int *w) { return attn_bwd_fault_of<decltype(rule)::value>(w); });
+}
+#endif
+
+template <>
+cudaError_t launch_attn_bwd_rule<kRule>(const AttnProblem &p, cudaStream_t stream)
+{
     // dq first: it improves the statistics that the pass over the keys reads
-    err = p.d <= 64 ? launch_pass<64, false>(p, stream) : launch_pass<128, false>(p, stream);
+    const cudaError_t err = p.d <= 64 ? launch_pass<64, false>(p, stream) : launch_pass<128, false>(p, stream);
     if (err != cudaSuccess) return err;
     return p.d <= 64 ? launch_pass<64, true>(p, stream) : launch_pass<128, true>(p, stream);
 }
 
-int attn_bwd_fault_word(int *word)
+template <>
+int attn_bwd_fault_of<kRule>(int *word)
 {
     return read_fault_word(word, g_attn_bwd_fault);
 }

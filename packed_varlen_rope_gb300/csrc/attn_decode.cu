@@ -26,6 +26,7 @@
 
 #include "attn_internal.h"
 #include "fastdiv.cuh"
+#include "score_rule.cuh"
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
@@ -52,6 +53,7 @@ struct DecodeArgs {
     int32_t n_tokens, n_seqs, hq, hkv, group, d, causal, tile_tokens, splits;
     FastDiv div_page, div_tile, div_group;
     float scale;
+    ScoreRule rule;
 };
 
 template <int DP, int WARPS>
@@ -125,9 +127,11 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
     const int kv = inside ? max(f.used, -1) : 0;
     const int keys = inside ? min(max(kv, 0), a.max_pages * a.page_size) : 0;
     const int offset = kv - len;
+    const int prefix = prefix_of(a.rule, f.sample, a.n_seqs, keys);
     auto limit = [&](int i) {                                // keys that row i of the sample sees
         if (!inside || i >= len || i + offset < 0) return 0;
-        return a.causal ? min(keys, i + offset + 1) : keys;
+        const int own = a.causal ? min(keys, i + offset + 1) : keys;
+        return kRuled ? max(own, prefix) : own;
     };
     const int n_tok = min(a.tile_tokens, len - first);
     const int n_rows = n_tok * a.group;
@@ -175,11 +179,14 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
     find_page(chunk + (kStages - 1) * step);
 
     // this lane's rows of the m16 tile: lane / 4 and that + 8
-    int lim[2];
+    int lim[2], own_key[2];
+    float slope2[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int row = (lane >> 2) + 8 * r;
-        lim[r] = row < n_rows ? limit(first + static_cast<int>(fast_div(row, a.div_group))) : 0;
+        const int row = (lane >> 2) + 8 * r, tok_in = static_cast<int>(fast_div(row, a.div_group));
+        lim[r] = row < n_rows ? limit(first + tok_in) : 0;
+        own_key[r] = first + tok_in + offset;
+        slope2[r] = kBias && row < n_rows ? a.rule.slopes[kvh * a.group + row - tok_in * a.group] * kLog2e : 0.0f;
     }
     // ldmatrix addresses: matrix lane / 8, row lane % 8
     const int mi = lane >> 3, mr = lane & 7;
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    const float c = a.scale * kLog2e;
+    const float c = kShaped ? 1.0f : a.scale * kLog2e;       // shaped scores are exponents of 2
 
     int stage = 0, turn = 0;
     for (; ok && chunk < n_chunks; chunk += step) {
@@ -240,6 +247,17 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
             }
         }
         bool grew = false;
+        if (kShaped) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {                // two neighbouring keys of a row
+                    uint32_t x[2] = {__float_as_uint(s[n][2 * r]), __float_as_uint(s[n][2 * r + 1])};
+                    shape<true>(a.rule, x, slope2[r], static_cast<float>(chunk * kKeys + 8 * n + 2 * (lane & 3) - own_key[r]));
+                    s[n][2 * r] = __uint_as_float(x[0]);
+                    s[n][2 * r + 1] = __uint_as_float(x[1]);
+                }
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -405,6 +423,7 @@ cudaError_t launch(const DecodeArgs &a, int cluster, int slots, cudaStream_t str
 
 }  // namespace
 
+#if PVR_SCORE_RULE == 0
 DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv)
 {
     DecodePlan plan;
@@ -442,6 +461,18 @@ DecodePlan attn_decode_plan(const AttnProblem &p, int64_t max_kv)
 
 cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream)
 {
+    return for_rule(p.rule(), [&](auto rule) { return launch_attn_decode_rule<decltype(rule)::value>(p, plan, workspace, stream); });
+}
+
+int attn_decode_fault_word(int *word)
+{
+    return sum_fault_words(word, [](auto rule, int *w) { return attn_decode_fault_of<decltype(rule)::value>(w); });
+}
+#endif
+
+template <>
+cudaError_t launch_attn_decode_rule<kRule>(const AttnProblem &p, const DecodePlan &plan, float *workspace, cudaStream_t stream)
+{
     DecodeArgs a;
     const int tile = kRows / p.group;
     a.box_rows = p.pages.page_size % kKeys == 0 ? kKeys : 8;
@@ -469,6 +500,7 @@ cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, flo
     a.div_group = make_fastdiv(static_cast<uint32_t>(p.group));
     a.div_page = make_fastdiv(static_cast<uint32_t>(p.pages.page_size));
     a.scale = p.scale;
+    a.rule = rule_of(p);
     const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;
     a.part_o = workspace;
     a.part_lse = plan.splits > 1 ? workspace + plan.splits * rows * p.d : nullptr;
@@ -481,7 +513,8 @@ cudaError_t launch_attn_decode(const AttnProblem &p, const DecodePlan &plan, flo
     return launch_attn_join(a.part_o, a.part_lse, p, plan.splits, stream);
 }
 
-int attn_decode_fault_word(int *word)
+template <>
+int attn_decode_fault_of<kRule>(int *word)
 {
     return read_fault_word(word, g_attn_decode_fault);
 }

@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "attn_internal.h"
+#include "score_rule.cuh"
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
@@ -72,6 +73,7 @@ struct FwdArgs {
     int32_t n_slots, splits;
     FastDiv div_cta, div_group;         // by the CTA's tokens, by group
     float scale;
+    ScoreRule rule;
 };
 
 template <int DP>
@@ -159,10 +161,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         keys = rows_used;
         offset = 0;
     }
-    // keys that row `i` of the sample sees (a prefix)
+    const int prefix = prefix_of(a.rule, where.sample, a.n_seqs, keys);
+    // keys that row `i` of the sample sees: the first so many
     auto limit = [&](int i) {
         if (i >= rows_used || i + offset < 0) return 0;
-        return a.causal ? min(keys, i + offset + 1) : keys;
+        const int own = a.causal ? min(keys, i + offset + 1) : keys;
+        return kRuled ? max(own, prefix) : own;
     };
     int count[2], lo_tile = 0, n_tiles = 0;
     {
@@ -179,7 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
         for (int x = 0; x < 2; ++x) count[x] = max(0, min(n[x], hi) - lo_tile);
         n_tiles = max(count[0], count[1]);
+        // biased scores: both row tiles start with the last key tile, the earlier one hiding it
+        if (kBias)
+            for (int x = 0; x < 2; ++x)
+                if (count[x] > 0) count[x] = n_tiles;
     }
+    // Key tiles go upwards; with a bias by distance downwards, so that causal rows meet their
+    // largest exponents first and hardly ever rescale.
+    auto tile_at = [&](int i) { return kBias ? n_tiles - 1 - i : i; };
     constexpr uint32_t kColS = 0, kColO = 256;
 
     if (n_tiles == 0) {
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int box = lane % (PAGED ? per_tile : 1), col = lane / (PAGED ? per_tile : 1);
         int issued = 0;
         for (int i = 0; i < n_tiles; ++i) {
-            const int key0 = (lo_tile + i) * kKeys;
+            const int key0 = (lo_tile + tile_at(i)) * kKeys;
             int c_slot = where.start + key0, c_page = 0;
             if (PAGED) {
                 // keys past the sequence's end read as zero: a page coordinate past the pool's
@@ -267,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             ok = full(t);
             // value rows past the last key (another sample's, or stale) are cleared: their
             // weights are zero, but zero times NaN is not
-            const int valid = keys - (lo_tile + i) * kKeys;
+            const int valid = keys - (lo_tile + tile_at(i)) * kKeys;
             if (ok && valid < kKeys) {
                 uint8_t *v = smem + Sh::kOffKV + (t % kStages) * Sh::kTileBytes;
                 for (int r = valid + (lane >> 3); r < kKeys; r += 4)
@@ -359,16 +370,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         // from the CTA's first key on: keys that every row of the tile sees, and that this
         // thread's columns of the row see
         const int whole = limit(tok0) - lo_tile * kKeys, visible = lim - lo_tile * kKeys - 64 * half;
-        const float c = a.scale * kLog2e;
+        const float c = kShaped ? 1.0f : a.scale * kLog2e;             // shaped scores are exponents of 2
+        const float slope2 = !kBias || !mine ? 0.0f
+            : a.rule.slopes[kvh * a.group + row - static_cast<int>(fast_div(row, a.div_group)) * a.group] * kLog2e;
+        const int row_key = i_tok + offset - lo_tile * kKeys - 64 * half;   // this row's own key, from this thread's first
         float m = -INFINITY, l = 0.0f, mc = 0.0f;
         bool ok = true;
         bool folded = false;                                           // m is known, and small
-        // 32 of this thread's scores of tile i, those it does not see at -infinity
+        // 32 of this thread's scores of step i, those it does not see at -infinity
         auto load = [&](int i, int h, uint32_t(&s)[32]) {
             tmem_ld32(t_s + 32 * h, s);
             tc_wait_ld(s);
-            if ((i + 1) * kKeys > whole) {
-                const int left = visible - i * kKeys - 32 * h;
+            if (kShaped) shape_any(a.rule, s, slope2, static_cast<float>(tile_at(i) * kKeys + 32 * h - row_key));
+            if ((tile_at(i) + 1) * kKeys > whole) {
+                const int left = visible - tile_at(i) * kKeys - 32 * h;
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (j >= left) s[j] = 0xff800000u;
@@ -439,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 m = grown;
                 const float shift = m == -INFINITY ? 0.0f : m;
                 mc = shift * c;
-                folded = __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
+                // (the difference of two exponents is exact where it matters, however large they are)
+                folded = kShaped || __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
                 sum = 0.0f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 a.part_lse[static_cast<int64_t>(split) * a.n_tokens * a.hq + at] =
                     l == 0.0f ? -INFINITY : m * c + log2f(l);
             } else if (a.lse != nullptr) {
-                a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l == 0.0f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
+                a.lse[static_cast<int64_t>(head) * a.n_tokens + tok] = l == 0.0f ? -INFINITY : (kShaped ? m * kLn2 : m * a.scale) + kLn2 * log2f(l);
             }
         }
         const int col0 = half * (DP / 2);
@@ -542,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
 }
 
+#if PVR_SCORE_RULE == 0
 // Joins the partial results of the splits: o = sum_i w_i o_i, w_i = 2^(lse_i - lse).  One
 // warp a row, 4 elements a lane.  A part whose lse is -infinity holds no weight and nothing
 // was written for it; one of NaN (which the maximum passes over) makes the row NaN.  The grid
@@ -582,6 +599,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const float *part_o, con
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
+#endif
+
 template <int DP, bool PAGED>
 cudaError_t launch_fwd(const FwdArgs &a, cudaStream_t stream)
 {
@@ -603,6 +622,7 @@ cudaError_t launch_fwd(const FwdArgs &a, cudaStream_t stream)
 
 }  // namespace
 
+#if PVR_SCORE_RULE == 0
 // Splits of the keys: enough CTAs to fill the GPU, at least two key tiles a split.
 int attn_fwd_splits(const AttnProblem &p, int64_t max_kv)
 {
@@ -615,6 +635,13 @@ int attn_fwd_splits(const AttnProblem &p, int64_t max_kv)
 }
 
 cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, cudaStream_t stream)
+{
+    return for_rule(p.rule(), [&](auto rule) { return launch_attn_fwd_rule<decltype(rule)::value>(p, splits, workspace, stream); });
+}
+#endif
+
+template <>
+cudaError_t launch_attn_fwd_rule<kRule>(const AttnProblem &p, int splits, float *workspace, cudaStream_t stream)
 {
     FwdArgs a;
     const int dp = p.d <= 64 ? 64 : 128;
@@ -657,6 +684,7 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, 
     a.div_group = make_fastdiv(static_cast<uint32_t>(p.group));
     a.div_cta = make_fastdiv(static_cast<uint32_t>(2 * tile));
     a.scale = p.scale;
+    a.rule = rule_of(p);
     const int64_t rows = static_cast<int64_t>(p.n_tokens) * p.hq;
     a.part_o = workspace;
     a.part_lse = splits > 1 ? workspace + splits * rows * p.d : nullptr;
@@ -667,6 +695,13 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, 
     return launch_attn_join(a.part_o, a.part_lse, p, splits, stream);
 }
 
+template <>
+int attn_fwd_fault_of<kRule>(int *word)
+{
+    return read_fault_word(word, g_attn_fault);
+}
+
+#if PVR_SCORE_RULE == 0
 cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const AttnProblem &p, int splits,
                              cudaStream_t stream)
 {
@@ -686,7 +721,8 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, const A
 
 int attn_fault_word(int *word)
 {
-    return read_fault_word(word, g_attn_fault);
+    return sum_fault_words(word, [](auto rule, int *w) { return attn_fwd_fault_of<decltype(rule)::value>(w); });
 }
+#endif
 
 }  // namespace pvr
