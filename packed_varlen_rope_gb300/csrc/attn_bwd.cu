@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             }
             // wide: capped scores past the fit of the tanh are among the warp's
             auto weights = [&](auto wide) {
+                Bias bias(slope2, far);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         float2 p = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), factor;
                         if (kCap) p = tanh2<decltype(wide)::value>(a.rule, p, factor);
                         if (kBias) {
-                            p = fma2(p, c2, bias2(slope2, make_float2(far + e, far + (e + 1))));
+                            p = fma2(p, c2, bias.next());
                             p = add2(p, n2);
                         } else {
                             p = fma2(p, c2, n2);

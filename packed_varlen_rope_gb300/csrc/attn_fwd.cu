@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (ok && elect_one()) {
 #pragma unroll
                     for (int s = 0; s < kKeys / 16; ++s)
-                        mma_ts(utmem + kColO + x * DP, utmem + kColS + x * kKeys + s * 8, d_v + sv * kStep + s * (2048 >> 4),
+                        mma_ts(utmem + kColO + x * DP, utmem + kColS + x * kKeys + s * 8 + (kShaped && s >= 4 ? 32 : 0), d_v + sv * kStep + s * (2048 >> 4),
                                kDescO, i > 0 || s > 0);
                     if (i + 1 == count[x]) tc_commit(o_done + 8 * x);
                     else scores(x, sk);
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int pair = 1 + x * 4 + (warp & 3);                       // the two warps' barrier
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + x * kKeys + half * 64;
-        const uint32_t t_p = tmem + lanes + kColS + x * kKeys + half * 32;
+        // P of a half over S of both; shaped scores: over the half's own S alone
+        const uint32_t t_p = tmem + lanes + kColS + x * kKeys + half * (kShaped ? 64 : 32);
         const uint32_t t_o = tmem + lanes + kColO + x * DP + half * (DP / 2);
         const int tok0 = first + x * a.tile_tokens;                    // of the sample
         const int i_tok = tok0 + static_cast<int>(fast_div(row, a.div_group));
@@ -381,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         auto load = [&](int i, int h, uint32_t(&s)[32]) {
             tmem_ld32(t_s + 32 * h, s);
             tc_wait_ld(s);
-            if (kShaped) shape_any(a.rule, s, slope2, static_cast<float>(tile_at(i) * kKeys + 32 * h - row_key));
             if ((tile_at(i) + 1) * kKeys > whole) {
                 const int left = visible - tile_at(i) * kKeys - 32 * h;
 #pragma unroll
@@ -410,6 +410,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
+        // shaped scores, 16 at a time: few live registers, as every spilled one costs a trip to L2
+        auto load16 = [&](int i, int h, uint32_t(&s)[16]) {
+            tmem_ld16(t_s + 16 * h, s);
+            tc_wait_ld16(s);
+            const int key0 = tile_at(i) * kKeys + 16 * h;
+            shape_any(a.rule, s, slope2, static_cast<float>(key0 - row_key));
+            if ((tile_at(i) + 1) * kKeys > whole) {
+                const int left = visible - key0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j >= left) s[j] = 0xff800000u;
+            }
+        };
+        auto highest16 = [&](const uint32_t(&s)[16]) {
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+                top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            return fmaxf(top[0], top[1]);
+        };
+        auto weights16 = [&](const uint32_t(&s)[16], uint32_t *p, float fixed) {
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 x = add2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), twice(-fixed));
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[j & 1] = add2(sum[j & 1], x);
+                p[j] = pack_bf16(x.x, x.y);
+            }
+            return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        };
+        // Capped exponents that stay within +-80 need no maximum: weights within 2^+-80 and sums of
+        // 2^24 of them keep their precision in binary32, and the two halves of a row never meet.
+        if (kCap && !kBias && a.rule.fixed) {
+            m = 0.0f;
+            for (int i = 0; i < count[x]; ++i) {
+                if (ok) ok = warp_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
+                tc_fence_after();
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t s[16], p[8];
+                    load16(i, h, s);
+                    l += weights16(s, p, 0.0f);
+                    tmem_st8(t_p + 8 * h, p);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * x);
+            }
+        } else
         // after a wait that ran out the loop goes on without waiting, so that the pair's
         // barriers stay matched
         for (int i = 0; i < count[x]; ++i) {
@@ -419,12 +471,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             // rounding not to matter
             uint32_t p[32];
             float high = -INFINITY, sum = 0.0f;
+            if (kShaped) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t s[32];
-                load(i, h, s);
-                high = fmaxf(high, highest(s));
-                if (folded) sum += weights(s, p + 16 * h, mc);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t s[16];
+                    load16(i, h, s);
+                    high = fmaxf(high, highest16(s));
+                    if (folded) sum += weights16(s, p + 8 * h, mc);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t s[32];
+                    load(i, h, s);
+                    high = fmaxf(high, highest(s));
+                    if (folded) sum += weights(s, p + 16 * h, mc);
+                }
             }
             // rows that see no key may hold anything: they take no part in the warp's decisions
             if (lim == 0) high = -INFINITY;
@@ -457,13 +519,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 // (the difference of two exponents is exact where it matters, however large they are)
                 folded = kShaped || __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
                 sum = 0.0f;
+                if (kShaped) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t s[32];
-                    load(i, h, s);
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t s[16];
+                        load16(i, h, s);
+                        sum += weights16(s, p + 8 * h, shift);
+                    }
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
-                    sum += weights(s, p + 16 * h, 0.0f);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t s[32];
+                        load(i, h, s);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
+                        sum += weights(s, p + 16 * h, 0.0f);
+                    }
                 }
                 tc_fence_before();
                 named_barrier(pair, 64);

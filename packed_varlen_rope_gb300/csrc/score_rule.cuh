@@ -35,6 +35,7 @@ constexpr bool kShaped = kCap || kBias;      // scores are exponents of 2 before
 struct ScoreRule {
     float a, k, a2;                          // capped scores: scale / cap, cap log2(e), 2 log2(e) scale / cap
     float c;                                 // others: scale log2(e)
+    int32_t fixed;                           // capped exponents within +-80: no maximum is needed
     const float *slopes;                     // [hq]
     const int32_t *prefix;                   // [n_seqs], or NULL
 };
@@ -49,7 +50,8 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+// Both halves of a pair alike.
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 // tanh of two scores times a.  wide: some score of the warp is past the fit, so each takes the form
 // that is right for it (no branch of its own: what follows is for converged warps).  The factor is
@@ -57,13 +59,13 @@ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 template <bool WIDE>
 __device__ __forceinline__ float2 tanh2(const ScoreRule &r, float2 s, float2 &factor)
 {
-    const float2 u = mul2(s, pair(r.a)), z = mul2(u, u);
-    float2 p = fma2(z, pair(kTanh4), pair(kTanh3));
-    p = fma2(z, p, pair(kTanh2));
-    p = fma2(z, p, pair(kTanh1));
-    p = fma2(z, p, pair(kTanh0));
+    const float2 u = mul2(s, twice(r.a)), z = mul2(u, u);
+    float2 p = fma2(z, twice(kTanh4), twice(kTanh3));
+    p = fma2(z, p, twice(kTanh2));
+    p = fma2(z, p, twice(kTanh1));
+    p = fma2(z, p, twice(kTanh0));
     float2 t = mul2(u, p);
-    factor = fma2(t, mul2(t, pair(-1.0f)), pair(1.0f));
+    factor = fma2(t, mul2(t, twice(-1.0f)), twice(1.0f));
     if (WIDE) {
         const float qx = rcp(1.0f + ex2(s.x * r.a2)), qy = rcp(1.0f + ex2(s.y * r.a2));
         // (a NaN score takes the second form, and stays one)
@@ -76,40 +78,53 @@ __device__ __forceinline__ float2 tanh2(const ScoreRule &r, float2 s, float2 &fa
     return t;
 }
 
-// Whether some of the warp's scores is past the fit of the tanh (a NaN is not, and comes through).
+// The largest magnitude of N scores (NaN is passed over).
 template <int N>
-__device__ __forceinline__ bool any_wide(const ScoreRule &r, const uint32_t (&s)[N])
+__device__ __forceinline__ float largest(const uint32_t (&s)[N])
 {
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < N; j += 2)
         top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
-    return __any_sync(0xffffffffu, fmaxf(top[0], top[1]) * r.a > 1.0f);
+    return fmaxf(top[0], top[1]);
 }
 
-// The bias of two neighbouring columns, the first `distance` past the row: -slope2 |distance|.
-__device__ __forceinline__ float2 bias2(float slope2, float2 distance)
-{
-    return mul2(pair(-slope2), make_float2(fabsf(distance.x), fabsf(distance.y)));
-}
+// Biases of a thread's columns, a pair at a time, the first one `distance` past the row's own
+// place: -slope2 |distance|.  Distances are whole numbers and exact.
+struct Bias {
+    float2 at, slope;
+    __device__ __forceinline__ Bias(float slope2, float distance)
+        : at(make_float2(distance, distance + 1.0f)), slope(twice(-slope2)) {}
+    __device__ __forceinline__ float2 next()
+    {
+        const float2 x = mul2(slope, make_float2(fabsf(at.x), fabsf(at.y)));
+        at = add2(at, twice(2.0f));
+        return x;
+    }
+};
 
 // N scores, columns from `distance` past the row on, to exponents of 2, in place.
 template <bool WIDE, int N>
 __device__ __forceinline__ void shape(const ScoreRule &r, uint32_t (&s)[N], float slope2, float distance)
 {
+    Bias bias(slope2, distance);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         float2 x = make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), factor;
-        const float2 bias = kBias ? bias2(slope2, make_float2(distance + j, distance + (j + 1))) : pair(0.0f);
-        if (kCap) {
-            x = tanh2<WIDE>(r, x, factor);
-            x = kBias ? fma2(x, pair(r.k), bias) : mul2(x, pair(r.k));
-        } else {
-            x = fma2(x, pair(r.c), bias);
-        }
+        if (kCap) x = tanh2<WIDE>(r, x, factor);
+        const float2 scale = twice(kCap ? r.k : r.c);
+        x = kBias ? fma2(x, scale, bias.next()) : mul2(x, scale);
         s[j] = __float_as_uint(x.x);
         s[j + 1] = __float_as_uint(x.y);
     }
+}
+
+// Whether some score of a converged warp is past the fit of the tanh.  A thread that holds one may
+// have it in a place that nobody sees: the two forms give a score within the fit the same bits.
+template <int N>
+__device__ __forceinline__ bool any_wide(const ScoreRule &r, const uint32_t (&s)[N])
+{
+    return __any_sync(0xffffffffu, largest(s) * r.a > 1.0f);
 }
 
 template <int N>
@@ -137,6 +152,7 @@ inline ScoreRule rule_of(const AttnProblem &p)
         r.a2 = 2.0f * kLog2 * r.a;
     }
     r.c = p.scale * kLog2;
+    r.fixed = p.cap > 0.0f && p.slopes == nullptr && r.k <= 80.0f;
     r.slopes = p.slopes;
     r.prefix = p.prefix;
     return r;
