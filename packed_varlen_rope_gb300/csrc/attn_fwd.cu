@@ -411,17 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
         // shaped scores, 16 at a time: few live registers, as every spilled one costs a trip to L2
-        auto load16 = [&](int i, int h, uint32_t(&s)[16]) {
-            tmem_ld16(t_s + 16 * h, s);
-            tc_wait_ld16(s);
+        auto finish16 = [&](int i, int h, uint32_t(&s)[16]) {
             const int key0 = tile_at(i) * kKeys + 16 * h;
-            shape_any(a.rule, s, slope2, static_cast<float>(key0 - row_key));
+            float far = static_cast<float>(key0 - row_key);
+            asm volatile("" : "+f"(far));        // or the distances are kept for the second pass, in spilled registers
+            shape_any(a.rule, s, slope2, far);
             if ((tile_at(i) + 1) * kKeys > whole) {
                 const int left = visible - key0;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (j >= left) s[j] = 0xff800000u;
             }
+        };
+        auto load16 = [&](int i, int h, uint32_t(&s)[16]) {
+            tmem_ld16(t_s + 16 * h, s);
+            tc_wait_ld16(s);
+            finish16(i, h, s);
         };
         auto highest16 = [&](const uint32_t(&s)[16]) {
             float top[2] = {-INFINITY, -INFINITY};
@@ -449,11 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             for (int i = 0; i < count[x]; ++i) {
                 if (ok) ok = warp_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
                 tc_fence_after();
-#pragma unroll 1
+                uint32_t s[2][16];
+                tmem_ld16(t_s, s[0]);
+#pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    uint32_t s[16], p[8];
-                    load16(i, h, s);
-                    l += weights16(s, p, 0.0f);
+                    uint32_t p[8];
+                    tc_wait_ld16(s[h & 1]);
+                    if (h < 3) tmem_ld16(t_s + 16 * (h + 1), s[(h + 1) & 1]);
+                    finish16(i, h, s[h & 1]);
+                    l += weights16(s[h & 1], p, 0.0f);
                     tmem_st8(t_p + 8 * h, p);
                 }
                 tc_wait_st();
