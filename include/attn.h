@@ -173,7 +173,8 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
  * document that the whole sequence is about).  The backward has ds_ij (1 - tanh^2(u_ij / cap)) in
  * place of ds_ij where it sums dq and dk; slopes are constants of the model and get no gradient.
  *
- * A cap moves a score by less than 8e-6 of its distance from 0, computed in binary32.  A score of
+ * Computed in binary32: a cap puts a score within 8e-6 of the cap of where it belongs, a cap past
+ * 128 within 1e-6 of the score and 2^-21 of the cap where the score is larger than it.  A score of
  * +-infinity is capped like any other; a NaN comes out in its row.
  */
 typedef struct attn_score_rule {

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + 32 * quarter, t_p = tmem + lanes + kColP + 32 * quarter;
         const int xi = first + row;                                    // key or query of the sample
-        const float c = kCap ? a.rule.k : a.scale * kLog2e;            // of a tanh, or of a score
+        const float c = a.scale * kLog2e;
         int head = KEYS ? xhead * a.group + head0 : xhead;             // the query head of the tile
         float2 mine = make_float2(-INFINITY, 0.0f);
         if (!KEYS && live && xi < rows)
@@ -408,9 +408,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
             }
-            // wide: capped scores past the fit of the tanh are among the warp's
-            auto weights = [&](auto wide) {
-                Bias bias(slope2, far);
+            if (kCap && masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e < from || e >= to) s[e] = 0u;
+            }
+            by_form(a.rule, s, xi >= rows, [&](auto form) {
+                Tops<decltype(form)::value> tops(a.rule, slope2, far, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
@@ -418,14 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                     for (int h = 0; h < 2; ++h) {
                         const int e = j + 2 * h;
                         const float2 n2 = h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w);
-                        float2 p = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), factor;
-                        if (kCap) p = tanh2<decltype(wide)::value>(a.rule, p, factor);
-                        if (kBias) {
-                            p = fma2(p, c2, bias.next());
-                            p = add2(p, n2);
-                        } else {
-                            p = fma2(p, c2, n2);
-                        }
+                        const float2 score = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                        float2 p, factor;
+                        if (kShaped) p = exponent2<decltype(form)::value>(a.rule, score, add2(tops.next(), n2), factor);
+                        else p = fma2(score, c2, n2);
                         p.x = ex2(p.x);
                         p.y = ex2(p.y);
                         if (masked) {
@@ -433,14 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
                         }
                         packed[e / 2] = pack_bf16(p.x, p.y);
-                        if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2)
+                        if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2), here a quarter of it
                         s[e] = __float_as_uint(p.x);
                         s[e + 1] = __float_as_uint(p.y);
                     }
                 }
-            };
-            if (kCap && any_wide(a.rule, s)) weights(std::true_type{});
-            else weights(std::false_type{});
+            });
             // P and dS take the first half of the columns this thread has read
             if (KEYS) {
                 tmem_st16(t_s, packed);
@@ -454,26 +452,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             tc_fence_after();
             const uint32_t t_dp = t_p + (t & 1) * kNextP;
             uint32_t dp[32];
-            tmem_ld32(t_dp, dp);
-            tc_wait_ld(dp);
+            if (!kCap || !single) {
+                tmem_ld32(t_dp, dp);
+                tc_wait_ld(dp);
+            }
             if (single) {
                 float sum[2] = {0.0f, 0.0f};
                 if (kCap) {
-                    // the weights again, from the scores: S is read for the last time
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t again[16];
-                        tmem_ld16(t_s + 16 * j, again);
+                    // the weights again, from the scores (S is read for the last time): what s holds
+                    // has the tanh's factor in it
+#pragma unroll 1
+                    for (int j = 0; j < 32; j += 16) {
+                        uint32_t again[16], d[16];
+                        tmem_ld16(t_s + j, again);
+                        tmem_ld16(t_dp + j, d);
                         tc_wait_ld16(again);
-                        shape_any(a.rule, again, slope2, far + 16 * j);
+                        tc_wait_ld16(d);
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (j + e < from || j + e >= to) again[e] = 0u;
+                        }
+                        by_form(a.rule, again, xi >= rows, [&](auto form) {
+                            shape<decltype(form)::value>(a.rule, again, slope2, far + j, -mine.x);
+                        });
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int col = 16 * j + e;
-                            float p = ex2(__uint_as_float(again[e]) + mine.x);
-                            if (masked && (col < from || col >= to)) p = 0.0f;
-                            sum[e & 1] = fmaf(p, __uint_as_float(dp[col]), sum[e & 1]);
+                            float p = ex2(__uint_as_float(again[e]));
+                            if (masked && (j + e < from || j + e >= to)) p = 0.0f;
+                            sum[e & 1] = fmaf(p, __uint_as_float(d[e]), sum[e & 1]);
                         }
                     }
+                    tmem_ld32(t_dp, dp);
+                    tc_wait_ld(dp);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sum[e & 1] = fmaf(__uint_as_float(s[e]), __uint_as_float(dp[e]), sum[e & 1]);
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // epilogue: dk and dv by two groups each, or a quarter of dq's columns a group
         const int xi = first + row;
         const bool in_use = xi < rows;
-        const float mult = second ? 1.0f : a.scale;
+        const float mult = second ? 1.0f : kCap ? 4.0f * a.scale : a.scale;   // (dS of capped scores: a quarter)
         uint32_t v[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j) {

@@ -247,16 +247,21 @@ __global__ void __launch_bounds__(32 * WARPS) attn_decode_kernel(const __grid_co
             }
         }
         bool grew = false;
-        if (kShaped) {
+        auto shape_chunk = [&](auto form) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {                // two neighbouring keys of a row
                     uint32_t x[2] = {__float_as_uint(s[n][2 * r]), __float_as_uint(s[n][2 * r + 1])};
-                    shape<true>(a.rule, x, slope2[r], static_cast<float>(chunk * kKeys + 8 * n + 2 * (lane & 3) - own_key[r]));
+                    shape<decltype(form)::value>(
+                        a.rule, x, slope2[r], static_cast<float>(chunk * kKeys + 8 * n + 2 * (lane & 3) - own_key[r]), 0.0f);
                     s[n][2 * r] = __uint_as_float(x[0]);
                     s[n][2 * r + 1] = __uint_as_float(x[1]);
                 }
+        };
+        if (kShaped) {
+            if (kCap && a.rule.large) shape_chunk(FormTag<kLarge>{});
+            else shape_chunk(FormTag<kAny>{});
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n)

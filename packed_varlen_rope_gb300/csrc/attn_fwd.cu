@@ -375,7 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const float slope2 = !kBias || !mine ? 0.0f
             : a.rule.slopes[kvh * a.group + row - static_cast<int>(fast_div(row, a.div_group)) * a.group] * kLog2e;
         const int row_key = i_tok + offset - lo_tile * kKeys - 64 * half;   // this row's own key, from this thread's first
-        float m = -INFINITY, l = 0.0f, mc = 0.0f;
+        // Capped exponents that stay within +-80 need no maximum: their weights and the sums of 2^24 of
+        // them keep their precision in binary32, and the two halves of a row need not meet
+        const bool fixed = kCap && !kBias && a.rule.fixed != 0;
+        float m = fixed ? 0.0f : -INFINITY, l = 0.0f, mc = 0.0f;
         bool ok = true;
         bool folded = false;                                           // m is known, and small
         // 32 of this thread's scores of step i, those it does not see at -infinity
@@ -410,67 +413,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
-        // shaped scores, 16 at a time: few live registers, as every spilled one costs a trip to L2
-        auto finish16 = [&](int i, int h, uint32_t(&s)[16]) {
-            const int key0 = tile_at(i) * kKeys + 16 * h;
-            float far = static_cast<float>(key0 - row_key);
-            asm volatile("" : "+f"(far));        // or the distances are kept for the second pass, in spilled registers
-            shape_any(a.rule, s, slope2, far);
-            if ((tile_at(i) + 1) * kKeys > whole) {
-                const int left = visible - key0;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j >= left) s[j] = 0xff800000u;
-            }
-        };
-        auto load16 = [&](int i, int h, uint32_t(&s)[16]) {
-            tmem_ld16(t_s + 16 * h, s);
-            tc_wait_ld16(s);
-            finish16(i, h, s);
-        };
-        auto highest16 = [&](const uint32_t(&s)[16]) {
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 16; j += 2)
-                top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            return fmaxf(top[0], top[1]);
-        };
-        auto weights16 = [&](const uint32_t(&s)[16], uint32_t *p, float fixed) {
+        // Shaped scores: this thread's 64 of tile step i, 16 at a time (few live registers, as every
+        // spilled one costs a trip to L2), to weights 2^(x - shift).  Returns their sum; high is the
+        // largest x - shift.
+        auto shaped_pass = [&](int i, float shift, uint32_t(&p)[32], float &high) {
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            high = -INFINITY;
+            constexpr int kAhead = kBias ? 0 : 1;                      // chunks loaded ahead: what the registers hold
+            uint32_t s[kAhead + 1][16];
+            if (kAhead > 0) tmem_ld16(t_s, s[0]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float2 x = add2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), twice(-fixed));
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-                sum[j & 1] = add2(sum[j & 1], x);
-                p[j] = pack_bf16(x.x, x.y);
+            for (int h = 0; h < 4; ++h) {
+                uint32_t(&w)[16] = s[h & kAhead];
+                if (kAhead == 0) tmem_ld16(t_s + 16 * h, w);
+                tc_wait_ld16(w);
+                if (kAhead > 0 && h < 3) tmem_ld16(t_s + 16 * (h + 1), s[(h + 1) & kAhead]);
+                const int key0 = tile_at(i) * kKeys + 16 * h;
+                float far = static_cast<float>(key0 - row_key);
+                asm volatile("" : "+f"(far));    // or all chunks' distances are made at once, in spilled registers
+                const int left = visible - key0;
+                const bool masked = (tile_at(i) + 1) * kKeys > whole;
+                if (kCap && masked) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j >= left) w[j] = 0u;
+                }
+                by_form(a.rule, w, lim == 0, [&](auto form) { shape<decltype(form)::value>(a.rule, w, slope2, far, shift); });
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j >= left) w[j] = 0xff800000u;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    float2 e = make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+                    if (!fixed) high = max3(high, e.x, e.y);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
+                    p[8 * h + j / 2] = pack_bf16(e.x, e.y);
+                }
             }
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
-        // Capped exponents that stay within +-80 need no maximum: weights within 2^+-80 and sums of
-        // 2^24 of them keep their precision in binary32, and the two halves of a row never meet.
-        if (kCap && !kBias && a.rule.fixed) {
-            m = 0.0f;
-            for (int i = 0; i < count[x]; ++i) {
-                if (ok) ok = warp_wait(s_full + 8 * x, i & 1, &s_abort, &g_attn_fault);
-                tc_fence_after();
-                uint32_t s[2][16];
-                tmem_ld16(t_s, s[0]);
+        // this thread's half of the output so far, and its sum, to a new maximum.  S of the tile is
+        // complete, and with it every earlier product into O
+        auto rescale = [&](int i, float shrink) {
+            if (i == 0) return;
+            l *= shrink;
+#pragma unroll 1
+            for (int j = 0; j < DP / 32; ++j) {
+                uint32_t o[16];
+                tmem_ld16(t_o + 16 * j, o);
+                tc_wait_ld16(o);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t p[8];
-                    tc_wait_ld16(s[h & 1]);
-                    if (h < 3) tmem_ld16(t_s + 16 * (h + 1), s[(h + 1) & 1]);
-                    finish16(i, h, s[h & 1]);
-                    l += weights16(s[h & 1], p, 0.0f);
-                    tmem_st8(t_p + 8 * h, p);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * x);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                tmem_st16(t_o + 16 * j, o);
             }
-        } else
+        };
         // after a wait that ran out the loop goes on without waiting, so that the pair's
         // barriers stay matched
         for (int i = 0; i < count[x]; ++i) {
@@ -481,12 +481,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             uint32_t p[32];
             float high = -INFINITY, sum = 0.0f;
             if (kShaped) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t s[16];
-                    load16(i, h, s);
-                    high = fmaxf(high, highest16(s));
-                    if (folded) sum += weights16(s, p + 8 * h, mc);
+                for (bool settled = fixed;;) {                         // once more where the maximum has grown too far
+                    sum = shaped_pass(i, mc, p, high);
+                    if (settled) break;
+                    settled = true;
+                    if (lim == 0) high = -INFINITY;
+                    high += mc;
+                    s_swap[i & 1][x][half][row] = high;
+                    named_barrier(pair, 64);
+                    high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
+                    if (!__any_sync(0xffffffffu, !folded || high - m > kGrow)) break;
+                    const float grown = fmaxf(m, high);
+                    rescale(i, m == grown ? 1.0f : ex2(m - grown));
+                    m = grown;
+                    mc = m == -INFINITY ? 0.0f : m;
+                    folded = true;
                 }
             } else {
 #pragma unroll
@@ -496,46 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     high = fmaxf(high, highest(s));
                     if (folded) sum += weights(s, p + 16 * h, mc);
                 }
-            }
-            // rows that see no key may hold anything: they take no part in the warp's decisions
-            if (lim == 0) high = -INFINITY;
-            s_swap[i & 1][x][half][row] = high;
-            // past the barrier both warps have read their scores, and P may overwrite them
-            tc_fence_before();
-            named_barrier(pair, 64);
-            tc_fence_after();
-            high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
-            if (__any_sync(0xffffffffu, !folded || (high - m) * c > kGrow)) {
-                // a new maximum; both warps of the pair come here, as they hold the same rows.
-                // S of this tile is complete, and with it every earlier product into O
-                const float grown = fmaxf(m, high);
-                if (i > 0) {
-                    const float shrink = m == grown ? 1.0f : ex2((m - grown) * c);
-                    l *= shrink;
-#pragma unroll 1
-                    for (int j = 0; j < DP / 32; ++j) {
-                        uint32_t o[16];
-                        tmem_ld16(t_o + 16 * j, o);
-                        tc_wait_ld16(o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-                        tmem_st16(t_o + 16 * j, o);
-                    }
-                }
-                m = grown;
-                const float shift = m == -INFINITY ? 0.0f : m;
-                mc = shift * c;
-                // (the difference of two exponents is exact where it matters, however large they are)
-                folded = kShaped || __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
-                sum = 0.0f;
-                if (kShaped) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t s[16];
-                        load16(i, h, s);
-                        sum += weights16(s, p + 8 * h, shift);
-                    }
-                } else {
+                // rows that see no key may hold anything: they take no part in the warp's decisions
+                if (lim == 0) high = -INFINITY;
+                s_swap[i & 1][x][half][row] = high;
+                // past the barrier both warps have read their scores, and P may overwrite them
+                tc_fence_before();
+                named_barrier(pair, 64);
+                tc_fence_after();
+                high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
+                if (__any_sync(0xffffffffu, !folded || (high - m) * c > kGrow)) {
+                    // a new maximum; both warps of the pair come here, as they hold the same rows
+                    const float grown = fmaxf(m, high);
+                    rescale(i, m == grown ? 1.0f : ex2((m - grown) * c));
+                    m = grown;
+                    const float shift = m == -INFINITY ? 0.0f : m;
+                    mc = shift * c;
+                    folded = __all_sync(0xffffffffu, fabsf(mc) <= kFoldLimit);
+                    sum = 0.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t s[32];
@@ -544,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - shift);
                         sum += weights(s, p + 16 * h, 0.0f);
                     }
+                    tc_fence_before();
+                    named_barrier(pair, 64);
+                    tc_fence_after();
                 }
-                tc_fence_before();
-                named_barrier(pair, 64);
-                tc_fence_after();
             }
             tmem_st32(t_p, p);
             l += sum;

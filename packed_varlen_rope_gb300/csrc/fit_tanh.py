@@ -1,14 +1,29 @@
-"""Coefficients of the tanh approximation of the capped attention scores (csrc/score_rule.cuh).
+"""Coefficients of the tanh approximations of the capped attention scores (csrc/score_rule.cuh).
 
-tanh(u) = u P(u^2) on |u| <= 1: tanh(u)/u is a smooth function of z = u^2 (its nearest
-singularity is z = -(pi/2)^2), so a Chebyshev interpolant in z on [0, 1] converges fast.
-Degree 4 leaves a relative error below 7.2e-6, which moves a score capped at 50 by less than
-2.8e-4, an eighth of what rounding the weight to bf16 may do (2^-9).  Run: python fit_tanh.py
-[degree]  (prints the coefficients of P, lowest degree first, and the error of the fit).
+tanh(u) = u P(u^2), odd polynomials that interpolate it at Chebyshev nodes (its nearest singularity
+is i pi/2, so they converge fast):
+
+* near: degree 7 on |u| <= 0.8, interpolating tanh itself: absolute error below 6.7e-6, which moves a
+  score capped at 50 by less than 3.4e-4, a tenth of what rounding the weight to bf16 may do (2^-8);
+* large: degree 11 on |u| <= 1, interpolating tanh(u)/u in u^2: relative error below 6.1e-7, for caps
+  so large that scores far below them have to keep theirs.
+
+Run: python fit_tanh.py  (prints the coefficients of P, lowest degree first, and the errors).
 """
 from __future__ import annotations
 
 import numpy as np
+
+NEAR = 0.8
+
+
+def near(degree: int = 3):
+    """P of the absolute fit, in u^2."""
+    n = 2 * degree + 3                                                   # zeros of the next odd term
+    k = np.arange(n)
+    u = NEAR * np.cos((2 * k + 1) * np.pi / (2 * n))
+    odd = np.vander(u * u, degree + 1, increasing=True) * u[:, None]
+    return np.linalg.lstsq(odd, np.tanh(u), rcond=None)[0]
 
 
 def target(z):
@@ -17,25 +32,26 @@ def target(z):
     return np.where(z < 1e-8, 1.0 - z / 3.0, np.tanh(u) / np.where(u > 0, u, 1.0))
 
 
-def fit(degree: int):
+def large(degree: int = 5):
+    """P of the relative fit, in z = u^2 on [0, 1]."""
     k = np.arange(degree + 1)
-    x = np.cos((2 * k + 1) * np.pi / (2 * (degree + 1)))     # Chebyshev nodes
+    x = np.cos((2 * k + 1) * np.pi / (2 * (degree + 1)))
     cheb = np.polynomial.chebyshev.chebfit(x, target((x + 1) / 2), degree)
     p = np.polynomial.Polynomial(np.polynomial.chebyshev.cheb2poly(cheb))
-    return p(np.polynomial.Polynomial([-1.0, 2.0])).coef     # in z, x = 2 z - 1
+    return p(np.polynomial.Polynomial([-1.0, 2.0])).coef                 # x = 2 z - 1
 
 
-def max_error(coef, n=20001):
-    """Largest relative error on [0, 1]."""
+def near_error(coef, n=40001):
+    u = np.linspace(0.0, NEAR, n)
+    return float(np.max(np.abs(u * np.polynomial.polynomial.polyval(u * u, coef) - np.tanh(u))))
+
+
+def large_error(coef, n=40001):
     z = np.linspace(0.0, 1.0, n)
     return float(np.max(np.abs(np.polynomial.polynomial.polyval(z, coef) / target(z) - 1.0)))
 
 
 if __name__ == "__main__":
-    import sys
-
-    degree = int(sys.argv[1]) if len(sys.argv) > 1 else 4
-    c = fit(degree)
-    print("degree %d: largest relative error %.3g for |u| <= 1" % (degree, max_error(c)))
-    for v in c:
-        print("    %.9ef," % v)
+    for name, c, e in (("near", near(), near_error(near())), ("large", large(), large_error(large()))):
+        print("%s: error %.3g" % (name, e))
+        print("    " + ", ".join("%.9ef" % v for v in c))

@@ -4,16 +4,24 @@
 //
 //   y_ij = cap tanh(scale q_i.k_j / cap) - slope_h |i - j|
 //
-// Scores become exponents of 2 before the softmax, x = y log2(e): K tanh(s a) with K = cap
-// log2(e) and a = scale / cap for capped ones, s c with c = scale log2(e) for others.  tanh is
-// u P(u^2) for |u| <= 1 (fit_tanh.py: relative error 7.2e-6, 2.8e-4 of a score capped at 50,
-// against the 2^-9 that rounding a weight to bf16 moves), and 1 - 2 / (1 + 2^(2 log2(e) u))
-// beyond, whose error of about 2^-22 of the cap is small against a score that large.
+// Scores become exponents of 2 before the softmax, x = y log2(e): K tanh(u) with K = cap log2(e) and
+// u = s scale / cap for capped ones, s c with c = scale log2(e) for others.  The tanh takes one of
+// three forms:
+//
+//   kNear   K u P(u^2), degree 7: 5 packed operations for two scores, absolute error 6.7e-6 of the cap
+//           (fit_tanh.py); for caps up to 128, where no score of the warp's chunk is past 0.8 caps
+//   kAny    K (1 - 2 q), q = 1 / (1 + e^2u), off by about 2^-22 K: 3 packed operations, but two special
+//           functions a score; for such caps elsewhere
+//   kLarge  caps past 128: u P(u^2), degree 11, relative error 6.1e-7, for |u| <= 1, so that scores far
+//           below the cap keep theirs; kAny's beyond; chosen score by score
+//
+// Forward, 16,384 tokens, 32/8 heads of 128, cap 50: MEASURED_FORMS.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "tensor_core.cuh"
@@ -35,13 +43,22 @@ constexpr bool kShaped = kCap || kBias;      // scores are exponents of 2 before
 struct ScoreRule {
     float a, k, a2;                          // capped scores: scale / cap, cap log2(e), 2 log2(e) scale / cap
     float c;                                 // others: scale log2(e)
+    float near[4], near_factor;              // kNear: x = s sum near_i s^2i, (1 - tanh^2) / 4 = 1/4 + near_factor x^2
+    float near_limit;                        // for |s| up to
+    int32_t large;                           // the cap takes kLarge
     int32_t fixed;                           // capped exponents within +-80: no maximum is needed
     const float *slopes;                     // [hq]
     const int32_t *prefix;                   // [n_seqs], or NULL
 };
 
-constexpr float kTanh0 = 9.999928679e-01f, kTanh1 = -3.329738354e-01f, kTanh2 = 1.303347757e-01f, kTanh3 = -4.476498296e-02f,
-                kTanh4 = 9.010406017e-03f;
+constexpr float kNearCap = 128.0f, kNearEnd = 0.8f;
+constexpr float kNear0 = 9.999243658e-01f, kNear1 = -3.317269685e-01f, kNear2 = 1.238189323e-01f, kNear3 = -3.164692249e-02f;
+constexpr float kTanh0 = 9.999993948e-01f, kTanh1 = -3.332895137e-01f, kTanh2 = 1.328072065e-01f, kTanh3 = -5.158598840e-02f,
+                kTanh4 = 1.672085518e-02f, kTanh5 = -3.058229038e-03f;
+
+enum Form { kNear, kAny, kLarge };
+template <Form FORM>
+using FormTag = std::integral_constant<Form, FORM>;
 
 __device__ __forceinline__ float rcp(float x)
 {
@@ -53,85 +70,88 @@ __device__ __forceinline__ float rcp(float x)
 // Both halves of a pair alike.
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
-// tanh of two scores times a.  wide: some score of the warp is past the fit, so each takes the form
-// that is right for it (no branch of its own: what follows is for converged warps).  The factor is
-// 1 - tanh^2, the gradient's.
-template <bool WIDE>
-__device__ __forceinline__ float2 tanh2(const ScoreRule &r, float2 s, float2 &factor)
+// Two scores to exponents of 2, plus an offset: K tanh(a s) + offset or s c + offset.  top is the
+// offset, K + offset for kAny.  factor: (1 - tanh^2) / 4, of the gradient.
+template <Form FORM>
+__device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2 top, float2 &factor)
 {
-    const float2 u = mul2(s, twice(r.a)), z = mul2(u, u);
-    float2 p = fma2(z, twice(kTanh4), twice(kTanh3));
-    p = fma2(z, p, twice(kTanh2));
-    p = fma2(z, p, twice(kTanh1));
-    p = fma2(z, p, twice(kTanh0));
-    float2 t = mul2(u, p);
-    factor = fma2(t, mul2(t, twice(-1.0f)), twice(1.0f));
-    if (WIDE) {
-        const float qx = rcp(1.0f + ex2(s.x * r.a2)), qy = rcp(1.0f + ex2(s.y * r.a2));
-        // (a NaN score takes the second form, and stays one)
-        const bool nx = fabsf(u.x) <= 1.0f, ny = fabsf(u.y) <= 1.0f;
-        t.x = nx ? t.x : fmaf(-2.0f, qx, 1.0f);
-        t.y = ny ? t.y : fmaf(-2.0f, qy, 1.0f);
-        factor.x = nx ? factor.x : 4.0f * qx * (1.0f - qx);
-        factor.y = ny ? factor.y : 4.0f * qy * (1.0f - qy);
+    if (!kCap) return fma2(s, twice(r.c), top);
+    if (FORM == kNear) {
+        const float2 z = mul2(s, s);
+        float2 p = fma2(z, twice(r.near[3]), twice(r.near[2]));
+        p = fma2(z, p, twice(r.near[1]));
+        p = fma2(z, p, twice(r.near[0]));
+        const float2 y = mul2(s, p);
+        factor = fma2(mul2(y, y), twice(r.near_factor), twice(0.25f));
+        return fma2(s, p, top);
     }
-    return t;
+    const float2 e = mul2(s, twice(r.a2));
+    const float2 d = add2(make_float2(ex2(e.x), ex2(e.y)), twice(1.0f));
+    const float2 q = make_float2(rcp(d.x), rcp(d.y));
+    float2 x = FORM == kAny ? fma2(q, twice(-2.0f * r.k), top) : add2(fma2(q, twice(-2.0f * r.k), twice(r.k)), top);
+    factor = mul2(q, fma2(q, twice(-1.0f), twice(1.0f)));
+    if (FORM == kLarge) {
+        const float2 u = mul2(s, twice(r.a)), z = mul2(u, u);
+        float2 p = fma2(z, twice(kTanh5), twice(kTanh4));
+        p = fma2(z, p, twice(kTanh3));
+        p = fma2(z, p, twice(kTanh2));
+        p = fma2(z, p, twice(kTanh1));
+        p = fma2(z, p, twice(kTanh0));
+        const float2 t = mul2(u, p), y = fma2(t, twice(r.k), top);
+        const float2 f = mul2(twice(0.25f), fma2(t, mul2(t, twice(-1.0f)), twice(1.0f)));
+        if (fabsf(u.x) <= 1.0f) { x.x = y.x; factor.x = f.x; }
+        if (fabsf(u.y) <= 1.0f) { x.y = y.y; factor.y = f.y; }
+    }
+    return x;
 }
 
-// The largest magnitude of N scores (NaN is passed over).
-template <int N>
-__device__ __forceinline__ float largest(const uint32_t (&s)[N])
-{
-    float top[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < N; j += 2)
-        top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
-    return fmaxf(top[0], top[1]);
-}
-
-// Biases of a thread's columns, a pair at a time, the first one `distance` past the row's own
-// place: -slope2 |distance|.  Distances are whole numbers and exact.
-struct Bias {
-    float2 at, slope;
-    __device__ __forceinline__ Bias(float slope2, float distance)
-        : at(make_float2(distance, distance + 1.0f)), slope(twice(-slope2)) {}
+// What exponent2 takes as `top` for a thread's columns, a pair at a time, the first one `distance`
+// past the row's own place: -slope2 |distance| + offset, and K with kAny.  Distances are whole numbers and exact.
+template <Form FORM>
+struct Tops {
+    float2 at, slope, base;
+    __device__ __forceinline__ Tops(const ScoreRule &r, float slope2, float distance, float offset)
+        : at(make_float2(distance, distance + 1.0f)), slope(twice(-slope2)), base(twice(kCap && FORM == kAny ? r.k + offset : offset)) {}
     __device__ __forceinline__ float2 next()
     {
-        const float2 x = mul2(slope, make_float2(fabsf(at.x), fabsf(at.y)));
+        if (!kBias) return base;
+        const float2 x = fma2(slope, make_float2(fabsf(at.x), fabsf(at.y)), base);
         at = add2(at, twice(2.0f));
         return x;
     }
 };
 
-// N scores, columns from `distance` past the row on, to exponents of 2, in place.
-template <bool WIDE, int N>
-__device__ __forceinline__ void shape(const ScoreRule &r, uint32_t (&s)[N], float slope2, float distance)
+// N scores, columns from `distance` past the row on, to exponents of 2 less `shift`, in place.
+template <Form FORM, int N>
+__device__ __forceinline__ void shape(const ScoreRule &r, uint32_t (&s)[N], float slope2, float distance, float shift)
 {
-    Bias bias(slope2, distance);
+    Tops<FORM> tops(r, slope2, distance, -shift);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-        float2 x = make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), factor;
-        if (kCap) x = tanh2<WIDE>(r, x, factor);
-        const float2 scale = twice(kCap ? r.k : r.c);
-        x = kBias ? fma2(x, scale, bias.next()) : mul2(x, scale);
+        float2 factor;
+        const float2 x = exponent2<FORM>(r, make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), tops.next(), factor);
         s[j] = __float_as_uint(x.x);
         s[j + 1] = __float_as_uint(x.y);
     }
 }
 
-// Whether some score of a converged warp is past the fit of the tanh.  A thread that holds one may
-// have it in a place that nobody sees: the two forms give a score within the fit the same bits.
-template <int N>
-__device__ __forceinline__ bool any_wide(const ScoreRule &r, const uint32_t (&s)[N])
+// Calls fn(FormTag<FORM>) with the form for N scores of every thread of a converged warp.  Scores
+// that nobody sees must not decide (hidden: the thread's row is none): they are 0 here.
+template <int N, typename Fn>
+__device__ __forceinline__ void by_form(const ScoreRule &r, const uint32_t (&s)[N], bool hidden, Fn fn)
 {
-    return __any_sync(0xffffffffu, largest(s) * r.a > 1.0f);
-}
-
-template <int N>
-__device__ __forceinline__ void shape_any(const ScoreRule &r, uint32_t (&s)[N], float slope2, float distance)
-{
-    if (kCap && any_wide(r, s)) shape<true>(r, s, slope2, distance);
-    else shape<false>(r, s, slope2, distance);
+    if (!kCap) {
+        fn(FormTag<kNear>{});
+        return;
+    }
+    float top[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < N; j += 2)
+        top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
+    // (a NaN is passed over, and comes through every form)
+    if (r.large) fn(FormTag<kLarge>{});
+    else if (__any_sync(0xffffffffu, !hidden && fmaxf(top[0], top[1]) > r.near_limit)) fn(FormTag<kAny>{});
+    else fn(FormTag<kNear>{});
 }
 
 // The keys at the start of a sequence that all its rows see.
@@ -150,6 +170,14 @@ inline ScoreRule rule_of(const AttnProblem &p)
         r.a = p.scale / p.cap;
         r.k = p.cap * kLog2;
         r.a2 = 2.0f * kLog2 * r.a;
+        // (the powers of a have to be normal numbers)
+        r.large = !(p.cap <= kNearCap) || !(r.a >= 1e-5f && r.a <= 1e5f);
+        r.near_limit = kNearEnd / r.a;
+        const float fit[4] = {kNear0, kNear1, kNear2, kNear3};
+        double power = static_cast<double>(r.k) * r.a;
+        for (int i = 0; i < 4 && !r.large; ++i, power *= static_cast<double>(r.a) * r.a)
+            r.near[i] = static_cast<float>(power * fit[i]);
+        r.near_factor = -0.25f / (r.k * r.k);
     }
     r.c = p.scale * kLog2;
     r.fixed = p.cap > 0.0f && p.slopes == nullptr && r.k <= 80.0f;

@@ -3,16 +3,17 @@
 Beside the bounds of attn_util (u = 2^-8 for the roundings to bf16, 2^-10 for what binary32 adds to
 each weight), a rule adds to each weight:
 
-* a cap: the tanh is off by 7.2e-6 of itself (its fit) and a few units of binary32, together less
-  than 8e-6, so a score moves by at most 8e-6 cap, and a weight, whose row's sum moves too, by twice
+* a cap: the tanh is off by at most 7e-6 (its fit with the roundings of binary32, or fewer units of
+  2^-23), so a score moves by at most 8e-6 cap, and a weight, whose row's sum moves too, by twice
   that: 16e-6 cap.
 * a distance bias: slope * distance rounds to 2^-24 of itself in the product and the sum, scaled by
   log2(e) with one more rounding: 3 * 2^-24 * 1.45 * slope * distance, twice for the row's sum.  Keys
   whose weight counts at all (above 2^-24 of the largest) are those whose bias stays within 20 plus
   the scores' spread of the row's best; the bound takes the whole of it.
 
-ds = p (1 - tanh^2) (dP - D): the factor's error, 2 tanh * 8e-6 absolute where it is at least 0.4 and
-2^-20 relative beyond, stays below 2^-13 of it and is inside binary32's 2^-10 of the others.
+ds = p (1 - tanh^2) (dP - D): the factor's error, 2e-5 absolute where it is at least 0.36 and a few
+2^-23 of its own terms beyond, stays below 2^-13 of it where it counts and is inside binary32's 2^-10
+of the others.
 """
 from __future__ import annotations
 

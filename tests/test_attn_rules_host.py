@@ -60,41 +60,68 @@ def test_formulas_against_differences(cap, sloped, prefix, causal):
         assert abs(float(slope - (ref[name][0] * way).sum())) < 1e-7
 
 
-def kernel_constants():
+def kernel_constants(name, n):
     text = open(os.path.join(CSRC, "score_rule.cuh")).read()
-    return np.array([float(re.search(r"kTanh%d = ([-0-9.e]+)f" % i, text).group(1)) for i in range(5)])
+    return np.array([float(re.search(r"%s%d = ([-0-9.e]+)f" % (name, i), text).group(1)) for i in range(n)])
 
 
-def test_tanh_constants_are_the_fit():
+@pytest.fixture(scope="module")
+def fit_tanh():
     sys.path.insert(0, CSRC)
     try:
-        import fit_tanh
+        import fit_tanh as module
     finally:
         sys.path.remove(CSRC)
-    want = fit_tanh.fit(4)
-    assert np.all(np.abs(kernel_constants() - want) <= 1e-9 * np.abs(want) + 1e-10)
-    assert fit_tanh.max_error(want) < 7.2e-6
+    return module
 
 
-def test_tanh_in_binary32():
-    """Step by step: below 8e-6 of the value for |u| <= 1, a few units of 2^-23 beyond."""
+def test_tanh_constants_are_the_fits(fit_tanh):
+    for name, want in (("kNear", fit_tanh.near()), ("kTanh", fit_tanh.large())):
+        got = kernel_constants(name, len(want))
+        assert np.all(np.abs(got - want) <= 1e-9 * np.abs(want) + 1e-10)
+    assert fit_tanh.near_error(fit_tanh.near()) < 6.7e-6 and fit_tanh.large_error(fit_tanh.large()) < 6.1e-7
+
+
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.088), (128.0, 0.125), (1.0, 1.0), (0.03, 20.0)])
+def test_near_form_in_binary32(fit_tanh, cap, scale):
+    """Step by step: within 7e-6 of the cap up to 0.8 of it, and the factor within 2e-5."""
     f = np.float32
-    c = kernel_constants().astype(f)
+    a, k = f(scale) / f(cap), f(cap) * f(1.4426950408889634)
+    coef = [f(float(k) * float(a) ** (2 * i + 1) * x) for i, x in enumerate(kernel_constants("kNear", 4))]
+    s = np.linspace(-0.8, 0.8, 200001).astype(f) * (f(1) / a)
+    z = s * s
+    p = z * coef[3] + coef[2]
+    p = z * p + coef[1]
+    p = z * p + coef[0]
+    x = s * p
+    t = np.tanh(s.astype(np.float64) * scale / cap)
+    assert np.max(np.abs(x.astype(np.float64) / 1.4426950408889634 - cap * t)) < 7e-6 * cap
+    factor = x * x * (f(-0.25) / (k * k)) + f(0.25)
+    assert np.max(np.abs(4 * factor.astype(np.float64) - (1 - t * t))) < 2e-5
+
+
+def test_other_forms_in_binary32():
+    """Step by step: the form of every score within a few units of 2^-23 of the cap, that of large
+    caps below 7e-7 of the score; their factors."""
+    f = np.float32
+    u = np.concatenate([-np.linspace(1e-3, 20, 100001), np.linspace(1e-3, 20, 100001)]).astype(f)
+    exact = np.tanh(u.astype(np.float64))
+    q = f(1) / (f(1) + np.exp2(f(2 * 1.4426950408889634) * u))
+    assert np.max(np.abs(f(1) - f(2) * q - exact)) < 4 * 2.0 ** -23
+    factor = 4.0 * (q * (f(1) - q)).astype(np.float64)
+    one_less = 1 / np.cosh(u.astype(np.float64)) ** 2
+    # 1 - q cancels where q is near 1: absolute there
+    assert np.max(np.abs(factor - one_less) / (one_less + 2.0 ** -6)) < 2.0 ** -15
+    c = kernel_constants("kTanh", 6).astype(f)
     u = np.linspace(1e-6, 1, 200001).astype(f)
     z = u * u
-    p = np.full_like(z, c[4])
-    for i in (3, 2, 1, 0):
+    p = np.full_like(z, c[5])
+    for i in (4, 3, 2, 1, 0):
         p = z * p + c[i]
     t = u * p
     exact = np.tanh(u.astype(np.float64))
-    assert np.max(np.abs(t / exact - 1)) < 8e-6
-    u = np.linspace(1, 20, 200001).astype(f)
-    q = f(1) / (f(1) + np.exp2(f(2 * 1.4426950408889634) * u))
-    t = f(1) - f(2) * q
-    exact = np.tanh(u.astype(np.float64))
-    assert np.max(np.abs(t - exact)) < 4 * 2.0 ** -23
-    factor = f(4) * q * (f(1) - q)
-    assert np.max(np.abs(factor / (1 / np.cosh(u.astype(np.float64)) ** 2) - 1)) < 2.0 ** -17
+    assert np.max(np.abs(t / exact - 1)) < 9e-7
+    assert np.max(np.abs((f(1) - t * t) - (1 - exact ** 2))) < 2.0 ** -19
 
 
 def test_structure_matches(tmp_path):
