@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // the rows are in one tile, D is taken from them instead, D = sum_j p dP, and kept for
         // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).
         const bool single = !KEYS && n_tiles == 1;
+        const bool line = a.causal && prefix <= 0;                     // of a biased row: its keys are on one side
         bool &ok = ok_softmax;
         int y = y0_first;
         for (int t = 0; t < n_tiles; ++t) {
@@ -413,8 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 for (int e = 0; e < 32; ++e)
                     if (e < from || e >= to) s[e] = 0u;
             }
-            by_form(a.rule, s, xi >= rows, [&](auto form) {
-                Tops<decltype(form)::value> tops(a.rule, slope2, far, 0.0f);
+            by_form(a.rule, s, xi >= rows, line, [&](auto form) {
+                constexpr Form kForm = decltype(form)::value;
+                Tops<kForm> tops(a.rule, KEYS && kForm == kLine ? -slope2 : slope2, far, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
@@ -424,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         const float2 n2 = h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w);
                         const float2 score = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                         float2 p, factor;
-                        if (kShaped) p = exponent2<decltype(form)::value>(a.rule, score, add2(tops.next(), n2), factor);
+                        if (kShaped)
+                            p = exponent2<kForm>(a.rule, score, kBias || kForm == kAny ? add2(tops.next(e), n2) : n2, factor);
                         else p = fma2(score, c2, n2);
                         p.x = ex2(p.x);
                         p.y = ex2(p.y);
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             for (int e = 0; e < 16; ++e)
                                 if (j + e < from || j + e >= to) again[e] = 0u;
                         }
-                        by_form(a.rule, again, xi >= rows, [&](auto form) {
+                        by_form(a.rule, again, xi >= rows, false, [&](auto form) {
                             shape<decltype(form)::value>(a.rule, again, slope2, far + j, -mine.x);
                         });
 #pragma unroll

@@ -413,45 +413,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
-        // Shaped scores: this thread's 64 of tile step i, 16 at a time (few live registers, as every
-        // spilled one costs a trip to L2), to weights 2^(x - shift).  Returns their sum; high is the
+        // Shaped scores: this thread's 64 of tile step i, 32 at a time, to weights 2^(x - shift): packed
+        // into p, or with `through` to tensor memory as they come.  Returns their sum; high is the
         // largest x - shift.
-        auto shaped_pass = [&](int i, float shift, uint32_t(&p)[32], float &high) {
+        const bool line = a.causal && prefix <= 0;
+        auto shaped_pass = [&](auto through, int i, float shift, uint32_t *p, float &high) {
+            constexpr bool kThrough = decltype(through)::value;
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             high = -INFINITY;
-            constexpr int kAhead = kBias ? 0 : 1;                      // chunks loaded ahead: what the registers hold
-            uint32_t s[kAhead + 1][16];
-            if (kAhead > 0) tmem_ld16(t_s, s[0]);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t(&w)[16] = s[h & kAhead];
-                if (kAhead == 0) tmem_ld16(t_s + 16 * h, w);
-                tc_wait_ld16(w);
-                if (kAhead > 0 && h < 3) tmem_ld16(t_s + 16 * (h + 1), s[(h + 1) & kAhead]);
-                const int key0 = tile_at(i) * kKeys + 16 * h;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+                tmem_ld32(t_s + 32 * h, w);
+                tc_wait_ld(w);
+                const int key0 = tile_at(i) * kKeys + 32 * h;
                 float far = static_cast<float>(key0 - row_key);
-                asm volatile("" : "+f"(far));    // or all chunks' distances are made at once, in spilled registers
+                asm volatile("" : "+f"(far));    // or the distances of all passes are made at once, in spilled registers
                 const int left = visible - key0;
                 const bool masked = (tile_at(i) + 1) * kKeys > whole;
                 if (kCap && masked) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         if (j >= left) w[j] = 0u;
                 }
-                by_form(a.rule, w, lim == 0, [&](auto form) { shape<decltype(form)::value>(a.rule, w, slope2, far, shift); });
+                by_form(a.rule, w, lim == 0, line, [&](auto form) { shape<decltype(form)::value>(a.rule, w, slope2, far, shift); });
                 if (masked) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         if (j >= left) w[j] = 0xff800000u;
                 }
+                tmem_loaded(w);                  // (all at once: spread out, what follows would need more registers)
+                uint32_t packed[16];
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
+                for (int j = 0; j < 32; j += 2) {
                     float2 e = make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
-                    if (!fixed) high = max3(high, e.x, e.y);
+                    if (!kThrough) high = max3(high, e.x, e.y);
                     e.x = ex2(e.x);
                     e.y = ex2(e.y);
                     sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
-                    p[8 * h + j / 2] = pack_bf16(e.x, e.y);
+                    (kThrough ? packed[j / 2] : p[16 * h + j / 2]) = pack_bf16(e.x, e.y);
+                }
+                if (kThrough) {
+                    tmem_st16(t_p + 16 * h, packed);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)  // (a chunk is done before the next one is loaded)
+                        asm volatile("" : "+r"(p[16 * h + j]), "+r"(p[16 * h + j + 1]), "+r"(p[16 * h + j + 2]), "+r"(p[16 * h + j + 3]));
                 }
             }
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -480,9 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             // rounding not to matter
             uint32_t p[32];
             float high = -INFINITY, sum = 0.0f;
-            if (kShaped) {
-                for (bool settled = fixed;;) {                         // once more where the maximum has grown too far
-                    sum = shaped_pass(i, mc, p, high);
+            if (kCap && !kBias && fixed) {
+                sum = shaped_pass(std::true_type{}, i, 0.0f, nullptr, high);
+            } else if (kShaped) {
+                for (bool settled = false;;) {                         // once more where the maximum has grown too far
+                    sum = shaped_pass(std::false_type{}, i, mc, p, high);
                     if (settled) break;
                     settled = true;
                     if (lim == 0) high = -INFINITY;
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     tc_fence_after();
                 }
             }
-            tmem_st32(t_p, p);
+            if (!(kCap && !kBias && fixed)) tmem_st32(t_p, p);
             l += sum;
             tc_wait_st();
             tc_fence_before();

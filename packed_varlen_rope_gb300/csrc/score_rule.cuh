@@ -56,7 +56,8 @@ constexpr float kNear0 = 9.999243658e-01f, kNear1 = -3.317269685e-01f, kNear2 = 
 constexpr float kTanh0 = 9.999993948e-01f, kTanh1 = -3.332895137e-01f, kTanh2 = 1.328072065e-01f, kTanh3 = -5.158598840e-02f,
                 kTanh4 = 1.672085518e-02f, kTanh5 = -3.058229038e-03f;
 
-enum Form { kNear, kAny, kLarge };
+// (kLine: uncapped scores, biased, of rows that see keys on one side of them alone)
+enum Form { kNear, kAny, kLarge, kLine };
 template <Form FORM>
 using FormTag = std::integral_constant<Form, FORM>;
 
@@ -69,6 +70,14 @@ __device__ __forceinline__ float rcp(float x)
 
 // Both halves of a pair alike.
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// The largest magnitude of three.
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Two scores to exponents of 2, plus an offset: K tanh(a s) + offset or s c + offset.  top is the
 // offset, K + offset for kAny.  factor: (1 - tanh^2) / 4, of the gradient.
@@ -106,17 +115,31 @@ __device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2
 }
 
 // What exponent2 takes as `top` for a thread's columns, a pair at a time, the first one `distance`
-// past the row's own place: -slope2 |distance| + offset, and K with kAny.  Distances are whole numbers and exact.
+// past the row's own place: -slope2 |distance| + offset, and K with kAny.  Distances are whole numbers
+// and exact.  With kLine the visible columns are on one side, and slope2 has its sign: the bias is
+// slope2 distance, a sum from 16 columns to the next.
 template <Form FORM>
 struct Tops {
+    float first, slope1, offset;
     float2 at, slope, base;
-    __device__ __forceinline__ Tops(const ScoreRule &r, float slope2, float distance, float offset)
-        : at(make_float2(distance, distance + 1.0f)), slope(twice(-slope2)), base(twice(kCap && FORM == kAny ? r.k + offset : offset)) {}
-    __device__ __forceinline__ float2 next()
+    __device__ __forceinline__ Tops(const ScoreRule &r, float slope2, float distance, float offset_)
+        : first(distance), slope1(slope2), offset(offset_), at(make_float2(distance, distance + 1.0f)),
+          slope(twice(FORM == kLine ? 2.0f * slope2 : -slope2)), base(twice(kCap && FORM == kAny ? r.k + offset_ : offset_)) {}
+    __device__ __forceinline__ float2 next(int j)
     {
         if (!kBias) return base;
-        const float2 x = fma2(slope, make_float2(fabsf(at.x), fabsf(at.y)), base);
-        at = add2(at, twice(2.0f));
+        float2 x;
+        if (FORM == kLine) {
+            if (j % 16 == 0) {
+                at.x = fmaf(slope1, first + j, offset);
+                at.y = at.x + slope1;
+            }
+            x = at;
+            at = add2(at, slope);
+        } else {
+            x = fma2(slope, make_float2(fabsf(at.x), fabsf(at.y)), base);
+            at = add2(at, twice(2.0f));
+        }
         return x;
     }
 };
@@ -129,25 +152,27 @@ __device__ __forceinline__ void shape(const ScoreRule &r, uint32_t (&s)[N], floa
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         float2 factor;
-        const float2 x = exponent2<FORM>(r, make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), tops.next(), factor);
+        const float2 x = exponent2<FORM>(r, make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), tops.next(j), factor);
         s[j] = __float_as_uint(x.x);
         s[j + 1] = __float_as_uint(x.y);
     }
 }
 
 // Calls fn(FormTag<FORM>) with the form for N scores of every thread of a converged warp.  Scores
-// that nobody sees must not decide (hidden: the thread's row is none): they are 0 here.
+// that nobody sees must not decide (hidden: the thread's row is none): they are 0 here.  line: the
+// rows see keys on one side alone.
 template <int N, typename Fn>
-__device__ __forceinline__ void by_form(const ScoreRule &r, const uint32_t (&s)[N], bool hidden, Fn fn)
+__device__ __forceinline__ void by_form(const ScoreRule &r, const uint32_t (&s)[N], bool hidden, bool line, Fn fn)
 {
     if (!kCap) {
-        fn(FormTag<kNear>{});
+        if (kBias && line) fn(FormTag<kLine>{});
+        else fn(FormTag<kNear>{});
         return;
     }
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < N; j += 2)
-        top[(j >> 1) & 1] = max3(top[(j >> 1) & 1], fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
+        top[(j >> 1) & 1] = max3_abs(top[(j >> 1) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
     // (a NaN is passed over, and comes through every form)
     if (r.large) fn(FormTag<kLarge>{});
     else if (__any_sync(0xffffffffu, !hidden && fmaxf(top[0], top[1]) > r.near_limit)) fn(FormTag<kAny>{});

@@ -6,8 +6,9 @@ each weight), a rule adds to each weight:
 * a cap: the tanh is off by at most 7e-6 (its fit with the roundings of binary32, or fewer units of
   2^-23), so a score moves by at most 8e-6 cap, and a weight, whose row's sum moves too, by twice
   that: 16e-6 cap.
-* a distance bias: slope * distance rounds to 2^-24 of itself in the product and the sum, scaled by
-  log2(e) with one more rounding: 3 * 2^-24 * 1.45 * slope * distance, twice for the row's sum.  Keys
+* a distance bias: slope * distance rounds to 2^-24 of itself in the product, in up to eight sums from
+  one column to the next, in the sum with the score, and once scaled by log2(e): 11 * 2^-24 * 1.45 *
+  slope * distance, twice for the row's sum.  Keys
   whose weight counts at all (above 2^-24 of the largest) are those whose bias stays within 20 plus
   the scores' spread of the row's best; the bound takes the whole of it.
 
@@ -65,7 +66,7 @@ def sample_reference(q, k, v, scale, cap=0.0, slopes=None, prefix=None, causal=T
     l = e.sum(dim=2, keepdim=True)
     p = e / torch.where(l > 0, l, torch.ones_like(l))
     steep = 0.0 if slopes is None else float(slopes.abs().max()) * m
-    rule = 16e-6 * cap + 2 * 3 * 1.45 * 2.0 ** -24 * steep
+    rule = 16e-6 * cap + 2 * 11 * 1.45 * 2.0 ** -24 * steep
     o = p @ V
     tol_o = U * o.abs() + (U + B32 + rule) * (p @ V.abs()) + 1e-30
     out = {"o": (o.transpose(0, 1), tol_o.transpose(0, 1)), "lse": (torch.log(l) + top)[:, :, 0], "rule": rule}
