@@ -6,7 +6,6 @@ import ctypes
 import struct
 from typing import Optional
 
-from ._axes import pack_axes
 from ._binding import RopeCosSinCacheDesc, _cache_arg, _check, _empty, load_library
 
 ATTN_EXPORTS = ("attn_varlen_fwd", "attn_varlen_bwd", "attn_varlen_bwd_workspace_bytes", "attn_paged",
@@ -281,7 +280,7 @@ def rope_kv_append(q, k, v, cache: PagedKVCache, page_table, kv_lens, cu_seqlens
             raise ValueError("interleaved and own_frequencies need position_ids and sections")
         _launch(load_library().rope_kv_append, "rope_kv_append", dev, stream, desc)
     else:
-        axes = pack_axes(position_ids, sections, T, dev, interleaved, own_frequencies)
+        axes = _axes.pack_axes(position_ids, sections, T, dev, interleaved, own_frequencies)
         _launch(load_library().rope_kv_append_axes, "rope_kv_append_axes", dev, stream, desc, axes)
     return q if q_out is None else q_out
 
@@ -496,3 +495,6 @@ def apply_attn(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] 
         raise ValueError("distance_slopes are constants: they get no gradient")
     return _Attn.apply(_rows(q), _rows(k), _rows(v), cu_seqlens, bool(causal), scale, seq_used, score_cap,
                        distance_slopes, prefix_lens)
+
+
+from . import _axes  # noqa: E402  (which takes the helpers above)

@@ -3,11 +3,15 @@ argument marshalling only, in the manner of ``_binding``."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
+from . import _attention as A
 from . import _binding as B
 
 ROPE_MAX_AXES = 4
 ROPE_AXES_INTERLEAVED, ROPE_AXES_OWN_FREQUENCIES, ROPE_AXES_IDS_INT64 = 0x1, 0x2, 0x4
+
+_NO_SECTIONS = (0,) * ROPE_MAX_AXES
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -19,41 +23,45 @@ class RopeAxesDesc(ctypes.Structure):
                 ("sections", _i32 * ROPE_MAX_AXES)]
 
 
+# packed in one go, as the attention's descriptors: the structures above and RopeQKDesc
+_AXES_PACK = struct.Struct("@Pqii4i").pack
+_QK_PACK = struct.Struct("@" + 4 * "Pqq" + "PiiiiPqqddPiiPPii").pack
+
+
 def _declare(lib):
-    """Signatures of the entry points (called by ``load_library``)."""
-    lib.rope_axes_apply.argtypes = [ctypes.POINTER(B.RopeQKDesc), ctypes.POINTER(RopeAxesDesc), _vp]
-    lib.rope_kv_append_axes.argtypes = [_vp, ctypes.POINTER(RopeAxesDesc), _vp]
+    """Signatures of the entry points (called by ``load_library``); descriptors packed as bytes."""
+    lib.rope_axes_apply.argtypes = [_vp, _vp, _vp]
+    lib.rope_kv_append_axes.argtypes = [_vp, _vp, _vp]
     lib.rope_axes_apply.restype = lib.rope_kv_append_axes.restype = ctypes.c_int
 
 
 def check_sections(sections, head_dim: int):
     """``sections`` as a tuple of 1 to 4 counts that share head_dim/2 frequencies among the axes."""
-    counts = tuple(int(x) for x in sections)
+    counts = tuple(map(int, sections))
     if not 1 <= len(counts) <= ROPE_MAX_AXES or min(counts) < 1 or sum(counts) != head_dim // 2:
         raise ValueError("sections must be 1 to %d positive counts that add up to head_dim/2 = %d" %
                          (ROPE_MAX_AXES, head_dim // 2))
     return counts
 
 
-def pack_axes(position_ids, sections, T: int, device_index: int, interleaved: bool, own_frequencies: bool):
-    """The ``rope_axes`` of a call over T tokens (the sections' sum is checked by the library)."""
-    import torch
-
+def pack_axes(position_ids, sections, T: int, dev: int, interleaved: bool, own_frequencies: bool) -> bytes:
+    """The packed ``rope_axes`` of a call over T tokens on CUDA device ``dev`` (the sections' sum is
+    checked by the library)."""
     if position_ids is None or sections is None:
         raise ValueError("position_ids and sections go together")
     n = len(sections)
     if not 1 <= n <= ROPE_MAX_AXES:
         raise ValueError("give 1 to %d sections" % ROPE_MAX_AXES)
-    if position_ids.dtype not in (torch.int32, torch.int64) or position_ids.get_device() != device_index or \
-            tuple(position_ids.shape) != (n, T) or (T > 1 and position_ids.stride(1) != 1):
+    st, dtype = position_ids.stride(), position_ids.dtype
+    flags = 0 if dtype is A._i32t else ROPE_AXES_IDS_INT64
+    if (flags != 0 and dtype is not A._torch.int64) or position_ids.get_device() != dev or position_ids.shape != (n, T) or (st[1] != 1 and T > 1):
         raise ValueError("position_ids must be an int32 or int64 [%d axes, %d tokens] tensor with contiguous rows on the "
                          "device of q" % (n, T))
-    desc = RopeAxesDesc(position_ids.data_ptr(), position_ids.stride(0) if n > 1 else T, n)
-    desc.flags = (ROPE_AXES_INTERLEAVED if interleaved else 0) | (ROPE_AXES_OWN_FREQUENCIES if own_frequencies else 0) | \
-        (ROPE_AXES_IDS_INT64 if position_ids.dtype == torch.int64 else 0)
-    for i, x in enumerate(sections):
-        desc.sections[i] = int(x)
-    return desc
+    if interleaved:
+        flags |= ROPE_AXES_INTERLEAVED
+    if own_frequencies:
+        flags |= ROPE_AXES_OWN_FREQUENCIES
+    return _AXES_PACK(position_ids.data_ptr(), st[0] if n > 1 else T, n, flags, *sections, *_NO_SECTIONS[n:])
 
 
 def rope_axes_apply(q, k, theta: float, sections, position_ids, backward: bool = False, q_out=None, k_out=None,
@@ -70,32 +78,23 @@ def rope_axes_apply(q, k, theta: float, sections, position_ids, backward: bool =
     not its part of one.  Where a token's positions are equal the result has the bits of
     ``rope_qk_apply``.  ``backward``: the transpose rotation.  A ``cos_sin_cache`` serves all
     axes (not with ``own_frequencies``).  Returns (q, k) in place, else (q_out, k_out)."""
-    qp, q_ts, q_hs = B._view_args(q, "q")
-    kp, k_ts, k_hs = B._view_args(k, "k")
-    if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or q.device != k.device:
+    A._torch or A._load_torch()
+    qv, kv = A._view(q, "q"), A._view(k, "k")
+    (T, hq, d), (Tk, hkv, dk), dev = q.shape, k.shape, q.get_device()
+    if Tk != T or dk != d or k.get_device() != dev:
         raise ValueError("q and k must share tokens, head_dim and device")
-    T, hq, d = q.shape
-    desc = B.RopeQKDesc()
-    desc.q, desc.q_stride_token, desc.q_stride_head = qp, q_ts, q_hs
-    desc.k, desc.k_stride_token, desc.k_stride_head = kp, k_ts, k_hs
-    if (q_out is None) != (k_out is None):
-        raise ValueError("give both q_out and k_out, or neither (in place)")
-    if q_out is not None:
-        if q_out.shape != q.shape or k_out.shape != k.shape or q_out.device != q.device or k_out.device != q.device:
+    qo = ko = (0, 0, 0)
+    if q_out is not None or k_out is not None:
+        if q_out is None or k_out is None:
+            raise ValueError("give both q_out and k_out, or neither (in place)")
+        if q_out.shape != q.shape or k_out.shape != k.shape or q_out.get_device() != dev or k_out.get_device() != dev:
             raise ValueError("q_out/k_out must have the shapes and device of q/k")
-        desc.q_out, desc.q_out_stride_token, desc.q_out_stride_head = B._view_args(q_out, "q_out")
-        desc.k_out, desc.k_out_stride_token, desc.k_out_stride_head = B._view_args(k_out, "k_out")
-    axes = pack_axes(position_ids, check_sections(sections, d), T, q.get_device(), interleaved, own_frequencies)
-    desc.n_q_heads, desc.n_kv_heads, desc.head_dim, desc.total_tokens = hq, k.shape[1], d, T
-    desc.theta, desc.position_scale = float(theta), float(position_scale)
-    cache = B._cache_arg(cos_sin_cache, d, q.device)
-    if cache is not None:
-        desc.cos_sin_cache = cache
-    desc.backward = 1 if backward else 0
-    st = B._on(q.device, B.load_library().rope_axes_apply, ctypes.byref(desc), ctypes.byref(axes),
-               B._stream(stream, q.device))
-    del cache
-    B._check("rope_axes_apply", st)
+        qo, ko = A._view(q_out, "q_out"), A._view(k_out, "k_out")
+    axes = pack_axes(position_ids, check_sections(sections, d), T, dev, interleaved, own_frequencies)
+    ref = None if cos_sin_cache is None else B._cache_arg(cos_sin_cache, d, q.device)
+    desc = _QK_PACK(*qv, *kv, *qo, *ko, 0, 0, hq, hkv, d, 0, T, 0, theta, position_scale,
+                    0 if ref is None else ctypes.addressof(ref.contents), 1 if backward else 0, 0, 0, 0, 0, 0)
+    A._launch(B.load_library().rope_axes_apply, "rope_axes_apply", dev, stream, desc, axes)
     return (q, k) if q_out is None else (q_out, k_out)
 
 

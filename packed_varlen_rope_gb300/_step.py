@@ -3,7 +3,9 @@ marshalling only, in the manner of ``_binding``."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
+from . import _attention as A
 from . import _binding as B
 
 PAGED_EXPORTS = ("paged_kv_step",)
@@ -22,9 +24,12 @@ class PagedKVStepDesc(ctypes.Structure):
                 ("max_tokens", _i64), ("n_seqs", _i32), ("max_pages", _i32), ("page_size", _i32), ("reserved", _i32)]
 
 
+_STEP_PACK = struct.Struct("@PPPPqPPPPPPPqqiiii").pack
+
+
 def _declare(lib):
-    """Signature of the entry point (called by ``load_library``)."""
-    lib.paged_kv_step.argtypes = [ctypes.POINTER(PagedKVStepDesc), _vp]
+    """Signature of the entry point (called by ``load_library``); the descriptor packed as bytes."""
+    lib.paged_kv_step.argtypes = [_vp, _vp]
     lib.paged_kv_step.restype = ctypes.c_int
 
 
@@ -43,35 +48,39 @@ def paged_kv_step(free_pages, free_count, page_table, past_lens, new_lens, page_
     ``count_out``: the count after the step (``free_count`` itself unless given).  ``status``
     (int32 [1]) receives STEP_* bits: no pages left, a row longer than the table, a stack or the
     slots too small, a negative length."""
-    import torch
-
-    dev, n = page_table.device, past_lens.numel()
-    if dev.type != "cuda" or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1) or (n > 1 and page_table.stride(0) < 0):
+    torch = A._torch or A._load_torch()
+    i32 = A._i32t
+    st, shape, dev = page_table.stride(), page_table.shape, page_table.get_device()
+    n = past_lens.numel()
+    if dev < 0 or page_table.dtype is not i32 or len(shape) != 2 or shape[0] != n or (shape[1] > 1 and st[1] != 1) or \
+            (n > 1 and st[0] < 0):
         raise ValueError("page_table must be a CUDA int32 [n_seqs, max_pages] tensor with contiguous rows")
-    max_tokens = int(max_tokens)
+    device, max_tokens = page_table.device, int(max_tokens)
     if slots is not None:
         max_tokens = slots.numel()
+        if slots.dtype is not torch.int64 or slots.get_device() != dev or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int64 tensor on %s" % device)
     elif max_tokens > 0:
-        slots = B._empty(max_tokens, torch.int64, dev, stream)
+        slots = B._empty(max_tokens, torch.int64, device, stream)
     if cu_seqlens is None:
-        cu_seqlens = B._empty(n + 1, torch.int32, dev, stream)
+        cu_seqlens = B._empty(n + 1, i32, device, stream)
     if kv_lens is None:
-        kv_lens = B._empty(n, torch.int32, dev, stream)
-    if count_out is None:
-        count_out = free_count
-    for name, t, size, dtype in (("free_pages", free_pages, free_pages.numel(), torch.int32),
-                                 ("free_count", free_count, 1, torch.int32), ("count_out", count_out, 1, torch.int32),
-                                 ("past_lens", past_lens, n, torch.int32), ("new_lens", new_lens, n, torch.int32),
-                                 ("finished", finished, n, torch.int32), ("cu_seqlens", cu_seqlens, n + 1, torch.int32),
-                                 ("kv_lens", kv_lens, n, torch.int32), ("slots", slots, max_tokens, torch.int64),
-                                 ("status", status, 1, torch.int32)):
-        if t is not None and (t.dtype != dtype or t.device != dev or t.numel() != size or not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous %s tensor of %d values on %s" % (name, dtype, size, dev))
-    desc = PagedKVStepDesc(B._ptr(free_pages), B._ptr(free_count), B._ptr(count_out), B._ptr(page_table),
-                           page_table.stride(0), B._ptr(past_lens), B._ptr(new_lens), B._ptr(finished), B._ptr(cu_seqlens),
-                           B._ptr(kv_lens), B._ptr(slots), B._ptr(status), free_pages.numel(), max_tokens, n,
-                           page_table.shape[1], int(page_size), 0)
-    st = B._on(dev, B.load_library().paged_kv_step, ctypes.byref(desc), B._stream(stream, dev))
-    B._check("paged_kv_step", st)
+        kv_lens = B._empty(n, i32, device, stream)
+    capacity = free_pages.numel()
+    count = _ints(free_count, dev, 1, "free_count")
+    desc = _STEP_PACK(_ints(free_pages, dev, capacity, "free_pages"), count,
+                      count if count_out is None else _ints(count_out, dev, 1, "count_out"), page_table.data_ptr(), st[0],
+                      _ints(past_lens, dev, n, "past_lens"), _ints(new_lens, dev, n, "new_lens"),
+                      0 if finished is None else _ints(finished, dev, n, "finished"),
+                      _ints(cu_seqlens, dev, n + 1, "cu_seqlens"), _ints(kv_lens, dev, n, "kv_lens"),
+                      0 if slots is None else slots.data_ptr(), 0 if status is None else _ints(status, dev, 1, "status"),
+                      capacity, max_tokens, n, shape[1], page_size, 0)
+    A._launch(B.load_library().paged_kv_step, "paged_kv_step", dev, stream, desc)
     return cu_seqlens, kv_lens, slots
+
+
+def _ints(t, dev: int, n: int, what: str) -> int:
+    """Pointer of a contiguous int32 tensor of n values on CUDA device ``dev``."""
+    if t.dtype is not A._i32t or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d values on the device of page_table" % (what, n))
+    return t.data_ptr()

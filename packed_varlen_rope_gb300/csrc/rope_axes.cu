@@ -28,8 +28,10 @@ namespace {
 using namespace pvr;
 
 constexpr int kThreads = 128;
-constexpr int kUnits = 3;               // 16-byte pair units in flight per thread
+constexpr int kUnits = 2;               // 16-byte pair units in flight per thread
+constexpr int kTileUnits = 640;         // about as many pair units a tile
 constexpr int kMaxTile = 16;            // tokens per tile
+constexpr int kSMs = 152;
 constexpr int kMaxStaged = 256;         // sequences whose cu_seqlens and kv_lens are staged
 
 struct AxesArgs {
@@ -47,7 +49,8 @@ struct AxesArgs {
     int32_t n_seqs, n_tokens, staged;
     int32_t hq, hkv, h_tot, cph, tile, n_axes, ids64;
     int32_t in_place, bwd;
-    FastDiv div_htot, div_cph;
+    int32_t rows_at_once;               // (cos, sin) rows that a CTA's threads make at a time
+    FastDiv div_htot, div_cph, div_row;
     float w[kMaxHalf];
     uint8_t axis[kMaxHalf];
 };
@@ -65,11 +68,12 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int n, int t)
     return lo;
 }
 
+// Every (cos, sin) of a tile is one thread's: thread i has frequency i % (d/2), whatever the token, so
+// that its frequency and axis are read once, and its position on that axis alone.
 template <bool APPEND>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_constant__ AxesArgs a)
+__global__ void __launch_bounds__(kThreads, APPEND ? 10 : 11) rope_axes_kernel(const __grid_constant__ AxesArgs a)
 {
     extern __shared__ __align__(16) float4 s_cs[];
-    __shared__ int s_pos[kMaxTile][ROPE_MAX_AXES];
     __shared__ int s_row[kMaxTile];                          // 0: the token is left out
     __shared__ int64_t s_slot_k[kMaxTile], s_slot_v[kMaxTile];
 
@@ -113,28 +117,40 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
                     : a.v_out + (slot + (head - a.hq - a.hkv) * a.vp_hs)) + 8 * w.chunk;
     };
 
+    // this thread's place in a token's (cos, sin) row, which is in the cache's [quad][chunk] order
+    const int per_row = 2 * row4;                            // frequencies, d / 2
+    const int my_row = static_cast<int>(fast_div(threadIdx.x, a.div_row)), at = static_cast<int>(threadIdx.x) - my_row * per_row;
+    const int quad = static_cast<int>(fast_div(static_cast<uint32_t>(at) >> 1, a.div_cph));
+    const int freq = 8 * ((at >> 1) - quad * cph) + 2 * quad + (at & 1);
+    const float w_j = a.w[freq];
+    const int64_t axis = a.axis[freq];
+
     // the grid may be scheduled while the kernel before it drains: nothing is read earlier
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    Where at[kUnits];
+    Where unit[kUnits];
     uint4 lo[kUnits], hi[kUnits];
     auto load = [&](uint32_t base) {
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t u = base + threadIdx.x + k * kThreads;
             if (u >= units) continue;
-            at[k] = where(u);
-            const __nv_bfloat16 *src = source(at[k]);
+            unit[k] = where(u);
+            const __nv_bfloat16 *src = source(unit[k]);
             lo[k] = load_stream(src);
             hi[k] = load_stream(src + h);
         }
     };
+    auto id_of = [&](int64_t x, int t) {
+        return a.ids64 ? static_cast<const int64_t *>(a.ids)[x * a.ids_stride + t]
+                       : static_cast<int64_t>(static_cast<const int32_t *>(a.ids)[x * a.ids_stride + t]);
+    };
     load(0);
 
-    // positions and pages, one thread per token
+    // which tokens are left out, and where they go, one thread per token
+    int32_t *s_cu = reinterpret_cast<int32_t *>(s_cs + a.tile * row4);
     if (APPEND && a.staged) {
-        int32_t *s_cu = reinterpret_cast<int32_t *>(s_cs + a.tile * row4);
         for (int i = threadIdx.x; i < 2 * a.n_seqs + 1; i += kThreads)
             s_cu[i] = i <= a.n_seqs ? a.cu[i] : a.kv_lens[i - a.n_seqs - 1];
         __syncthreads();
@@ -143,13 +159,10 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
         const int t = t0 + static_cast<int>(threadIdx.x);
         bool in = true;
         for (int x = 0; x < a.n_axes; ++x) {
-            const int64_t p = a.ids64 ? static_cast<const int64_t *>(a.ids)[x * a.ids_stride + t]
-                                      : static_cast<const int32_t *>(a.ids)[x * a.ids_stride + t];
+            const int64_t p = id_of(x, t);
             in = in && p >= 0 && p < kMaxTokens;
-            s_pos[threadIdx.x][x] = static_cast<int>(p);
         }
         if (APPEND) {
-            const int32_t *s_cu = reinterpret_cast<const int32_t *>(s_cs + a.tile * row4);
             const int32_t *cu = a.staged ? s_cu : a.cu, *kv = a.staged ? s_cu + a.n_seqs + 1 : a.kv_lens;
             int64_t slot_k = -1, slot_v = -1;
             const int s = sequence_of(cu, a.n_seqs, t);
@@ -173,23 +186,19 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
         }
         s_row[threadIdx.x] = in ? 1 : 0;
     }
-    __syncthreads();
 
-    // (cos, sin) rows of the tile, in the cache's [quad][chunk] order
-    float2 *s_cs2 = reinterpret_cast<float2 *>(s_cs);
-    for (int p2 = threadIdx.x; p2 < 2 * tt * row4; p2 += kThreads) {
-        const int idx = p2 >> 1;
-        const int i = idx / row4;
-        const int r = idx - i * row4;
-        if (s_row[i] == 0) continue;
-        const int quad = r / cph;
-        const int j = 8 * (r - quad * cph) + 2 * quad + (p2 & 1);
-        const int pos = s_pos[i][a.axis[j]];
-        float2 cs = pos < a.cache_rows
-                        ? __ldg(reinterpret_cast<const float2 *>(a.cache + static_cast<int64_t>(pos) * row4 + r) + (p2 & 1))
-                        : cos_sin_at(pos, a.w[j]);
-        if (a.bwd) cs.y = -cs.y;
-        s_cs2[p2] = cs;
+    // (cos, sin) rows of the tile; what a token left out gets here is not used
+    if (my_row < a.rows_at_once) {
+        float2 *dst = reinterpret_cast<float2 *>(s_cs);
+        for (int i = my_row; i < tt; i += a.rows_at_once) {
+            const int64_t id = id_of(axis, t0 + i);
+            const int pos = id >= 0 && id < kMaxTokens ? static_cast<int>(id) : 0;
+            float2 cs = pos < a.cache_rows
+                            ? __ldg(reinterpret_cast<const float2 *>(a.cache + static_cast<int64_t>(pos) * row4) + at)
+                            : cos_sin_at(pos, w_j);
+            if (a.bwd) cs.y = -cs.y;
+            dst[i * per_row + at] = cs;
+        }
     }
     __syncthreads();
 
@@ -203,13 +212,18 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
             rotate2(x.z, y.z, cs[2 * cph]);
             rotate2(x.w, y.w, cs[3 * cph]);
         }
-        *reinterpret_cast<uint4 *>(dst) = x;
-        *reinterpret_cast<uint4 *>(dst + h) = y;
+        if (APPEND) {                   // read again soon, by the attention
+            *reinterpret_cast<uint4 *>(dst) = x;
+            *reinterpret_cast<uint4 *>(dst + h) = y;
+        } else {
+            __stcs(reinterpret_cast<uint4 *>(dst), x);
+            __stcs(reinterpret_cast<uint4 *>(dst + h), y);
+        }
     };
     for (uint32_t base = 0;;) {
 #pragma unroll
         for (int k = 0; k < kUnits; ++k)
-            if (base + threadIdx.x + k * kThreads < units) finish(at[k], lo[k], hi[k]);
+            if (base + threadIdx.x + k * kThreads < units) finish(unit[k], lo[k], hi[k]);
         base += kUnits * kThreads;
         if (base >= units) break;
         load(base);
@@ -263,9 +277,13 @@ int launch(AxesArgs &a, int64_t T, int64_t d, const rope_cos_sin_cache *cs, void
     a.cph = static_cast<int32_t>(d / 16);
     a.div_htot = make_fastdiv(static_cast<uint32_t>(a.h_tot));
     a.div_cph = make_fastdiv(static_cast<uint32_t>(a.cph));
-    // as many tokens as one batch of units covers
+    a.div_row = make_fastdiv(static_cast<uint32_t>(d / 2));
+    a.rows_at_once = static_cast<int32_t>(kThreads / (d / 2));   // d <= 256: at least one
+    // Tokens a tile: kTileUnits of them, so that all threads evaluate (two tokens of 40 heads of 128; one
+    // token a tile took 128 us for what two take 113); fewer where the tiles would not fill the GPU
     const int64_t per_token = static_cast<int64_t>(a.h_tot) * a.cph;
-    const int64_t fit = (kUnits * kThreads) / per_token;
+    int64_t fit = kTileUnits / per_token, spread = T / (kSMs * 8);
+    if (fit > spread) fit = spread;
     a.tile = static_cast<int32_t>(fit < 1 ? 1 : fit > kMaxTile ? kMaxTile : fit);
     const size_t smem = static_cast<size_t>(a.tile) * 4 * a.cph * sizeof(float4) +
                         (APPEND && a.staged ? (2 * static_cast<size_t>(a.n_seqs) + 1) * sizeof(int32_t) : 0);

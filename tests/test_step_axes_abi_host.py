@@ -55,6 +55,24 @@ def test_headers_are_plain_c_and_structures_match(tmp_path):
     assert got == want
 
 
+def test_packed_descriptors_fill_the_fields_in_order():
+    from packed_varlen_rope_gb300 import PagedKVStepDesc, RopeAxesDesc, RopeQKDesc
+    from packed_varlen_rope_gb300 import _axes, _step
+
+    for pack, st in ((_axes._AXES_PACK, RopeAxesDesc), (_axes._QK_PACK, RopeQKDesc), (_step._STEP_PACK, PagedKVStepDesc)):
+        assert pack.__self__.size == ctypes.sizeof(st)
+    x = RopeAxesDesc.from_buffer_copy(_axes._AXES_PACK(1, 2, 3, 4, 5, 6, 7, 8))
+    assert (x.position_ids, x.position_stride, x.n_axes, x.flags, *x.sections) == tuple(range(1, 9))
+    q = RopeQKDesc.from_buffer_copy(_axes._QK_PACK(*range(1, 13), 13, 14, 15, 16, 17, 18, 19, 20, 1e4, 2.0, 0, 1, 0, 24, 0, 26, 0))
+    assert (q.q, q.q_stride_token, q.q_stride_head, q.k, q.k_stride_token, q.k_stride_head, q.q_out, q.q_out_stride_token,
+            q.q_out_stride_head, q.k_out, q.k_out_stride_token, q.k_out_stride_head, q.cu_seqlens, q.n_seqs, q.n_q_heads,
+            q.n_kv_heads, q.head_dim, q.position_ids, q.total_tokens, q.token_offset, q.theta, q.position_scale,
+            bool(q.cos_sin_cache), q.backward, q.flags, q.seq_used, bool(q.segments), q.n_segments, q.reserved) == \
+        (*range(1, 21), 1e4, 2.0, False, 1, 0, 24, False, 26, 0)
+    d = PagedKVStepDesc.from_buffer_copy(_step._STEP_PACK(*range(1, 19)))
+    assert tuple(getattr(d, f[0]) for f in d._fields_) == tuple(range(1, 19))
+
+
 def axes(**kw):
     from packed_varlen_rope_gb300 import RopeAxesDesc
 
