@@ -58,7 +58,7 @@ typedef struct paged_kv_step_desc {
     int64_t n_free_max;            /* below 2^31                                          */
     int64_t max_tokens;            /* below 2^31                                          */
     int32_t n_seqs;                /* at most 2^24                                        */
-    int32_t max_pages;             /* max_pages * page_size below 2^30                    */
+    int32_t max_pages;             /* at most 2^24, times page_size below 2^30             */
     int32_t page_size;             /* 1 .. 65,536                                         */
     int32_t reserved;              /* 0 */
 } paged_kv_step_desc;

@@ -61,22 +61,31 @@ def paged_kv_step(free_pages, free_count, page_table, past_lens, new_lens, page_
         if slots.dtype is not torch.int64 or slots.get_device() != dev or not slots.is_contiguous():
             raise ValueError("slots must be a contiguous int64 tensor on %s" % device)
     elif max_tokens > 0:
-        slots = B._empty(max_tokens, torch.int64, device, stream)
+        slots = _new(torch, max_tokens, torch.int64, device, stream)
     if cu_seqlens is None:
-        cu_seqlens = B._empty(n + 1, i32, device, stream)
+        cu_seqlens = _new(torch, n + 1, i32, device, stream)
+        cu = cu_seqlens.data_ptr()
+    else:
+        cu = _ints(cu_seqlens, dev, n + 1, "cu_seqlens")
     if kv_lens is None:
-        kv_lens = B._empty(n, i32, device, stream)
+        kv_lens = _new(torch, n, i32, device, stream)
+        kv = kv_lens.data_ptr()
+    else:
+        kv = _ints(kv_lens, dev, n, "kv_lens")
     capacity = free_pages.numel()
     count = _ints(free_count, dev, 1, "free_count")
     desc = _STEP_PACK(_ints(free_pages, dev, capacity, "free_pages"), count,
                       count if count_out is None else _ints(count_out, dev, 1, "count_out"), page_table.data_ptr(), st[0],
                       _ints(past_lens, dev, n, "past_lens"), _ints(new_lens, dev, n, "new_lens"),
                       0 if finished is None else _ints(finished, dev, n, "finished"),
-                      _ints(cu_seqlens, dev, n + 1, "cu_seqlens"), _ints(kv_lens, dev, n, "kv_lens"),
-                      0 if slots is None else slots.data_ptr(), 0 if status is None else _ints(status, dev, 1, "status"),
-                      capacity, max_tokens, n, shape[1], page_size, 0)
+                      cu, kv, 0 if slots is None else slots.data_ptr(),
+                      0 if status is None else _ints(status, dev, 1, "status"), capacity, max_tokens, n, shape[1], page_size, 0)
     A._launch(B.load_library().paged_kv_step, "paged_kv_step", dev, stream, desc)
     return cu_seqlens, kv_lens, slots
+
+
+def _new(torch, n: int, dtype, device, stream):
+    return torch.empty(n, dtype=dtype, device=device) if stream is None else B._empty(n, dtype, device, stream)
 
 
 def _ints(t, dev: int, n: int, what: str) -> int:

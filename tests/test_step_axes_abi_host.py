@@ -163,6 +163,7 @@ def step(**kw):
     (dict(n_free_max=1 << 31), ERR_SHAPE), (dict(max_tokens=-1), ERR_SHAPE), (dict(max_tokens=1 << 31), ERR_SHAPE),
     (dict(page_table_stride=9), ERR_SHAPE), (dict(reserved=1), ERR_UNSUPPORTED),
     (dict(max_pages=1 << 27, page_table_stride=1 << 27), ERR_UNSUPPORTED),
+    (dict(max_pages=(1 << 24) + 1, page_table_stride=1 << 25, page_size=1), ERR_UNSUPPORTED),
     (dict(free_pages=None), ERR_NULL), (dict(free_count=None), ERR_NULL), (dict(count_out=None), ERR_NULL),
     (dict(page_table=None), ERR_NULL), (dict(past_lens=None), ERR_NULL), (dict(new_lens=None), ERR_NULL),
     (dict(cu_seqlens=None), ERR_NULL), (dict(kv_lens=None), ERR_NULL), (dict(slots=BASE + (9 << 30) + 4), ERR_ALIGN),
