@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 for (int e = 0; e < 32; ++e)
                     if (e < from || e >= to) s[e] = 0u;
             }
-            by_form(a.rule, s, xi >= rows, line, [&](auto form) {
+            auto weights = [&](auto form, auto hides) {
                 constexpr Form kForm = decltype(form)::value;
+                constexpr bool kHides = decltype(hides)::value;        // some column is hidden
                 Tops<kForm> tops(a.rule, KEYS && kForm == kLine ? -slope2 : slope2, far, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         else p = fma2(score, c2, n2);
                         p.x = ex2(p.x);
                         p.y = ex2(p.y);
-                        if (masked) {
+                        if (kRuled ? kHides : masked) {
                             if (e < from || e >= to) p.x = 0.0f;
                             if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
                         }
@@ -441,6 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         s[e + 1] = __float_as_uint(p.y);
                     }
                 }
+            };
+            // two bodies for tiles with hidden columns and without: as selects in one they would cost
+            // each column 2.6 instructions of 16
+            by_form(a.rule, s, xi >= rows, line, [&](auto form) {
+                if (kRuled && masked) weights(form, std::true_type{});
+                else weights(form, std::false_type{});
             });
             // P and dS take the first half of the columns this thread has read
             if (KEYS) {
