@@ -132,8 +132,9 @@ def _axes_function():
 
 def apply_rope_axes(q, k, theta: float, sections, position_ids, cos_sin_cache=None, position_scale: float = 1.0,
                     interleaved: bool = False, own_frequencies: bool = False):
-    """Differentiable in-place ``rope_axes_apply``.  Differentiable once: a second derivative
-    raises."""
+    """Differentiable in-place ``rope_axes_apply``, of tensors of their own: autograd refuses views
+    (the slices of one projection's output) rotated in place together, clone them.  Differentiable
+    once: a second derivative raises."""
     global _RopeAxes
     if _RopeAxes is None:
         _RopeAxes = _axes_function()
