@@ -175,7 +175,9 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
  *
  * Computed in binary32: a cap puts a score within 8e-6 of the cap of where it belongs, a cap past
  * 128 within 1e-6 of the score and 2^-21 of the cap where the score is larger than it.  A score of
- * +-infinity is capped like any other; a NaN comes out in its row.
+ * +-infinity is capped like any other; a NaN comes out in its row.  Distances are exact below 2^24.
+ * With caps up to 55 and no slopes the forward's weights reach 2^60 before they are normalised: values
+ * are expected below 2^43 there.
  */
 typedef struct attn_score_rule {
     const float *slopes;           /* device float [n_q_heads], finite; or NULL: no bias   */

@@ -44,7 +44,8 @@ extern "C" {
 typedef struct rope_axes {
     const void *position_ids;      /* device int32 [n_axes, total_tokens], a token's positions
                                       contiguous along the tokens; aligned to its type      */
-    int64_t position_stride;       /* elements from one axis to the next, >= total_tokens   */
+    int64_t position_stride;       /* elements from one axis to the next, >= 0 (0: all axes
+                                      share their positions)                                */
     int32_t n_axes;                /* 1 .. ROPE_MAX_AXES                                    */
     int32_t flags;
     int32_t sections[ROPE_MAX_AXES];   /* each >= 1 (0 past n_axes), sum head_dim / 2       */

@@ -71,7 +71,8 @@ def rope_axes_apply(q, k, theta: float, sections, position_ids, backward: bool =
     (C entry point ``rope_axes_apply``).
 
     q, k: bf16 CUDA views [T, Hq, d] and [T, Hkv, d] with any token/head strides.
-    ``position_ids``: int32 or int64 [axes, T], a position of every token on each axis; a token
+    ``position_ids``: int32 or int64 [axes, T] with contiguous rows (one row expanded to all axes
+    too), a position of every token on each axis; a token
     with one outside [0, 2^24) is left out (give pad rows -1).  ``sections``: how many of the
     d/2 frequencies turn by each axis, consecutive ones, or with ``interleaved`` taking turns.
     ``own_frequencies``: every axis has the whole range of frequencies (theta^(-i/section)),

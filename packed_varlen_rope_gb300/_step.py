@@ -79,7 +79,7 @@ def paged_kv_step(free_pages, free_count, page_table, past_lens, new_lens, page_
                       _ints(past_lens, dev, n, "past_lens"), _ints(new_lens, dev, n, "new_lens"),
                       0 if finished is None else _ints(finished, dev, n, "finished"),
                       cu, kv, 0 if slots is None else slots.data_ptr(),
-                      0 if status is None else _ints(status, dev, 1, "status"), capacity, max_tokens, n, shape[1], page_size, 0)
+                      0 if status is None else _ints(status, dev, 1, "status"), capacity, max_tokens, n, shape[1], int(page_size), 0)
     A._launch(B.load_library().paged_kv_step, "paged_kv_step", dev, stream, desc)
     return cu_seqlens, kv_lens, slots
 

@@ -13,6 +13,9 @@
 // sequence's keys) through distributed shared memory; only where that leaves SMs idle do
 // further splits join through the workspace in a second launch.
 //
+// Rules on the scores (score_rule.cuh), an instance each: a few operations a score more, hidden by the
+// loads (the batch below, capped: 327-333 us).
+//
 // Bound by HBM: G operations a byte of cache (64 sequences of 500-16,000 tokens, 32/8 heads
 // of 128: 325-330 us for 2.2 GB, 6.7-6.8 TB/s, a copy's rate); a short sequence by the chain of
 // its dependent steps (one of 4,098 tokens 10.7 us, of which 2.5 us of loads).

@@ -18,6 +18,14 @@
 // keys each); one warp issues the products, one the loads, one watches the loads.  While one
 // row tile's softmax runs the tensor core works for the other.
 //
+// Rules on the scores (score_rule.cuh), an instance each.  A prefix only moves the rows' limits.
+// Shaped scores (capped, biased) become exponents 32 columns at a time between tensor memory and the
+// exponential; with a bias by distance the key tiles go downwards, so that causal rows meet their
+// largest exponents first.  They hold the softmax warps, not the tensor core, back: the packed batch
+// below, 32/8 heads of 128, 500 us plain, 509 with prefixes, 555 with slopes, 648 capped, 872 both
+// (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64
+// 330, 332, 401, 423 and 619 us.
+//
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
 // elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
 // register spill (none in the packed instances, one of 4 bytes in the paged ones): with 200 KB
@@ -85,6 +93,13 @@ struct Shared {
     static constexpr int kOffBars = kOffKV + kStages * kTileBytes;
     static constexpr int kBytes = kOffBars + 256 + 1024;              // + alignment slack
 };
+
+// Capped exponents that stay within +-80 need no maximum, a quarter of K does for all rows: weights
+// are within 2^60 and 2^-100, so that they and the sums of 2^24 of them keep their precision in
+// binary32, and products with values up to 2^43 their range; the two halves of a row need not meet.
+// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 648 us,
+// 872 with the maximum; both in one instance cost the first 803).
+constexpr bool kFixed = kRule == kRuleCap;
 
 template <int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdArgs a)
@@ -372,15 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         // thread's columns of the row see
         const int whole = limit(tok0) - lo_tile * kKeys, visible = lim - lo_tile * kKeys - 64 * half;
         const float c = kShaped ? 1.0f : a.scale * kLog2e;             // shaped scores are exponents of 2
-        const float slope2 = !kBias || !mine ? 0.0f
+        const float slope2 = !kBias || !mine || a.rule.slopes == nullptr ? 0.0f
             : a.rule.slopes[kvh * a.group + row - static_cast<int>(fast_div(row, a.div_group)) * a.group] * kLog2e;
         const int row_key = i_tok + offset - lo_tile * kKeys - 64 * half;   // this row's own key, from this thread's first
-        // Capped exponents that stay within +-80 need no maximum: their weights and the sums of 2^24 of
-        // them keep their precision in binary32, and the two halves of a row need not meet
-        const bool fixed = kCap && !kBias && a.rule.fixed != 0;
-        float m = fixed ? 0.0f : -INFINITY, l = 0.0f, mc = 0.0f;
+        float m = kFixed ? 0.25f * a.rule.k : -INFINITY, l = 0.0f, mc = 0.0f;
         bool ok = true;
-        bool folded = false;                                           // m is known, and small
+        bool folded = false;                                           // m is known, and small (shaped: known)
+        bool fold = true;                                              // shaped: m is small
         // 32 of this thread's scores of step i, those it does not see at -infinity
         auto load = [&](int i, int h, uint32_t(&s)[32]) {
             tmem_ld32(t_s + 32 * h, s);
@@ -414,11 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
         // Shaped scores: this thread's 64 of tile step i, 32 at a time, to weights 2^(x - shift): packed
-        // into p, or with `through` to tensor memory as they come.  Returns their sum; high is the
-        // largest x - shift.
+        // into p, or with a fixed maximum to tensor memory as they come.  Returns their sum; high is the
+        // largest x.  A large shift is not folded into the exponents' last operation: their rounding
+        // would differ from that of the maximum, and the largest weight be far from 1.
         const bool line = a.causal && prefix <= 0;
-        auto shaped_pass = [&](auto through, int i, float shift, uint32_t *p, float &high) {
-            constexpr bool kThrough = decltype(through)::value;
+        auto shaped_pass = [&](auto folds, int i, float shift, uint32_t *p, float &high) {
+            constexpr bool kFold = decltype(folds)::value;
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             high = -INFINITY;
 #pragma unroll
@@ -436,7 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     for (int j = 0; j < 32; ++j)
                         if (j >= left) w[j] = 0u;
                 }
-                by_form(a.rule, w, lim == 0, line, [&](auto form) { shape<decltype(form)::value>(a.rule, w, slope2, far, shift); });
+                by_form(a.rule, w, lim == 0, line, [&](auto form) {
+                    shape<decltype(form)::value>(a.rule, w, slope2, far, kFold ? shift : 0.0f);
+                });
                 if (masked) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -447,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     float2 e = make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
-                    if (!kThrough) high = max3(high, e.x, e.y);
+                    if (!kFixed) high = max3(high, e.x, e.y);
+                    if (!kFold) e = add2(e, twice(-shift));
                     e.x = ex2(e.x);
                     e.y = ex2(e.y);
                     sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
-                    (kThrough ? packed[j / 2] : p[16 * h + j / 2]) = pack_bf16(e.x, e.y);
+                    (kFixed ? packed[j / 2] : p[16 * h + j / 2]) = pack_bf16(e.x, e.y);
                 }
-                if (kThrough) {
+                if (kFixed) {
                     tmem_st16(t_p + 16 * h, packed);
                 } else {
 #pragma unroll
@@ -461,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         asm volatile("" : "+r"(p[16 * h + j]), "+r"(p[16 * h + j + 1]), "+r"(p[16 * h + j + 2]), "+r"(p[16 * h + j + 3]));
                 }
             }
+            if (kFold) high += shift;
             return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
         // this thread's half of the output so far, and its sum, to a new maximum.  S of the tile is
@@ -487,24 +505,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             // rounding not to matter
             uint32_t p[32];
             float high = -INFINITY, sum = 0.0f;
-            if (kCap && !kBias && fixed) {
-                sum = shaped_pass(std::true_type{}, i, 0.0f, nullptr, high);
+            if (kFixed) {
+                sum = shaped_pass(std::true_type{}, i, m, p, high);
             } else if (kShaped) {
                 for (bool settled = false;;) {                         // once more where the maximum has grown too far
-                    sum = shaped_pass(std::false_type{}, i, mc, p, high);
+                    sum = fold ? shaped_pass(std::true_type{}, i, mc, p, high) : shaped_pass(std::false_type{}, i, mc, p, high);
                     if (settled) break;
-                    settled = true;
+                    // (both warps of the pair hold the same rows: they go the same way)
                     if (lim == 0) high = -INFINITY;
-                    high += mc;
                     s_swap[i & 1][x][half][row] = high;
                     named_barrier(pair, 64);
                     high = fmaxf(high, s_swap[i & 1][x][half ^ 1][row]);
                     if (!__any_sync(0xffffffffu, !folded || high - m > kGrow)) break;
-                    const float grown = fmaxf(m, high);
+                    const float grown = fmaxf(m, high), next = grown == -INFINITY ? 0.0f : grown;
+                    const bool small = __all_sync(0xffffffffu, fabsf(next) <= kFoldLimit);
+                    if (fold && !small) {                              // the maximum again, without a shift in it
+                        fold = false;
+                        named_barrier(pair, 64);
+                        continue;
+                    }
                     rescale(i, m == grown ? 1.0f : ex2(m - grown));
                     m = grown;
-                    mc = m == -INFINITY ? 0.0f : m;
-                    folded = true;
+                    mc = next;
+                    fold = small;
+                    settled = folded = true;
                 }
             } else {
 #pragma unroll
@@ -544,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     tc_fence_after();
                 }
             }
-            if (!(kCap && !kBias && fixed)) tmem_st32(t_p, p);
+            if (!kFixed) tmem_st32(t_p, p);
             l += sum;
             tc_wait_st();
             tc_fence_before();
@@ -711,7 +735,10 @@ int attn_fwd_splits(const AttnProblem &p, int64_t max_kv)
 
 cudaError_t launch_attn_fwd(const AttnProblem &p, int splits, float *workspace, cudaStream_t stream)
 {
-    return for_rule(p.rule(), [&](auto rule) { return launch_attn_fwd_rule<decltype(rule)::value>(p, splits, workspace, stream); });
+    int rule = p.rule();
+    constexpr float kFixedLimit = 80.0f;                     // of K
+    if (rule == kRuleCap && !(p.cap * kLog2e <= kFixedLimit)) rule |= kRuleBias;
+    return for_rule(rule, [&](auto rule) { return launch_attn_fwd_rule<decltype(rule)::value>(p, splits, workspace, stream); });
 }
 #endif
 

@@ -248,7 +248,7 @@ int check_axes(const rope_axes &x, int64_t T, int32_t head_dim, double theta, do
     if (T > 0) {
         if (x.position_ids == nullptr) return ROPE_ERR_NULL;
         if (!aligned(x.position_ids, (x.flags & ROPE_AXES_IDS_INT64) != 0 ? 8 : 4)) return ROPE_ERR_ALIGN;
-        if (x.n_axes > 1 && (x.position_stride < T || x.position_stride > (int64_t(1) << 56))) return ROPE_ERR_SHAPE;
+        if (x.n_axes > 1 && (x.position_stride < 0 || x.position_stride > (int64_t(1) << 56))) return ROPE_ERR_SHAPE;
     }
     host_inv_freq(theta, head_dim, scale, a.w);
     int had[ROPE_MAX_AXES] = {};

@@ -153,6 +153,77 @@ def test_caps(dev, cap, qscale):
     check_varlen(dev, [260, 90], 4, 2, 64, cap=cap, seed=50, qscale=qscale, grads=qscale * 3 < 20 * cap)
 
 
+@pytest.mark.parametrize("vscale", [1e-9, 1e9])
+@pytest.mark.parametrize("towards", [1.0, -1.0])
+def test_values_far_from_one_at_the_cap(dev, vscale, towards):
+    """Scores all near the cap, or near its negative, and values far from 1, where the forward takes a
+    fixed maximum (cap 55) and where it does not (56)."""
+    m = pr()
+    n, d = 400, 64
+    q = torch.full((n, 2, d), 4.0, dtype=torch.bfloat16, device=dev)
+    k = (towards * 4.0 + normal((n, 1, d), 53, dev).float() / 16).to(torch.bfloat16)
+    v = (normal((n, 1, d), 54, dev).float() * vscale).to(torch.bfloat16)
+    for cap in (55.0, 56.0):
+        o, lse = m.attn_varlen_fwd(q, k, v, ints([0, n], dev), scale=0.125, score_cap=cap, return_lse=True)
+        ref = sample_reference(q, k, v, 0.125, cap)
+        assert_within(o, *ref["o"], "o")
+        assert float((lse.double() - ref["lse"]).abs().max()) <= ref["rule"] + 2.0 ** -11 * (1 + float(ref["lse"].abs().max()))
+
+
+@pytest.mark.parametrize("cap,scale", [(1e-25, 1e-22), (1e-3, 1e3), (1e-12, 1e-16), (1e20, 1e16), (2e4, 0.125)])
+def test_caps_and_scales_at_the_ends(dev, cap, scale):
+    """Caps and scales whose powers leave binary32: scores moderate against the cap all the same."""
+    spread = 0.6 * cap / scale / 64.0                        # |q.k| up to about 0.6 cap / scale
+    m = pr()
+    q, k = ((normal((90, 1, 64), 55 + i, dev).float() * (spread if i == 0 else 1.0)).to(torch.bfloat16) for i in range(2))
+    v = normal((90, 1, 64), 57, dev)
+    o = m.attn_varlen_fwd(q, k, v, ints([0, 90], dev), scale=scale, score_cap=cap)
+    ref = sample_reference(q, k, v, scale, cap)
+    if cap <= 2e4:                                           # (beyond, binary32 scores of that size mean little)
+        assert_within(o, *ref["o"], "o")
+    assert bool((o.double().abs() <= 1.01 * v.double().abs().max()).all())
+
+
+def test_scores_of_any_size_with_slopes(dev):
+    """Uncapped: however large the scores, the largest weight is 1 and one of the keys' values comes
+    out, as they are too far apart for two."""
+    m = pr()
+    n = 300
+    q, k, v = (normal((n, 2, 64), 58 + i, dev) for i in range(3))
+    for size in (1e6, 1e15, 1e30):
+        big = (k.float() * size).to(torch.bfloat16)
+        for causal in (True, False):
+            o = m.attn_varlen_fwd(q, big, v, ints([0, n], dev), causal=causal, distance_slopes=series(2, dev))
+            s = torch.einsum("ihd,jhd->hij", q.double(), big.double())
+            if causal:
+                s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=dev).triu(1), -math.inf)
+            best = s.argmax(dim=2)                           # [heads, rows]
+            top2 = s.topk(2, dim=2).values
+            # ahead by more than binary32's error in the scores, and than the bias can make up for
+            ahead = top2[..., 0] - top2[..., 1]
+            clear = (ahead > 1e-4 * top2[..., 0].abs()) & (0.125 * ahead > 0.5 * n + 50)
+            want = torch.stack([v[best[h], h] for h in range(2)])
+            got = o.transpose(0, 1)
+            assert bool((got[clear] == want[clear]).all()) and not bool(o.isnan().any())
+
+
+@pytest.mark.parametrize("size", [1e4, 1e8, 3e9, 1e10, 1e13, 1e30])
+def test_large_scores_after_small_ones(dev, size):
+    """Keys of ordinary scores, then one whose score is far larger: the rows that see it take its value."""
+    m, n = pr(), 700
+    q, k, v = (normal((n, 1, 64), 90 + i, dev) for i in range(3))
+    for at in (600, 20):
+        for d in (0, 8):                                     # of q and k: the large key's direction
+            q[:, 0, d] = 1.0
+            big = k.clone()
+            big[at, 0] = 0.0
+            big[at, 0, d] = size
+            o = m.attn_varlen_fwd(q, big, v, ints([0, n], dev), distance_slopes=series(1, dev, 1e-3))
+            assert bool((o[at:] == v[at]).all()) and not bool(o.isnan().any())
+            ref = sample_reference(q[:at], big[:at], v[:at], 0.125, 0.0, series(1, dev, 1e-3))
+            assert_within(o[:at], *ref["o"], "o")
+
+
 @pytest.mark.parametrize("first", [0.0, -0.01, 0.02, 4.0, 40.0])
 @pytest.mark.parametrize("causal", [True, False])
 def test_slopes(dev, first, causal):

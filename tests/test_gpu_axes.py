@@ -103,6 +103,8 @@ def test_equal_positions_give_the_bits_of_one_axis(dev):
         got = m.rope_axes_apply(q.clone(), k.clone(), 1e6, (16, 24, 24), ids.expand(3, 999).contiguous(),
                                 interleaved=interleaved)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+        got = m.rope_axes_apply(q.clone(), k.clone(), 1e6, (16, 24, 24), ids[None].expand(3, 999), interleaved=interleaved)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def append_case(dev, new, kv, page, hq, hkv, sections, seed, in_place=False, cached=0, wide=False, table_edit=None,

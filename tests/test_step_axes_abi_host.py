@@ -108,7 +108,7 @@ def rotation(**kw):
     ({}, dict(sections=(32, 0, 0, 0)), ERR_SHAPE), ({}, dict(sections=(16, 8, 8, 0)), ERR_SHAPE),
     ({}, dict(sections=(48, -16, 0, 0)), ERR_SHAPE), ({}, dict(flags=8), ERR_UNSUPPORTED),
     ({}, dict(position_ids=None), ERR_NULL), ({}, dict(position_ids=BASE + 2), ERR_ALIGN),
-    ({}, dict(position_ids=BASE + 4, flags=4), ERR_ALIGN), ({}, dict(position_stride=999), ERR_SHAPE),
+    ({}, dict(position_ids=BASE + 4, flags=4), ERR_ALIGN), ({}, dict(position_stride=-1), ERR_SHAPE),
 ])
 def test_axes_refusals(lib, kw, ax, want):
     assert lib.rope_axes_apply(ctypes.byref(rotation(**kw)), ctypes.byref(axes(**ax)), None) == want
