@@ -378,9 +378,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // The D that comes in is dout . o with o rounded to bf16.  Against the few keys of a
         // sample's first rows that error is as large as the rounding of ds; where all keys of
         // the rows are in one tile, D is taken from them instead, D = sum_j p dP, and kept for
-        // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).
+        // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).  With shaped scores every
+        // row's D is made whole for that pass: the ds of capped scores, sharp as they may be, are smaller than
+        // the terms they are the difference of, and dk was off by 4.1e-3 where it is by 2.5e-3.
         const bool single = !KEYS && n_tiles == 1;
         const bool line = a.causal && prefix <= 0;                     // of a biased row: its keys are on one side
+        float lacks = 0.0f;
+        // the sum over a row's four threads, whose warps all come here (after a wait that ran out too)
+        auto row_sum = [&](float x) {
+            float *swap = reinterpret_cast<float *>(smem + Sh::kOffStats);   // [quarter][row]; of keys' statistics, not here
+            if (kShaped) named_barrier(1 + (warp & 3), 128);           // (used twice)
+            swap[quarter * kTile + row] = x;
+            named_barrier(1 + (warp & 3), 128);
+            return (swap[row] + swap[kTile + row]) + (swap[2 * kTile + row] + swap[3 * kTile + row]);
+        };
         bool &ok = ok_softmax;
         int y = y0_first;
         for (int t = 0; t < n_tiles; ++t) {
@@ -451,10 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             };
             // two bodies for tiles with hidden columns and without: as selects in one they would cost
             // each column 2.6 instructions of 16
-            by_form(a.rule, s, xi >= rows, line, [&](auto form) {
-                if (kRuled && masked) weights(form, std::true_type{});
-                else weights(form, std::false_type{});
-            });
+            if (KEYS || !kShaped)
+                by_form(a.rule, s, xi >= rows, line, [&](auto form) {
+                    if (kRuled && masked) weights(form, std::true_type{});
+                    else weights(form, std::false_type{});
+                });
             // P and dS take the first half of the columns this thread has read
             if (KEYS) {
                 tmem_st16(t_s, packed);
@@ -467,68 +479,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (!ok && !single) break;
             tc_fence_after();
             const uint32_t t_dp = t_p + (t & 1) * kNextP;
-            uint32_t dp[32];
-            if (!kCap || !single) {
+            if (!KEYS && kShaped) {
+                // Queries, shaped scores: weights and ds together, as dP is long there; a half at a time,
+                // with no more than a half's registers beside the scores.  Returns the row's sum of
+                // p (dP - D), with `first` that of p dP alone.
+                auto gradients = [&](auto form, auto hides, auto first) {
+                    constexpr Form kForm = decltype(form)::value;
+                    constexpr bool kHides = decltype(hides)::value, kFirst = decltype(first)::value;
+                    Tops<kForm> tops(a.rule, slope2, far, mine.x);
+                    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t dp[16], out[8];
+                        tmem_ld16(t_dp + 16 * h, dp);
+                        tc_wait_ld16(dp);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const int e = 16 * h + j;
+                            float2 factor;
+                            float2 p = exponent2<kForm>(a.rule, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                                        tops.next(e), factor);
+                            p.x = ex2(p.x);
+                            p.y = ex2(p.y);
+                            if (kHides) {
+                                if (e >= to) p.x = 0.0f;
+                                if (e + 1 >= to) p.y = 0.0f;
+                            }
+                            float2 g = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
+                            if (!kFirst) g = add2(g, make_float2(mine.y, mine.y));
+                            sum = fma2(p, g, sum);
+                            if (kCap) p = mul2(p, factor);             // ds takes p (1 - tanh^2), here a quarter of it
+                            const float2 ds = mul2(p, g);
+                            out[j / 2] = pack_bf16(ds.x, ds.y);
+                        }
+                        if (!kFirst) tmem_st8(t_dp + 8 * h, out);
+                    }
+                    return sum.x + sum.y;
+                };
+                auto by_mask = [&](auto first) {
+                    float sum = 0.0f;
+                    by_form(a.rule, s, xi >= rows, line, [&](auto form) {
+                        if (masked || decltype(first)::value) sum = gradients(form, std::true_type{}, first);
+                        else sum = gradients(form, std::false_type{}, first);
+                    });
+                    return sum;
+                };
+                if (single) mine.y = -row_sum(by_mask(std::true_type{}));
+                lacks += by_mask(std::false_type{});
+            } else {
+                uint32_t dp[32];
                 tmem_ld32(t_dp, dp);
                 tc_wait_ld(dp);
-            }
-            if (single) {
-                float sum[2] = {0.0f, 0.0f};
-                if (kCap) {
-                    // the weights again, from the scores (S is read for the last time): what s holds
-                    // has the tanh's factor in it
-#pragma unroll 1
-                    for (int j = 0; j < 32; j += 16) {
-                        uint32_t again[16], d[16];
-                        tmem_ld16(t_s + j, again);
-                        tmem_ld16(t_dp + j, d);
-                        tc_wait_ld16(again);
-                        tc_wait_ld16(d);
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (j + e < from || j + e >= to) again[e] = 0u;
-                        }
-                        by_form(a.rule, again, xi >= rows, false, [&](auto form) {
-                            shape<decltype(form)::value>(a.rule, again, slope2, far + j, -mine.x);
-                        });
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float p = ex2(__uint_as_float(again[e]));
-                            if (masked && (j + e < from || j + e >= to)) p = 0.0f;
-                            sum[e & 1] = fmaf(p, __uint_as_float(d[e]), sum[e & 1]);
-                        }
-                    }
-                    tmem_ld32(t_dp, dp);
-                    tc_wait_ld(dp);
-                } else {
+                if (single) {
+                    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sum[e & 1] = fmaf(__uint_as_float(s[e]), __uint_as_float(dp[e]), sum[e & 1]);
+                    mine.y = -row_sum(sum[0] + sum[1]);
+                    if (quarter == 0 && live && xi < rows)
+                        a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y;
                 }
-                float *swap = reinterpret_cast<float *>(smem + Sh::kOffStats);   // [quarter][row]
-                swap[quarter * kTile + row] = sum[0] + sum[1];
-                named_barrier(1 + (warp & 3), 128);
-                mine.y = -((swap[row] + swap[kTile + row]) + (swap[2 * kTile + row] + swap[3 * kTile + row]));
-                if (quarter == 0 && live && xi < rows)
-                    a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y;
-            }
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 nd = KEYS ? smem_load4(st + 4 * (kTile + j)) : make_float4(mine.y, mine.y, mine.y, mine.y);
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 nd = KEYS ? smem_load4(st + 4 * (kTile + j)) : make_float4(mine.y, mine.y, mine.y, mine.y);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = j + 2 * h;
-                    const float2 ds = mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                           add2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
-                                                h == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w)));
-                    packed[e / 2] = pack_bf16(ds.x, ds.y);
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = j + 2 * h;
+                        const float2 ds = mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                               add2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                                    h == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w)));
+                        packed[e / 2] = pack_bf16(ds.x, ds.y);
+                    }
                 }
+                tmem_st16(t_dp, packed);
             }
-            tmem_st16(t_dp, packed);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full + 8 * (t & 1));
+        }
+        if (!KEYS && kShaped) {
+            // the D that came in was short of this much (zero where it was taken from the weights): the
+            // pass over the keys has it whole
+            const float more = row_sum(lacks);
+            if (quarter == 0 && live && xi < rows && mine.x != -INFINITY)
+                a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y - more;
         }
         if (ok && n_tiles > 0) {
             ok = warp_wait(done, 0, &s_abort, &g_attn_bwd_fault);
