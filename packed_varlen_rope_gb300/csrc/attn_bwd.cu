@@ -28,9 +28,9 @@
 //
 // Rules on the scores (score_rule.cuh), an instance each: the forward's exponents again, and for
 // capped scores ds = P (1 - tanh^2) (dP - D), a quarter of it in dS and the 4 in the last scaling.
-// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,800 us plain, 1,700 with prefixes, 1,718 with
-// slopes (tiles with hidden columns have a body of their own), 2,135 capped, 2,330 both: 11 cycles of
-// the FMA pipe a score where the plain instance has 3, tensor core 47 and 52 % of the time.
+// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,800 us plain, 1,705 with prefixes, 1,732 with
+// slopes (tiles with hidden columns have a body of their own), 2,190 capped, 2,366 both: 11 cycles of
+// the FMA pipe a score where the plain instance has 3, tensor core 47 and 48 % of the time.
 //
 // Bound by the tensor core: 2048 cycles a 128x128 tile for dk and dv, 1536 for dq.  32/8 heads
 // of 128, causal: one sample of 32,768 tokens 19.7-19.9 ms, 1,108-1,118 TFLOP/s by the five

@@ -29,7 +29,8 @@ constexpr int kMaxWarps = 32;           // of a CTA
 constexpr int kListed = 1024;           // sequences of a CTA up to which those that give back are dealt out
 constexpr int kPerWarp = 8;             // sequences a warp, up to what the largest cluster holds
 constexpr int kMaxCluster = 8;
-constexpr int64_t kOwnTokens = 1 << 14;  // slots that the cluster writes itself
+constexpr int64_t kOwnTokens = 512;     // slots that the cluster writes itself, or one a sequence up to
+constexpr int64_t kMostOwnTokens = 2048;
 constexpr int kFillThreads = 256, kFillTokens = 8;   // of the second launch; tokens a thread
 
 struct StepArgs {
@@ -500,7 +501,11 @@ extern "C" int paged_kv_step(const paged_kv_step_desc *desc, void *stream)
     warps = (warps + cluster - 1) / cluster;
     warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
     a.per_warp = static_cast<int32_t>((n + cluster * warps - 1) / (cluster * warps));
-    a.fill = desc->slots != nullptr && desc->max_tokens > kOwnTokens;
+    // A sequence's slots are one warp's in the first launch: 512 of one sequence 7.3 us, 513 by the second
+    // launch 6.9, 16,384 8.5 (by a warp some 80); one each of 512 sequences 5.1, of 4,096 7.3, but 39 if all
+    // 4,096 are one sequence's.
+    const int64_t own = n < kOwnTokens ? kOwnTokens : n < kMostOwnTokens ? n : kMostOwnTokens;
+    a.fill = desc->slots != nullptr && desc->max_tokens > own;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -89,11 +89,15 @@ def test_page_sizes(dev, page):
     check(dev, free, count, table, past, new, done, page, 77 * 150)
 
 
-@pytest.mark.parametrize("max_tokens", [0, 1, 16384, 16385, 70000])
+@pytest.mark.parametrize("max_tokens", [0, 1, 512, 513, 2048, 2049, 16384, 16385, 70000])
 def test_tokens_of_one_and_two_launches(dev, max_tokens):
     free, count, table, past, new, done = batch(3, 32, 900, 9000, 9000, 0.0, 1000, 5)
     check(dev, free, count, table, past, new, done, 32, max_tokens)
     check(dev, free, count, table, past, [0, 0, 0], done, 32, max_tokens)
+    free, count, table, past, new, done = batch(1, 32, 900, 9000, 9000, 0.0, 1000, 13)
+    check(dev, free, count, table, past, new, done, 32, max_tokens)
+    free, count, table, past, new, done = batch(1500, 8, 9, 30, 1, 0.2, 30000, 14)
+    check(dev, free, count, table, past, new, done, 8, max_tokens)
     free, count, table, past, new, done = batch(7000, 8, 9, 30, 12, 0.2, 30000, 6)
     check(dev, free, count, table, past, new, done, 8, max_tokens)
 
