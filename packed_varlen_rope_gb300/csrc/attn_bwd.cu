@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         else p = fma2(score, c2, n2);
                         p.x = ex2(p.x);
                         p.y = ex2(p.y);
-                        if (kRuled ? kHides : masked) {
+                        if (kHides) {
                             if (e < from || e >= to) p.x = 0.0f;
                             if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
                         }
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             // each column 2.6 instructions of 16
             if (KEYS || !kShaped)
                 by_form(a.rule, s, xi >= rows, line, [&](auto form) {
-                    if (kRuled && masked) weights(form, std::true_type{});
+                    if (masked) weights(form, std::true_type{});
                     else weights(form, std::false_type{});
                 });
             // P and dS take the first half of the columns this thread has read
