@@ -180,7 +180,8 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
  * are expected below 2^43 there.
  */
 typedef struct attn_score_rule {
-    const float *slopes;           /* device float [n_q_heads], finite; or NULL: no bias   */
+    const float *slopes;           /* device float [n_q_heads], times 1.45 and the longest
+                                      distance finite; or NULL: no bias                    */
     const int32_t *prefix;         /* device int32 [n_seqs], keys that all rows of the
                                       sequence see (cut to its keys, negative as 0); needs
                                       causal (else ROPE_ERR_UNSUPPORTED); or NULL          */

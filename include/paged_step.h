@@ -10,7 +10,7 @@
  *              ids of the row that are >= 0, onto the stack in the order of s and of the row; it
  *              is then an empty row, past 0 (new_lens[s] may admit another sequence into it).
  *   lengths    kv_lens[s] = past + new_lens[s]; cu_seqlens[0] = 0, cu_seqlens[s + 1] =
- *              cu_seqlens[s] + new_lens[s].  Negative lengths count as 0.
+ *              cu_seqlens[s] + new_lens[s].  Negative lengths count as 0, sums stop at 2^31 - 1.
  *   pages      row s needs the pages ceil(past / page_size) .. ceil(kv_lens[s] / page_size) - 1;
  *              in the order of s and of the pages each takes the top of the stack.  Other entries
  *              of the table are left as they are.
@@ -18,7 +18,7 @@
  *              without a page and for t >= cu_seqlens[n_seqs].
  *
  * When the stack runs out the remaining pages get id -1, which the cache's readers treat as no
- * page (STEP_NO_PAGES).  Pages past the table's width are not taken (STEP_TABLE_FULL); what does not
+ * page (STEP_NO_PAGES); later steps do not fill it: finish the row, which gives back what it got.  Pages past the table's width are not taken (STEP_TABLE_FULL); what does not
  * fit the stack is dropped (STEP_STACK_FULL); tokens past the slots' end get none
  * (STEP_TOKENS_PAST_END, where slots are wanted).  The bits go to *status.
  *

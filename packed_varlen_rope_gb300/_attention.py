@@ -112,6 +112,8 @@ def _rule(score_cap, distance_slopes, prefix_lens, q, dev: int, n: int):
     """The packed rule on the scores, None without one."""
     if score_cap == 0 and distance_slopes is None and prefix_lens is None:
         return None
+    if 0 < abs(score_cap) < 2.0 ** -126:                       # (it might be packed as 0, which is none)
+        raise ValueError("score_cap must be 0 or a positive normal float32")
     slopes = prefix = 0
     if distance_slopes is not None:
         if distance_slopes.requires_grad and _torch.is_grad_enabled():

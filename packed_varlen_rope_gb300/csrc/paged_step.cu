@@ -396,14 +396,15 @@ __global__ void __launch_bounds__(kFillThreads) paged_slots_kernel(const __grid_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5)) * (32 * kFillTokens);
     const int n = p.n_seqs, total = p.cu_seqlens[n];
-    int lo = 0, start = 0, end = 0, kv = 0, past_window = 0;   // past_window: the first token past the sequences kept
-    int seq[kFillTokens], pos[kFillTokens];
+    int lo = 0, start = 0, end = 0, past = 0, past_window = 0;   // past_window: the first token past the sequences kept
+    int seq[kFillTokens];
+    uint32_t pos[kFillTokens];
 #pragma unroll
     for (int k = 0; k < kFillTokens; ++k) {
         const int64_t t = t0 + 32 * k + lane;
         bool pending = t < total && t < p.max_tokens;
         seq[k] = -1;
-        pos[k] = 0;
+        pos[k] = 0u;
         for (uint32_t todo; (todo = __ballot_sync(0xffffffffu, pending)) != 0;) {
             const int next = static_cast<int>(t0 + 32 * k + __ffs(todo) - 1);
             if (next >= past_window) {
@@ -418,7 +419,9 @@ __global__ void __launch_bounds__(kFillThreads) paged_slots_kernel(const __grid_
                 }
                 start = p.cu_seqlens[min(lo + lane, n)];
                 end = p.cu_seqlens[min(lo + lane + 1, n)];
-                kv = lo + lane < n ? p.kv_lens[lo + lane] : 0;
+                // (not from kv_lens, which stops at 2^31 - 1)
+                const bool fresh = lo + lane >= n || (p.finished != nullptr && p.finished[lo + lane] != 0);
+                past = fresh ? 0 : max(p.past_lens[lo + lane], 0);
                 past_window = __shfl_sync(0xffffffffu, end, 31);
             }
             const int mine = static_cast<int>(t);
@@ -426,20 +429,21 @@ __global__ void __launch_bounds__(kFillThreads) paged_slots_kernel(const __grid_
 #pragma unroll
             for (int step = 16; step > 0; step /= 2)
                 if (__shfl_sync(0xffffffffu, start, owner + step) <= mine) owner += step;
-            const int to_end = __shfl_sync(0xffffffffu, end, owner) - mine, len = __shfl_sync(0xffffffffu, kv, owner);
+            const int in_new = mine - __shfl_sync(0xffffffffu, start, owner), before = __shfl_sync(0xffffffffu, past, owner);
             if (pending && mine < past_window) {
                 seq[k] = lo + owner;
-                pos[k] = len - to_end;
+                pos[k] = min(static_cast<uint32_t>(before) + static_cast<uint32_t>(in_new), static_cast<uint32_t>(INT32_MAX));
                 pending = false;
             }
         }
     }
-    int id[kFillTokens], in_page[kFillTokens];
+    int id[kFillTokens];
+    uint32_t in_page[kFillTokens];
 #pragma unroll
     for (int k = 0; k < kFillTokens; ++k) {
-        const int index = static_cast<int>(fast_div(static_cast<uint32_t>(pos[k]), a.div_page));
-        in_page[k] = pos[k] - index * p.page_size;
-        id[k] = seq[k] >= 0 && index < p.max_pages ? p.page_table[seq[k] * p.page_table_stride + index] : -1;
+        const uint32_t index = fast_div(pos[k], a.div_page);
+        in_page[k] = pos[k] - index * static_cast<uint32_t>(p.page_size);
+        id[k] = seq[k] >= 0 && index < static_cast<uint32_t>(p.max_pages) ? p.page_table[seq[k] * p.page_table_stride + index] : -1;
     }
 #pragma unroll
     for (int k = 0; k < kFillTokens; ++k) {

@@ -192,6 +192,14 @@ def test_second_derivative_raises_and_the_rule_reaches_the_backward(monkeypatch)
         A.apply_attn(q, k, v, torch.tensor([0, 3], dtype=torch.int32), distance_slopes=slopes.requires_grad_())
 
 
+@pytest.mark.parametrize("cap", [1e-50, -1e-50, 1e-40])
+def test_a_cap_that_would_be_packed_as_none(cap):
+    from packed_varlen_rope_gb300 import _attention as A
+
+    with pytest.raises(ValueError, match="score_cap"):
+        A._rule(cap, None, None, None, 0, 1)
+
+
 def test_every_rule_has_an_instance():
     """The rules that the build compiles are those that the dispatch names."""
     from packed_varlen_rope_gb300 import build

@@ -135,6 +135,26 @@ def test_lengths_out_of_range_stay_inside(dev):
             assert status.item() & (TABLE_FULL | TOKENS_PAST_END) == TABLE_FULL | TOKENS_PAST_END
 
 
+@pytest.mark.parametrize("tokens", [60, 500, 700, 3000])
+def test_slots_beside_a_length_that_no_cache_has(dev, tokens):
+    """A row whose length, and a sum of lengths, that stop at 2^31 - 1: what the table holds of it, and the
+    rows before it, have their slots all the same."""
+    m, page, width, end = pr(), 8, 40, (1 << 31) - 1
+    for past, new in (([0, 20], [10, end]), ([5, end], [3, 100]), ([0, 320, 0], [30, 10, end]), ([0, end, 0], [30, end, 50])):
+        n = len(past)
+        table = [[100 * i + j if j < -(-p // page) else -1 for j in range(width)] for i, p in enumerate(past)]
+        t, free = ints(table, dev), list(range(1000, 1100))
+        cu, kv, slots = m.paged_kv_step(ints(free, dev), ints([100], dev), t, ints(past, dev), ints(new, dev), page, tokens)
+        want, top = [], list(free)
+        for i in range(n):
+            for j in range(min(-(-past[i] // page), width), min(-(-(past[i] + new[i]) // page), width)):
+                table[i][j] = top.pop()
+            for q in range(past[i], past[i] + min(new[i], tokens)):
+                want.append(table[i][q // page] * page + q % page if q // page < width else -1)
+        assert t.tolist() == table and slots.tolist() == (want + [-1] * tokens)[:tokens]
+        assert kv.tolist() == [min(p + x, end) for p, x in zip(past, new)]
+
+
 def test_a_run_of_steps_in_a_graph(dev):
     """Captured once with the count updated in place, replayed for several steps of a batch
     whose sequences grow, end and are replaced."""

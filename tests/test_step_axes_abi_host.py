@@ -178,3 +178,23 @@ def test_step_refusals(lib, kw, want):
 
 def test_step_without_a_descriptor(lib):
     assert lib.paged_kv_step(None, None) == ERR_NULL
+
+
+def test_tensors_of_the_host_are_refused():
+    """Before the library is asked for anything."""
+    import packed_varlen_rope_gb300 as m
+
+    torch = pytest.importorskip("torch")
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="CUDA"):
+        m.paged_kv_step(torch.arange(4, dtype=i32), torch.tensor([4], dtype=i32), torch.zeros((1, 2), dtype=i32),
+                        torch.zeros(1, dtype=i32), torch.ones(1, dtype=i32), 8, 4)
+    q, k, ids = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros((3, 1, 64), dtype=torch.bfloat16), torch.zeros((2, 3), dtype=i32)
+    for call in (m.rope_axes_apply, m.apply_rope_axes):
+        with pytest.raises(ValueError):
+            call(q, k, 1e4, (16, 16), ids)
+    with pytest.raises(ValueError):
+        m.RotaryEmbedding(64, 1e4, use_cache=False, sections=(16, 16))(q, k, position_ids=ids)
+    for kw in (dict(sections=(16, 15)), dict(sections=()), dict(sections=(8,) * 5), dict(interleaved=True), dict(own_frequencies=True)):
+        with pytest.raises(ValueError):
+            m.RotaryEmbedding(64, 1e4, **kw)
