@@ -28,14 +28,14 @@
 //
 // Rules on the scores (score_rule.cuh), an instance each: the forward's exponents again, and for
 // capped scores ds = P (1 - tanh^2) (dP - D), a quarter of it in dS and the 4 in the last scaling.
-// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,800 us plain, 1,705 with prefixes, 1,732 with
-// slopes (tiles with hidden columns have a body of their own), 2,190 capped, 2,366 both: 11 cycles of
-// the FMA pipe a score where the plain instance has 3, tensor core 47 and 48 % of the time.
+// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,695 us plain, 1,705-1,726 with prefixes,
+// 1,732-1,756 with slopes, 2,190 capped, 2,366 both: 11 cycles of the FMA pipe a score where the plain
+// instance has 3, tensor core 47 and 48 % of the time.
 //
 // Bound by the tensor core: 2048 cycles a 128x128 tile for dk and dv, 1536 for dq.  32/8 heads
-// of 128, causal: one sample of 32,768 tokens 19.7-19.9 ms, 1,108-1,118 TFLOP/s by the five
-// products it needs, 1,551-1,565 by the seven it runs, and 20.0 ms over 0.8 s under the power
-// limit (the library's sustain 1,705); 8,192 tokens 1.30 and 1.35 ms.
+// of 128, causal: one sample of 32,768 tokens 19.1-19.2 ms, 1,145-1,151 TFLOP/s by the five
+// products it needs, 1,603-1,612 by the seven it runs, and 19.7-19.9 ms over 0.8 s under the power
+// limit (the library's sustain 1,705); 8,192 tokens 1.25-1.30 and 1.33 ms.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
