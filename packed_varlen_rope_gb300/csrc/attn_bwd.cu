@@ -27,7 +27,7 @@
 // memory.
 //
 // Rules on the scores (score_rule.cuh), an instance each: the forward's exponents again, and for
-// capped scores ds = P (1 - tanh^2) (dP - D), a quarter of it in dS and the 4 in the last scaling.
+// capped scores ds = P (1 - tanh^2) (dP - D), in dS times -K^2 and the rest in the last scaling.
 // 16,384 tokens of a packed batch, 32/8 heads of 128: 1,695 us plain, 1,705-1,726 with prefixes,
 // 1,732-1,756 with slopes, 2,190 capped, 2,366 both: 11 cycles of the FMA pipe a score where the plain
 // instance has 3, tensor core 47 and 48 % of the time.
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
                         }
                         packed[e / 2] = pack_bf16(p.x, p.y);
-                        if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2), here a quarter of it
+                        if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2)
                         s[e] = __float_as_uint(p.x);
                         s[e + 1] = __float_as_uint(p.y);
                     }
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             float2 g = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
                             if (!kFirst) g = add2(g, make_float2(mine.y, mine.y));
                             sum = fma2(p, g, sum);
-                            if (kCap) p = mul2(p, factor);             // ds takes p (1 - tanh^2), here a quarter of it
+                            if (kCap) p = mul2(p, factor);             // ds takes p (1 - tanh^2)
                             const float2 ds = mul2(p, g);
                             out[j / 2] = pack_bf16(ds.x, ds.y);
                         }
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // epilogue: dk and dv by two groups each, or a quarter of dq's columns a group
         const int xi = first + row;
         const bool in_use = xi < rows;
-        const float mult = second ? 1.0f : kCap ? 4.0f * a.scale : a.scale;   // (dS of capped scores: a quarter)
+        const float mult = second ? 1.0f : kCap ? a.rule.dq_scale : a.scale;
         uint32_t v[kCols / 2];
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j) {

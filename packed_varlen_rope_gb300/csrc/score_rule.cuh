@@ -46,8 +46,9 @@ constexpr bool kShaped = kCap || kBias;      // scores are exponents of 2 before
 struct ScoreRule {
     float a, k, a2;                          // capped scores: scale / cap, cap log2(e), 2 log2(e) scale / cap
     float c;                                 // others: scale log2(e)
-    float near[4], near_factor;              // kNear: x = s sum near_i s^2i, (1 - tanh^2) / 4 = 1/4 + near_factor x^2
-    float near_limit;                        // for |s| up to
+    float near[4], near_limit;               // kNear: x = s sum near_i s^2i, for |s| up to the limit
+    float unit;                              // of the gradient's factor, unit (tanh^2 - 1): K^2, as kNear has K tanh; 1 with kLarge
+    float dq_scale;                          // what dq and dk are multiplied by at the end: -scale / unit
     int32_t large;                           // the cap takes kLarge
     const float *slopes;                     // [hq]
     const int32_t *prefix;                   // [n_seqs], or NULL
@@ -82,7 +83,7 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c)
 }
 
 // Two scores to exponents of 2, plus an offset: K tanh(a s) + offset or s c + offset.  top is the
-// offset, K + offset for kAny.  factor: (1 - tanh^2) / 4, of the gradient.
+// offset, K + offset for kAny.  factor: unit (tanh^2 - 1), of the gradient.
 template <Form FORM>
 __device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2 top, float2 &factor)
 {
@@ -93,14 +94,14 @@ __device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2
         p = fma2(z, p, twice(r.near[1]));
         p = fma2(z, p, twice(r.near[0]));
         const float2 y = mul2(s, p);
-        factor = fma2(mul2(y, y), twice(r.near_factor), twice(0.25f));
+        factor = fma2(y, y, twice(-r.unit));
         return fma2(s, p, top);
     }
     const float2 e = mul2(s, twice(r.a2));
     const float2 d = add2(make_float2(ex2(e.x), ex2(e.y)), twice(1.0f));
     const float2 q = make_float2(rcp(d.x), rcp(d.y));
     float2 x = FORM == kAny ? fma2(q, twice(-2.0f * r.k), top) : add2(fma2(q, twice(-2.0f * r.k), twice(r.k)), top);
-    factor = mul2(q, fma2(q, twice(-1.0f), twice(1.0f)));
+    factor = mul2(q, fma2(q, twice(4.0f * r.unit), twice(-4.0f * r.unit)));
     if (FORM == kLarge) {
         const float2 u = mul2(s, twice(r.a)), z = mul2(u, u);
         float2 p = fma2(z, twice(kTanh5), twice(kTanh4));
@@ -109,7 +110,7 @@ __device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2
         p = fma2(z, p, twice(kTanh1));
         p = fma2(z, p, twice(kTanh0));
         const float2 t = mul2(u, p), y = fma2(t, twice(r.k), top);
-        const float2 f = mul2(twice(0.25f), fma2(t, mul2(t, twice(-1.0f)), twice(1.0f)));
+        const float2 f = fma2(t, t, twice(-1.0f));           // (unit is 1)
         if (fabsf(u.x) <= 1.0f) { x.x = y.x; factor.x = f.x; }
         if (fabsf(u.y) <= 1.0f) { x.y = y.y; factor.y = f.y; }
     }
@@ -197,14 +198,15 @@ inline ScoreRule rule_of(const AttnProblem &p)
         r.a = p.scale / p.cap;
         r.k = p.cap * kLog2;
         r.a2 = 2.0f * kLog2 * r.a;
-        // (the powers of a, and of K, have to be normal numbers)
-        r.large = !(p.cap <= kNearCap) || !(r.a >= 1e-5f && r.a <= 1e5f) || !(r.k >= 1e-15f);
+        // (the powers of a have to be normal numbers, and K^2 p dP)
+        r.large = !(p.cap <= kNearCap) || !(r.a >= 1e-5f && r.a <= 1e5f) || !(r.k >= 1e-6f);
         r.near_limit = kNearEnd / r.a;
         const float fit[4] = {kNear0, kNear1, kNear2, kNear3};
         double power = static_cast<double>(r.k) * r.a;
         for (int i = 0; i < 4 && !r.large; ++i, power *= static_cast<double>(r.a) * r.a)
             r.near[i] = static_cast<float>(power * fit[i]);
-        r.near_factor = -0.25f / (r.k * r.k);
+        r.unit = r.large ? 1.0f : r.k * r.k;
+        r.dq_scale = -p.scale / r.unit;
     }
     r.c = p.scale * kLog2;
     r.slopes = p.slopes;

@@ -96,8 +96,9 @@ def test_near_form_in_binary32(fit_tanh, cap, scale):
     x = s * p
     t = np.tanh(s.astype(np.float64) * scale / cap)
     assert np.max(np.abs(x.astype(np.float64) / 1.4426950408889634 - cap * t)) < 7e-6 * cap
-    factor = x * x * (f(-0.25) / (k * k)) + f(0.25)
-    assert np.max(np.abs(4 * factor.astype(np.float64) - (1 - t * t))) < 2e-5
+    unit = k * k
+    factor = x * x - unit
+    assert np.max(np.abs(-factor.astype(np.float64) / float(unit) - (1 - t * t))) < 2e-5
 
 
 def test_other_forms_in_binary32():
@@ -108,7 +109,7 @@ def test_other_forms_in_binary32():
     exact = np.tanh(u.astype(np.float64))
     q = f(1) / (f(1) + np.exp2(f(2 * 1.4426950408889634) * u))
     assert np.max(np.abs(f(1) - f(2) * q - exact)) < 4 * 2.0 ** -23
-    factor = 4.0 * (q * (f(1) - q)).astype(np.float64)
+    factor = -(q * (q * f(4) - f(4))).astype(np.float64)
     one_less = 1 / np.cosh(u.astype(np.float64)) ** 2
     # 1 - q cancels where q is near 1: absolute there
     assert np.max(np.abs(factor - one_less) / (one_less + 2.0 ** -6)) < 2.0 ** -15
