@@ -20,7 +20,7 @@
 // The products are issued in an order that keeps the tensor core busy while the warpgroups
 // compute, although tensor memory holds S and dP only once: for keys dP(t), dV(t), S(t+1),
 // dK(t), so that P(t) has the time of dK(t-1) and dP(t), and dS(t) that of dV(t) and S(t+1);
-// for queries, with two dP and no P to keep, S(t+1), dP(t+1), dQ(t).  Products of one issuer
+// for queries, with two dP and no P to keep, S(t+1), dP(t+1), dQ(t) (capped ones: as keys).  Products of one issuer
 // run in the order of issue: one that overwrites an operand of an earlier one follows it.
 // The issuing warp waits twice a tile: the arrival of Y is folded into the barrier of P by a
 // warp that watches it, as a wait costs some 200 cycles while the tensor core reads shared
@@ -28,9 +28,9 @@
 //
 // Rules on the scores (score_rule.cuh), an instance each: the forward's exponents again, and for
 // capped scores ds = P (1 - tanh^2) (dP - D), in dS times -K^2 and the rest in the last scaling.
-// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,695 us plain, 1,705-1,726 with prefixes,
-// 1,732-1,756 with slopes, 2,190 capped, 2,366 both: 11 cycles of the FMA pipe a score where the plain
-// instance has 3, tensor core 47 and 48 % of the time.
+// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,695 us plain, 1,705-1,733 with prefixes,
+// 1,752-1,766 with slopes, 2,315 capped (2,160 before dq was made right for D, a fourth product a tile),
+// 2,470 both.
 //
 // Bound by the tensor core: 2048 cycles a 128x128 tile for dk and dv, 1536 for dq.  32/8 heads
 // of 128, causal: one sample of 32,768 tokens 19.1-19.2 ms, 1,145-1,151 TFLOP/s by the five
@@ -38,6 +38,7 @@
 // limit (the library's sustain 1,705); 8,192 tokens 1.25-1.30 and 1.33 ms.
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -60,6 +61,13 @@ constexpr int kTile = 128;                 // rows of the resident and of the st
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ int g_attn_bwd_fault;           // bounded waits that ran out
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 
 struct BwdArgs {
     CUtensorMap x1, x2, y1, y2;
@@ -188,9 +196,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         head0 = from / per_pass;
         y0_first = y_lo + from - head0 * per_pass;
     }
-    // tensor memory; for queries dP is there twice
-    constexpr uint32_t kColS = 0, kColP = 128, kCol1 = KEYS ? 256 : 384, kCol2 = 256 + DP;
-    constexpr uint32_t kNextP = KEYS ? 0 : 128;
+    // Queries of capped scores take the products as keys do, with acc2 += P (1 - tanh^2) Y1: what the
+    // epilogue needs to make dq right for the D that only the whole row tells.
+    constexpr bool kWhole = kCap && !KEYS, kTwo = KEYS || kWhole;
+    // tensor memory; for queries dP is there twice, but with two accumulators
+    constexpr uint32_t kColS = 0, kColP = 128, kCol1 = kTwo ? 256 : 384, kCol2 = 256 + DP;
+    constexpr uint32_t kNextP = kTwo ? 0 : 128;
 
     bool ok_softmax = true;
     if (n_all == 0) {
@@ -319,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             tc_commit(which == 0 ? s_full : dp_full + 8 * (t & 1));
             if (!KEYS && which == 1) tc_commit(y_empty + 8 * place(t, which));
         };
-        // acc1 += dS Y1 (which = 0) or acc2 += P Y2 (1); one elected thread
+        // acc1 += dS Y1 (which = 0) or acc2 += P Y2 (1; capped queries: P Y1); one elected thread
         auto accumulate = [&](int t, int which) {
             const uint32_t d = utmem + (which == 0 ? kCol1 : kCol2);
             const uint32_t from = utmem + (which == 0 ? kColP + (t & 1) * kNextP : kColS);
-            const uint32_t y = d_ymn + place(t, which) * kStep;
+            const uint32_t y = d_ymn + place(t, KEYS ? which : 0) * kStep;
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
                 mma_ts(d, from + 32 * (s / 2) + 8 * (s % 2), y + s * (2048 >> 4), kDescA, t > 0 || s > 0);
-            tc_commit(y_empty + 8 * place(t, which));
+            if (KEYS || which == 0) tc_commit(y_empty + 8 * place(t, which));
             if (KEYS && which == 0) tc_commit(st_empty + 8 * (t & 1));
             if (which == 0 && t + 1 == n_tiles) tc_commit(done);
         };
@@ -341,17 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         }
         for (int t = 0; ok && t < n_tiles; ++t) {
             const bool more = t + 1 < n_tiles;
-            if (KEYS || more) wait(p_full, t);
+            if (kTwo || more) wait(p_full, t);
             if (ok && elect_one()) {
-                if (KEYS) accumulate(t, 1);
+                if (kTwo) accumulate(t, 1);
                 if (more) scores(t + 1, 0);
-                if (!KEYS && more) scores(t + 1, 1);
+                if (!kTwo && more) scores(t + 1, 1);
             }
             __syncwarp();
             wait(ds_full + 8 * (t & 1), t >> 1);
             if (ok && elect_one()) {
                 accumulate(t, 0);
-                if (KEYS && more) scores(t + 1, 1);
+                if (kTwo && more) scores(t + 1, 1);
             }
             __syncwarp();
         }
@@ -361,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         }
         __syncwarp();
     }
+    float lacks = 0.0f;                                                // of the row's D, shaped scores' queries
     if (n_tiles > 0 && warp < kMmaWarp) {
         // ---------------------------------------------------------- softmax
         // a row of X is four threads', 32 of a tile's columns each
@@ -378,12 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         // The D that comes in is dout . o with o rounded to bf16.  Against the few keys of a
         // sample's first rows that error is as large as the rounding of ds; where all keys of
         // the rows are in one tile, D is taken from them instead, D = sum_j p dP, and kept for
-        // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).  With shaped scores every
-        // row's D is made whole for that pass: the ds of capped scores, sharp as they may be, are smaller than
-        // the terms they are the difference of, and dk was off by 4.1e-3 where it is by 2.5e-3.
+        // the pass over the keys (with n keys the error shrinks as 1 / sqrt(n)).  Where scores are sharp it
+        // matters in long rows too, as D is nearly the dP of few keys.  With shaped scores D is made whole
+        // for the pass over the keys by what it lacks, sum_j p (dP - D): dk of scores of deviation 6 was off
+        // by 4.1e-3 and is by 2.4e-3.  With capped ones dq is made right too, dq -= lacks sum_j p (1 - tanh^2) k_j,
+        // by a fourth product a tile (4.2e-3 and 2.4e-3).
         const bool single = !KEYS && n_tiles == 1;
         const bool line = a.causal && prefix <= 0;                     // of a biased row: its keys are on one side
-        float lacks = 0.0f;
         // the sum over a row's four threads, whose warps all come here (after a wait that ran out too)
         auto row_sum = [&](float x) {
             float *swap = reinterpret_cast<float *>(smem + Sh::kOffStats);   // [quarter][row]; of keys' statistics, not here
@@ -416,12 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (KEYS && ok) ok = warp_wait(st_full + 8 * (t & 1), (t >> 1) & 1, &s_abort, &g_attn_bwd_fault);
             if (!ok && !single) break;         // (a single tile's warps meet below in any case)
             tc_fence_after();
-            uint32_t s[32], packed[16];
+            uint32_t s[32], packed[16];        // (capped queries: p as fp16)
             // how far the first column is from this row: the bias takes its magnitude
             const float far = static_cast<float>(y0 - xi);
             tmem_ld32(t_s, s);
             tc_wait_ld(s);
-            if (!KEYS) {                                               // S is free
+            if (!kTwo) {                                               // S is free
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
@@ -434,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             auto weights = [&](auto form, auto hides) {
                 constexpr Form kForm = decltype(form)::value;
                 constexpr bool kHides = decltype(hides)::value;        // some column is hidden
-                Tops<kForm> tops(a.rule, KEYS && kForm == kLine ? -slope2 : slope2, far, 0.0f);
+                Tops<kForm> tops(a.rule, KEYS && kForm == kLine ? -slope2 : slope2, far, kWhole ? mine.x : 0.0f);
+                uint32_t half[8];
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 nl = KEYS ? smem_load4(st + 4 * j) : make_float4(mine.x, mine.x, mine.x, mine.x);
@@ -444,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                         const float2 n2 = h == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w);
                         const float2 score = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                         float2 p, factor;
-                        if (kShaped)
+                        if (kWhole) p = exponent2<kForm>(a.rule, score, tops.next(e), factor);
+                        else if (kShaped)
                             p = exponent2<kForm>(a.rule, score, kBias || kForm == kAny ? add2(tops.next(e), n2) : n2, factor);
                         else p = fma2(score, c2, n2);
                         p.x = ex2(p.x);
@@ -453,23 +468,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             if (e < from || e >= to) p.x = 0.0f;
                             if (e + 1 < from || e + 1 >= to) p.y = 0.0f;
                         }
-                        packed[e / 2] = pack_bf16(p.x, p.y);
+                        packed[e / 2] = kWhole ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
                         if (kCap) p = mul2(p, factor);                 // ds takes p (1 - tanh^2)
                         s[e] = __float_as_uint(p.x);
                         s[e + 1] = __float_as_uint(p.y);
+                        if (kWhole) half[e / 2 % 8] = pack_bf16(p.x, p.y);
                     }
+                    if (kWhole && j % 16 == 12) tmem_st8(t_s + 8 * (j / 16), half);
                 }
             };
             // two bodies for tiles with hidden columns and without: as selects in one they would cost
             // each column 2.6 instructions of 16
-            if (KEYS || !kShaped)
+            if (kTwo || !kShaped)
                 by_form(a.rule, s, xi >= rows, line, [&](auto form) {
                     if (masked) weights(form, std::true_type{});
                     else weights(form, std::false_type{});
                 });
             // P and dS take the first half of the columns this thread has read
-            if (KEYS) {
-                tmem_st16(t_s, packed);
+            if (kTwo) {
+                if (KEYS) tmem_st16(t_s, packed);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -479,8 +496,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             if (!ok && !single) break;
             tc_fence_after();
             const uint32_t t_dp = t_p + (t & 1) * kNextP;
-            if (!KEYS && kShaped) {
-                // Queries, shaped scores: weights and ds together, as dP is long there; a half at a time,
+            if (kWhole) {
+                // the row's sum of p (dP - D), with `first` that of p dP alone
+                auto gradients = [&](auto first) {
+                    constexpr bool kFirst = decltype(first)::value;
+                    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t dp[16], out[8];
+                        tmem_ld16(t_dp + 16 * h, dp);
+                        tc_wait_ld16(dp);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const int e = 16 * h + j;
+                            float2 g = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
+                            if (!kFirst) g = add2(g, make_float2(mine.y, mine.y));
+                            sum = fma2(unpack_f16(packed[e / 2]), g, sum);
+                            const float2 ds = mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), g);
+                            out[j / 2] = pack_bf16(ds.x, ds.y);
+                        }
+                        if (!kFirst) tmem_st8(t_dp + 8 * h, out);
+                    }
+                    return sum.x + sum.y;
+                };
+                if (single) mine.y = -row_sum(gradients(std::true_type{}));
+                lacks += gradients(std::false_type{});
+            } else if (!KEYS && kShaped) {
+                // Queries, biased scores: weights and ds together, as dP is long there; a half at a time,
                 // with no more than a half's registers beside the scores.  Returns the row's sum of
                 // p (dP - D), with `first` that of p dP alone.
                 auto gradients = [&](auto form, auto hides, auto first) {
@@ -508,7 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                             float2 g = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
                             if (!kFirst) g = add2(g, make_float2(mine.y, mine.y));
                             sum = fma2(p, g, sum);
-                            if (kCap) p = mul2(p, factor);             // ds takes p (1 - tanh^2)
                             const float2 ds = mul2(p, g);
                             out[j / 2] = pack_bf16(ds.x, ds.y);
                         }
@@ -560,9 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
         if (!KEYS && kShaped) {
             // the D that came in was short of this much (zero where it was taken from the weights): the
             // pass over the keys has it whole
-            const float more = row_sum(lacks);
+            lacks = row_sum(lacks);
             if (quarter == 0 && live && xi < rows && mine.x != -INFINITY)
-                a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y - more;
+                a.stats[static_cast<int64_t>(xhead) * a.n_tokens + where.start + xi].y = mine.y - lacks;
         }
         if (ok && n_tiles > 0) {
             ok = warp_wait(done, 0, &s_abort, &g_attn_bwd_fault);
@@ -623,6 +664,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = 0u;
+            }
+            if (kWhole && n_tiles > 0) {
+                uint32_t more[16];
+                tmem_ld16(tmem + lanes + kCol2 + col0 + 16 * j, more);
+                tc_wait_ld16(more);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(fmaf(-lacks, __uint_as_float(more[e]), __uint_as_float(o[e])));
             }
             if (KEYS && ranks > 1) {
 #pragma unroll

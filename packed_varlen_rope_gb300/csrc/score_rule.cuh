@@ -16,8 +16,8 @@
 //           below the cap keep theirs; kAny's beyond; chosen score by score
 //
 // 16,384 tokens of a packed batch, 32/8 heads of 128, forward and backward: all chunks kNear (scores of
-// deviation 6, cap 50) 648 and 2,190 us, nearly all kAny (cap 20) 841 and 2,546 us, kLarge 1,271 and
-// 3,180 us; without a cap 502 and 1,695 us.  kAny for every second, third or fourth pair among kNear,
+// deviation 6, cap 50) 645 and 2,315 us, nearly all kAny (cap 20) 841 and 2,747 us, kLarge 1,270 and
+// 3,306 us; without a cap 502 and 1,695 us.  kAny for every second, third or fourth pair among kNear,
 // to spread the work over the pipes, took 20 to 25 % more forward and 0 to 3 % backward.
 #pragma once
 

@@ -170,6 +170,30 @@ def test_values_far_from_one_at_the_cap(dev, vscale, towards):
         assert float((lse.double() - ref["lse"]).abs().max()) <= ref["rule"] + 2.0 ** -11 * (1 + float(ref["lse"].abs().max()))
 
 
+@pytest.mark.parametrize("lengths,hq,hkv,d", [([1500], 8, 2, 128), ([130, 300, 900], 4, 4, 64), ([100, 128, 77], 4, 1, 80)], ids=str)
+@pytest.mark.parametrize("cap,sloped", [(50.0, False), (20.0, False), (100.0, True), (200.0, False)])
+def test_gradients_of_sharp_capped_scores(dev, lengths, hq, hkv, d, cap, sloped):
+    """Rows that one key has nearly to itself: their D is nearly that key's dP, and the rounding of the
+    output that comes in would show.  Off by the roundings of ds and of the result to bf16 alone: 2^-8 / sqrt(3)
+    of a value's binade is 1.66e-3 of the values (mean square, mantissas spread evenly over their
+    logarithm), both 2.35e-3; with 16e-6 cap from the tanh at most, 1.5e-3 of it on average for these
+    caps, sqrt(2.35^2 + 1.5^2) = 2.8e-3."""
+    m, g = pr(), torch.Generator("cuda").manual_seed(31)
+    n = sum(lengths)
+    q, k, v, dout = (torch.randn((n, h, d), generator=g, device=dev).bfloat16() for h in (hq, hkv, hkv, hq))
+    q *= 6
+    cu = torch.tensor([sum(lengths[:i]) for i in range(len(lengths) + 1)], dtype=torch.int32, device=dev)
+    slopes = series(hq, dev) if sloped else None
+    o, lse = m.attn_varlen_fwd(q, k, v, cu, return_lse=True, score_cap=cap, distance_slopes=slopes)
+    got = m.attn_varlen_bwd(dout, q, k, v, o, lse, cu, score_cap=cap, distance_slopes=slopes)
+    refs = [sample_reference(*(x[a:b] for x in (q, k, v)), 1 / math.sqrt(d), cap, slopes, dout=dout[a:b])
+            for a, b in zip(cu.tolist(), cu.tolist()[1:])]
+    for i, name in enumerate(("dq", "dk")):
+        want = torch.cat([r[name][0] for r in refs])
+        err = float((got[i].double() - want).norm() / want.norm())
+        assert err <= 2.8e-3, (name, err)
+
+
 @pytest.mark.parametrize("cap,scale", [(1e-25, 1e-22), (1e-3, 1e3), (1e-12, 1e-16), (1e20, 1e16), (2e4, 0.125)])
 def test_caps_and_scales_at_the_ends(dev, cap, scale):
     """Caps and scales whose powers leave binary32: scores moderate against the cap all the same."""
