@@ -20,8 +20,9 @@
 // The products are issued in an order that keeps the tensor core busy while the warpgroups
 // compute, although tensor memory holds S and dP only once: for keys dP(t), dV(t), S(t+1),
 // dK(t), so that P(t) has the time of dK(t-1) and dP(t), and dS(t) that of dV(t) and S(t+1);
-// for queries, with two dP and no P to keep, S(t+1), dP(t+1), dQ(t) (capped ones: as keys).  Products of one issuer
-// run in the order of issue: one that overwrites an operand of an earlier one follows it.
+// for queries, with two dP and no P to keep, S(t+1), dP(t+1), dQ(t) (of capped scores: as for keys).
+// Products of one issuer run in the order of issue: one that overwrites an operand of an earlier one
+// follows it.
 // The issuing warp waits twice a tile: the arrival of Y is folded into the barrier of P by a
 // warp that watches it, as a wait costs some 200 cycles while the tensor core reads shared
 // memory.

@@ -10,7 +10,7 @@
 // (cos, sin), shared by all heads, then the heads stream through.  Every element is read once
 // and written once: the bound is HBM for long packs (16,384 tokens of 32/8 heads of 128, 336 MB a
 // direction: 54 us, 6.2 TB/s, the evaluation of 64 angles a token beside 640 units of 32 bytes; an
-// append of 16,015 tokens of 64/8 heads 116 us, 6.0 TB/s; 4,520 tokens of 16/16 heads of 80, which
+// append of 17,043 tokens of 64/8 heads 116.5 us, 6.0 TB/s; 4,520 tokens of 16/16 heads of 80, which
 // stay in L2, 12.7 us, one wave of CTAs), the chain of dependent loads for a decoding step (8 tokens
 // 4.1 us, 11 through Python).  Registers are held to 11 resident CTAs an SM (the append: 10): 108 us
 // for both directions where 9 CTAs took 113 and the compiler's choice 122.
