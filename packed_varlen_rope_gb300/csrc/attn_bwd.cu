@@ -29,9 +29,8 @@
 //
 // Rules on the scores (score_rule.cuh), an instance each: the forward's exponents again, and for
 // capped scores ds = P (1 - tanh^2) (dP - D), in dS times -K^2 and the rest in the last scaling.
-// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,695 us plain, 1,705-1,733 with prefixes,
-// 1,752-1,766 with slopes, 2,315 capped (2,160 before dq was made right for D, a fourth product a tile),
-// 2,470 both.
+// 16,384 tokens of a packed batch, 32/8 heads of 128: 1,690 us plain, 1,711-1,733 with prefixes,
+// 1,731-1,766 with slopes, 2,290 capped (a fourth product of dq a tile, for D, is 7 % of it), 2,411 both.
 //
 // Bound by the tensor core: 2048 cycles a 128x128 tile for dk and dv, 1536 for dq.  32/8 heads
 // of 128, causal: one sample of 32,768 tokens 19.1-19.2 ms, 1,145-1,151 TFLOP/s by the five

@@ -22,9 +22,9 @@
 // Shaped scores (capped, biased) become exponents 32 columns at a time between tensor memory and the
 // exponential; with a bias by distance the key tiles go downwards, so that causal rows meet their
 // largest exponents first.  They hold the softmax warps, not the tensor core, back: the packed batch
-// below, 32/8 heads of 128, 500 us plain, 509 with prefixes, 555 with slopes, 648 capped, 872 both
+// below, 32/8 heads of 128, 501 us plain, 515 with prefixes, 565 with slopes, 595 capped, 793 both
 // (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64
-// 330, 332, 401, 423 and 619 us.
+// 329, 331, 400, 406 and 598 us.
 //
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
 // elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
@@ -97,8 +97,8 @@ struct Shared {
 // Capped exponents that stay within +-80 need no maximum, a quarter of K does for all rows: weights
 // are within 2^60 and 2^-100, so that they and the sums of 2^24 of them keep their precision in
 // binary32, and products with values up to 2^43 their range; the two halves of a row need not meet.
-// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 648 us,
-// 872 with the maximum; both in one instance cost the first 803).
+// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 595 us,
+// 797 with the maximum; with both in one instance the first took 803 where it took 648 by itself).
 constexpr bool kFixed = kRule == kRuleCap;
 
 template <int DP, bool PAGED>

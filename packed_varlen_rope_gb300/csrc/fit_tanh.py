@@ -5,6 +5,7 @@ is i pi/2, so they converge fast):
 
 * near: degree 7 on |u| <= 0.8, interpolating tanh itself: absolute error below 6.7e-6, which moves a
   score capped at 50 by less than 3.4e-4, a tenth of what rounding the weight to bf16 may do (2^-8);
+* small: degree 5 on |u| <= 0.5, the same way: below 5.6e-6;
 * large: degree 11 on |u| <= 1, interpolating tanh(u)/u in u^2: relative error below 6.1e-7, for caps
   so large that scores far below them have to keep theirs.
 
@@ -14,16 +15,20 @@ from __future__ import annotations
 
 import numpy as np
 
-NEAR = 0.8
+NEAR, SMALL = 0.8, 0.5
 
 
-def near(degree: int = 3):
+def near(degree: int = 3, end: float = NEAR):
     """P of the absolute fit, in u^2."""
     n = 2 * degree + 3                                                   # zeros of the next odd term
     k = np.arange(n)
-    u = NEAR * np.cos((2 * k + 1) * np.pi / (2 * n))
+    u = end * np.cos((2 * k + 1) * np.pi / (2 * n))
     odd = np.vander(u * u, degree + 1, increasing=True) * u[:, None]
     return np.linalg.lstsq(odd, np.tanh(u), rcond=None)[0]
+
+
+def small():
+    return near(2, SMALL)
 
 
 def target(z):
@@ -41,8 +46,8 @@ def large(degree: int = 5):
     return p(np.polynomial.Polynomial([-1.0, 2.0])).coef                 # x = 2 z - 1
 
 
-def near_error(coef, n=40001):
-    u = np.linspace(0.0, NEAR, n)
+def near_error(coef, n=40001, end: float = NEAR):
+    u = np.linspace(0.0, end, n)
     return float(np.max(np.abs(u * np.polynomial.polynomial.polyval(u * u, coef) - np.tanh(u))))
 
 
@@ -52,6 +57,7 @@ def large_error(coef, n=40001):
 
 
 if __name__ == "__main__":
-    for name, c, e in (("near", near(), near_error(near())), ("large", large(), large_error(large()))):
+    for name, c, e in (("near", near(), near_error(near())), ("small", small(), near_error(small(), end=SMALL)),
+                       ("large", large(), large_error(large()))):
         print("%s: error %.3g" % (name, e))
         print("    " + ", ".join("%.9ef" % v for v in c))

@@ -6,19 +6,21 @@
 //
 // Scores become exponents of 2 before the softmax, x = y log2(e): K tanh(u) with K = cap log2(e) and
 // u = s scale / cap for capped ones, s c with c = scale log2(e) for others.  The tanh takes one of
-// three forms:
+// four forms:
 //
-//   kNear   K u P(u^2), degree 7: 5 packed operations for two scores, absolute error 6.7e-6 of the cap
-//           (fit_tanh.py); for caps up to 128, where no score of the warp's chunk is past 0.8 caps
+//   kSmall  K u P(u^2), degree 5: 4 packed operations for two scores, absolute error 5.6e-6 of the cap
+//           (fit_tanh.py); for caps up to 128, where no score of the warp's chunk is past half the cap
+//   kNear   the same of degree 7, 5 operations, 6.7e-6; where none is past 0.8 caps
 //   kAny    K (1 - 2 q), q = 1 / (1 + e^2u), off by about 2^-22 K: 3 packed operations, but two special
 //           functions a score; for such caps elsewhere
 //   kLarge  caps past 128: u P(u^2), degree 11, relative error 6.1e-7, for |u| <= 1, so that scores far
 //           below the cap keep theirs; kAny's beyond; chosen score by score
 //
-// 16,384 tokens of a packed batch, 32/8 heads of 128, forward and backward: all chunks kNear (scores of
-// deviation 6, cap 50) 645 and 2,315 us, nearly all kAny (cap 20) 841 and 2,747 us, kLarge 1,270 and
-// 3,306 us; without a cap 502 and 1,695 us.  kAny for every second, third or fourth pair among kNear,
-// to spread the work over the pipes, took 20 to 25 % more forward and 0 to 3 % backward.
+// 16,384 tokens of a packed batch, 32/8 heads of 128, forward and backward: nearly all chunks kSmall
+// (scores of deviation 6, cap 50) 591-597 and 2,290 us (with kNear in its place 645 and 2,315), nearly
+// all kAny (cap 20) 849 and 2,810 us, kLarge 1,212 and 3,265 us; without a cap 501 and 1,686 us.  kAny
+// for every second, third or fourth pair among kNear, to spread the work over the pipes, took 20 to
+// 25 % more forward and 0 to 3 % backward.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -47,6 +49,7 @@ struct ScoreRule {
     float a, k, a2;                          // capped scores: scale / cap, cap log2(e), 2 log2(e) scale / cap
     float c;                                 // others: scale log2(e)
     float near[4], near_limit;               // kNear: x = s sum near_i s^2i, for |s| up to the limit
+    float small[3], small_limit;             // kSmall
     float unit;                              // of the gradient's factor, unit (tanh^2 - 1): K^2, as kNear has K tanh; 1 with kLarge
     float dq_scale;                          // what dq and dk are multiplied by at the end: -scale / unit
     int32_t large;                           // the cap takes kLarge
@@ -56,11 +59,13 @@ struct ScoreRule {
 
 constexpr float kNearCap = 128.0f, kNearEnd = 0.8f;
 constexpr float kNear0 = 9.999243658e-01f, kNear1 = -3.317269685e-01f, kNear2 = 1.238189323e-01f, kNear3 = -3.164692249e-02f;
+constexpr float kSmallEnd = 0.5f;
+constexpr float kSmall0 = 9.999222584e-01f, kSmall1 = -3.308141013e-01f, kSmall2 = 1.124106519e-01f;
 constexpr float kTanh0 = 9.999993948e-01f, kTanh1 = -3.332895137e-01f, kTanh2 = 1.328072065e-01f, kTanh3 = -5.158598840e-02f,
                 kTanh4 = 1.672085518e-02f, kTanh5 = -3.058229038e-03f;
 
 // (kLine: uncapped scores, biased, of rows that see keys on one side of them alone)
-enum Form { kNear, kAny, kLarge, kLine };
+enum Form { kSmall, kNear, kAny, kLarge, kLine };
 template <Form FORM>
 using FormTag = std::integral_constant<Form, FORM>;
 
@@ -88,11 +93,17 @@ template <Form FORM>
 __device__ __forceinline__ float2 exponent2(const ScoreRule &r, float2 s, float2 top, float2 &factor)
 {
     if (!kCap) return fma2(s, twice(r.c), top);
-    if (FORM == kNear) {
+    if (FORM == kNear || FORM == kSmall) {
         const float2 z = mul2(s, s);
-        float2 p = fma2(z, twice(r.near[3]), twice(r.near[2]));
-        p = fma2(z, p, twice(r.near[1]));
-        p = fma2(z, p, twice(r.near[0]));
+        float2 p;
+        if (FORM == kSmall) {
+            p = fma2(z, twice(r.small[2]), twice(r.small[1]));
+            p = fma2(z, p, twice(r.small[0]));
+        } else {
+            p = fma2(z, twice(r.near[3]), twice(r.near[2]));
+            p = fma2(z, p, twice(r.near[1]));
+            p = fma2(z, p, twice(r.near[0]));
+        }
         const float2 y = mul2(s, p);
         factor = fma2(y, y, twice(-r.unit));
         return fma2(s, p, top);
@@ -172,14 +183,19 @@ __device__ __forceinline__ void by_form(const ScoreRule &r, const uint32_t (&s)[
         else fn(FormTag<kNear>{});
         return;
     }
+    if (r.large) {
+        fn(FormTag<kLarge>{});
+        return;
+    }
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < N; j += 2)
         top[(j >> 1) & 1] = max3_abs(top[(j >> 1) & 1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
     // (a NaN is passed over, and comes through every form)
-    if (r.large) fn(FormTag<kLarge>{});
-    else if (__any_sync(0xffffffffu, !hidden && fmaxf(top[0], top[1]) > r.near_limit)) fn(FormTag<kAny>{});
-    else fn(FormTag<kNear>{});
+    const float most = hidden ? 0.0f : fmaxf(top[0], top[1]);
+    if (!__any_sync(0xffffffffu, most > r.small_limit)) fn(FormTag<kSmall>{});
+    else if (!__any_sync(0xffffffffu, most > r.near_limit)) fn(FormTag<kNear>{});
+    else fn(FormTag<kAny>{});
 }
 
 // The keys at the start of a sequence that all its rows see.
@@ -201,10 +217,13 @@ inline ScoreRule rule_of(const AttnProblem &p)
         // (the powers of a have to be normal numbers, and K^2 p dP)
         r.large = !(p.cap <= kNearCap) || !(r.a >= 1e-5f && r.a <= 1e5f) || !(r.k >= 1e-6f);
         r.near_limit = kNearEnd / r.a;
-        const float fit[4] = {kNear0, kNear1, kNear2, kNear3};
+        r.small_limit = kSmallEnd / r.a;
+        const float fit[4] = {kNear0, kNear1, kNear2, kNear3}, small[3] = {kSmall0, kSmall1, kSmall2};
         double power = static_cast<double>(r.k) * r.a;
-        for (int i = 0; i < 4 && !r.large; ++i, power *= static_cast<double>(r.a) * r.a)
+        for (int i = 0; i < 4 && !r.large; ++i, power *= static_cast<double>(r.a) * r.a) {
             r.near[i] = static_cast<float>(power * fit[i]);
+            if (i < 3) r.small[i] = static_cast<float>(power * small[i]);
+        }
         r.unit = r.large ? 1.0f : r.k * r.k;
         r.dq_scale = -p.scale / r.unit;
     }

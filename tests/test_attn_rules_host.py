@@ -76,23 +76,26 @@ def fit_tanh():
 
 
 def test_tanh_constants_are_the_fits(fit_tanh):
-    for name, want in (("kNear", fit_tanh.near()), ("kTanh", fit_tanh.large())):
+    for name, want in (("kNear", fit_tanh.near()), ("kSmall", fit_tanh.small()), ("kTanh", fit_tanh.large())):
         got = kernel_constants(name, len(want))
         assert np.all(np.abs(got - want) <= 1e-9 * np.abs(want) + 1e-10)
+    assert fit_tanh.near_error(fit_tanh.small(), end=fit_tanh.SMALL) < 5.6e-6
     assert fit_tanh.near_error(fit_tanh.near()) < 6.7e-6 and fit_tanh.large_error(fit_tanh.large()) < 6.1e-7
 
 
 @pytest.mark.parametrize("cap,scale", [(50.0, 0.088), (128.0, 0.125), (1.0, 1.0), (0.03, 20.0)])
-def test_near_form_in_binary32(fit_tanh, cap, scale):
-    """Step by step: within 7e-6 of the cap up to 0.8 of it, and the factor within 2e-5."""
+@pytest.mark.parametrize("name,end", [("kNear", 0.8), ("kSmall", 0.5)])
+def test_near_forms_in_binary32(fit_tanh, cap, scale, name, end):
+    """Step by step: within 7e-6 of the cap up to 0.8 or half of it, and the factor within 2e-5."""
     f = np.float32
     a, k = f(scale) / f(cap), f(cap) * f(1.4426950408889634)
-    coef = [f(float(k) * float(a) ** (2 * i + 1) * x) for i, x in enumerate(kernel_constants("kNear", 4))]
-    s = np.linspace(-0.8, 0.8, 200001).astype(f) * (f(1) / a)
+    assert end == {"kNear": fit_tanh.NEAR, "kSmall": fit_tanh.SMALL}[name]
+    coef = [f(float(k) * float(a) ** (2 * i + 1) * x) for i, x in enumerate(kernel_constants(name, 4 if name == "kNear" else 3))]
+    s = np.linspace(-end, end, 200001).astype(f) * (f(1) / a)
     z = s * s
-    p = z * coef[3] + coef[2]
-    p = z * p + coef[1]
-    p = z * p + coef[0]
+    p = np.full_like(z, coef[-1])
+    for x in coef[-2::-1]:
+        p = z * p + x
     x = s * p
     t = np.tanh(s.astype(np.float64) * scale / cap)
     assert np.max(np.abs(x.astype(np.float64) / 1.4426950408889634 - cap * t)) < 7e-6 * cap
