@@ -22,9 +22,9 @@
 // Shaped scores (capped, biased) become exponents 32 columns at a time between tensor memory and the
 // exponential; with a bias by distance the key tiles go downwards, so that causal rows meet their
 // largest exponents first.  They hold the softmax warps, not the tensor core, back: the packed batch
-// below, 32/8 heads of 128, 501 us plain, 515 with prefixes, 565 with slopes, 595 capped, 793 both
+// below, 32/8 heads of 128, 501 us plain, 515 with prefixes, 565 with slopes, 635 capped, 795 both
 // (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64
-// 329, 331, 400, 406 and 598 us.
+// 329, 331, 400, 438 and 598 us.
 //
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
 // elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
@@ -97,8 +97,11 @@ struct Shared {
 // Capped exponents that stay within +-80 need no maximum, a quarter of K does for all rows: weights
 // are within 2^60 and 2^-100, so that they and the sums of 2^24 of them keep their precision in
 // binary32, and products with values up to 2^43 their range; the two halves of a row need not meet.
-// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 595 us,
-// 797 with the maximum; with both in one instance the first took 803 where it took 648 by itself).
+// Where a maximum makes the largest weight 1, here it is rounded to bf16 too: the output is divided by
+// the sum of the rounded weights, so that a row of one key is that key's value (o off by 1.8-2.2e-3 of
+// itself, 2.3-2.4e-3 without, for 40 us of 635; lse takes the sum of the weights as they are).
+// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 635 us,
+// 797 with the maximum; both in one instance cost the first a quarter).
 constexpr bool kFixed = kRule == kRuleCap;
 
 template <int DP, bool PAGED>
@@ -431,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         // largest x.  A large shift is not folded into the exponents' last operation: their rounding
         // would differ from that of the maximum, and the largest weight be far from 1.
         const bool line = a.causal && prefix <= 0;
+        float2 rounded = make_float2(0.0f, 0.0f);                       // fixed maximum: sum of the weights as bf16
         auto shaped_pass = [&](auto folds, int i, float shift, uint32_t *p, float &high) {
             constexpr bool kFold = decltype(folds)::value;
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -469,6 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     e.y = ex2(e.y);
                     sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
                     (kFixed ? packed[j / 2] : p[16 * h + j / 2]) = pack_bf16(e.x, e.y);
+                    if (kFixed)
+                        rounded = add2(rounded, make_float2(__uint_as_float(packed[j / 2] << 16), __uint_as_float(packed[j / 2] & 0xffff0000u)));
                 }
                 if (kFixed) {
                     tmem_st16(t_p + 16 * h, packed);
@@ -575,12 +581,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * x);
         }
+        float norm = 0.0f;
         if (count[x] > 0) {
             if (ok) ok = warp_wait(o_done + 8 * x, 0, &s_abort, &g_attn_fault);
             tc_fence_after();
             s_swap[count[x] & 1][x][half][row] = l;
+            if (kFixed) s_swap[count[x] & 1 ^ 1][x][half][row] = norm = rounded.x + rounded.y;
             named_barrier(pair, 64);
             l += s_swap[count[x] & 1][x][half ^ 1][row];
+            if (kFixed) norm += s_swap[count[x] & 1 ^ 1][x][half ^ 1][row];
         }
         // epilogue: rows outside the pack, and rows that see no key, are zero (tiles that all
         // rows in use see whole are not masked, so such rows may have summed anything).  No
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         if (lim == 0) l = 0.0f;
         const int tok = where.start + i_tok;
         const int head = kvh * a.group + (row - static_cast<int>(fast_div(row, a.div_group)) * a.group);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / (kFixed ? norm : l);
         const bool joined = PAGED && a.splits > 1;
         const int64_t at = static_cast<int64_t>(tok) * a.hq + head;
         if (ok && mine && half == 0) {

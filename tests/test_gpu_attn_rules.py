@@ -170,6 +170,25 @@ def test_values_far_from_one_at_the_cap(dev, vscale, towards):
         assert float((lse.double() - ref["lse"]).abs().max()) <= ref["rule"] + 2.0 ** -11 * (1 + float(ref["lse"].abs().max()))
 
 
+@pytest.mark.parametrize("rule", [dict(score_cap=0.5), dict(score_cap=5.0), dict(score_cap=50.0), dict(score_cap=100.0),
+                                  dict(score_cap=500.0), dict(slopes=True), dict(score_cap=30.0, slopes=True)], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_of_one_key_is_its_value(dev, rule, d):
+    """The first row of a causal sample, to the bit: its weight and the sum it is divided by are the same."""
+    m, g = pr(), torch.Generator("cuda").manual_seed(41)
+    lengths = [1] * 150 + [2, 70, 300, 1, 513]
+    n, hq, hkv = sum(lengths), 8, 2
+    rule = dict(rule)
+    if rule.pop("slopes", False):
+        rule["distance_slopes"] = series(hq, dev)
+    cu = torch.tensor([sum(lengths[:i]) for i in range(len(lengths) + 1)], dtype=torch.int32, device=dev)
+    q, k, v = (torch.randn((n, h, d), generator=g, device=dev).bfloat16() for h in (hq, hkv, hkv))
+    first = cu[:-1].long()
+    for sharp in (0.1, 1.0, 6.0, 40.0):
+        o = m.attn_varlen_fwd(q * sharp, k, v, cu, **rule)
+        assert torch.equal(o[first], v[first].repeat_interleave(hq // hkv, dim=1))
+
+
 @pytest.mark.parametrize("lengths,hq,hkv,d", [([1500], 8, 2, 128), ([130, 300, 900], 4, 4, 64), ([100, 128, 77], 4, 1, 80)], ids=str)
 @pytest.mark.parametrize("cap,sloped", [(50.0, False), (20.0, False), (100.0, True), (200.0, False)])
 def test_gradients_of_sharp_capped_scores(dev, lengths, hq, hkv, d, cap, sloped):
