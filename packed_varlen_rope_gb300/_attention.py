@@ -489,11 +489,12 @@ def apply_attn(q, k, v, cu_seqlens, causal: bool = True, scale: Optional[float] 
     """Differentiable attention within each sample of a pack: ``attn_varlen_fwd`` with the
     gradients of ``attn_varlen_bwd``.  q, k, v may be any bf16 CUDA [T, heads, d] tensors;
     those that the kernels cannot address (broadcast ones) are copied.  Differentiable once: a
-    second derivative raises an error.  ``distance_slopes`` that require a gradient are refused."""
+    second derivative raises an error.  ``distance_slopes`` that require a gradient are refused where
+    gradients are recorded (they are constants): detach a parameter's."""
     global _Attn
     if _Attn is None:
         _Attn = _attn_function()
-    if distance_slopes is not None and distance_slopes.requires_grad:
+    if distance_slopes is not None and distance_slopes.requires_grad and (_torch or _load_torch()).is_grad_enabled():
         raise ValueError("distance_slopes are constants: they get no gradient")
     return _Attn.apply(_rows(q), _rows(k), _rows(v), cu_seqlens, bool(causal), scale, seq_used, score_cap,
                        distance_slopes, prefix_lens)
