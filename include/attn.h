@@ -28,7 +28,8 @@
  * the cache beyond a sequence's length may hold anything, NaN and infinities among it, and
  * reach no result.  Within a sample, a key that a causal row does not see has weight zero
  * in it, but its value row is a factor of the product: keys, values and output gradients
- * of a sample's own rows are expected to be finite, and queries in the backward.  A NaN or a
+ * of a sample's own rows are expected to be finite, and queries in the backward.  Weights reach 2^30
+ * before they are normalised: values are expected below 2^98 over the number of a row's keys.  A NaN or a
  * score above binary32's range, from a query or from a key that the row sees, makes the
  * row's out and lse NaN, however the keys are split; scores that are all -infinity weigh
  * nothing, as if the row saw no key.
@@ -176,8 +177,6 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
  * Computed in binary32: a cap puts a score within 8e-6 of the cap of where it belongs, a cap past
  * 128 within 1e-6 of the score and 2^-21 of the cap where the score is larger than it.  A score of
  * +-infinity is capped like any other; a NaN comes out in its row.  Distances are exact below 2^24.
- * With caps up to 55 and no slopes the forward's weights reach 2^60 before they are normalised: values
- * are expected below 2^43 there.
  */
 typedef struct attn_score_rule {
     const float *slopes;           /* device float [n_q_heads], times 1.45 and the longest

@@ -96,13 +96,19 @@ struct Shared {
 
 // Capped exponents that stay within +-80 need no maximum, a quarter of K does for all rows: weights
 // are within 2^60 and 2^-100, so that they and the sums of 2^24 of them keep their precision in
-// binary32, and products with values up to 2^43 their range; the two halves of a row need not meet.
+// binary32; the two halves of a row need not meet.
 // Where a maximum makes the largest weight 1, here it is rounded to bf16 too: the output is divided by
 // the sum of the rounded weights, so that a row of one key is that key's value (o off by 1.8-2.2e-3 of
 // itself, 2.3-2.4e-3 without, for 40 us of 635; lse takes the sum of the weights as they are).
-// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 635 us,
+// Their products with values far from 1 may leave binary32 all the same.  A row whose sum is above
+// kMostSum or below kLeastSum looks at its output, and where that has overflowed, or holds values so
+// small that they may have lost bits, the CTA runs once more, with that row's own lse as its maximum.
+// Other rows keep theirs, and their bits (626 -> 637 us, one CTA's work once more where it happens).
+// Larger caps are the biased instance's, with slopes of 0 (the packed batch, 32/8 heads of 128: 637 us,
 // 797 with the maximum; both in one instance cost the first a quarter).
 constexpr bool kFixed = kRule == kRuleCap;
+constexpr float kMostSum = 1073741824.0f, kLeastSum = 5.9604645e-8f;   // 2^30, 2^-24
+constexpr float kTiny = 7.8886091e-31f; // 2^-100: binary32 holds what is left of such an output to 2^-26
 
 template <int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdArgs a)
@@ -118,11 +124,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                    kv_empty = kv_full + 8 * kStages, first_full = kv_empty + 8 * kStages, drain = first_full + 8;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
+    __shared__ float s_start[kFixed ? 2 : 1][kRows];                   // [row tile][row], the fixed maximum
+    __shared__ volatile int s_again, s_loads;                          // the CTA is to run once more; tiles that it loaded
     __shared__ TileSlot s_slot;
     __shared__ float s_swap[2][2][2][kRows];                           // [parity][row tile][half][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
+    auto init_barriers = [&] {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
@@ -135,9 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         mbar_init(first_full, 1);
         mbar_init(drain, 1);
-        s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
+    };
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        s_again = 0;
+        init_barriers();
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);
     if (warp == kLoadWarp && lane == 0) {
@@ -145,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         tma_prefetch_map(&a.k);
         tma_prefetch_map(&a.v);
     }
+    if (kFixed && threadIdx.x < 2 * kRows) s_start[threadIdx.x / kRows][threadIdx.x % kRows] = 0.25f * a.rule.k;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -159,6 +172,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
+    // With a fixed maximum (kFixed) what follows may run once more: a copy of its own then, as a loop around
+    // one leaves the softmax fewer registers (2.6 KB of spills in the paged form).  The other instances have
+    // no function around it, which alone cost cap and slopes from pages 374 us for 336.
+#if PVR_SCORE_RULE == 2
+    auto attend = [&](auto repeats) {
+    constexpr bool kRepeated = decltype(repeats)::value;
+#else
+    constexpr bool kRepeated = false;
+#endif
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const TileSlot where = s_slot;
@@ -393,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const float slope2 = !kBias || !mine || a.rule.slopes == nullptr ? 0.0f
             : a.rule.slopes[kvh * a.group + row - static_cast<int>(fast_div(row, a.div_group)) * a.group] * kLog2e;
         const int row_key = i_tok + offset - lo_tile * kKeys - 64 * half;   // this row's own key, from this thread's first
-        float m = kFixed ? 0.25f * a.rule.k : -INFINITY, l = 0.0f, mc = 0.0f;
+        float m = kFixed ? s_start[x][row] : -INFINITY, l = 0.0f, mc = 0.0f;
         bool ok = true;
         bool folded = false;                                           // m is known, and small (shaped: known)
         bool fold = true;                                              // shaped: m is small
@@ -591,6 +613,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             l += s_swap[count[x] & 1][x][half ^ 1][row];
             if (kFixed) norm += s_swap[count[x] & 1 ^ 1][x][half ^ 1][row];
         }
+        if (kFixed && !kRepeated) {
+            const bool low = l < kLeastSum, far = lim > 0 && l > 0.0f && (low || l > kMostSum);
+            if (__any_sync(0xffffffffu, far)) {
+                bool off = false;
+#pragma unroll 1
+                for (int j = 0; j < DP / 32; ++j) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + 16 * j, o);
+                    tc_wait_ld16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float size = fabsf(__uint_as_float(o[e]));
+                        off = off || (half * (DP / 2) + 16 * j + e < a.d && (!(size < INFINITY) || (low && size < kTiny)));
+                    }
+                }
+                if (far && off) {                                      // (either of the row's threads, or both alike)
+                    s_start[x][row] = m + log2f(l);
+                    s_loads = 2 * n_tiles;
+                    s_again = 1;
+                }
+            }
+        }
         // epilogue: rows outside the pack, and rows that see no key, are zero (tiles that all
         // rows in use see whole are not masked, so such rows may have summed anything).  No
         // weight is l == 0, not !(l > 0): a NaN score makes l NaN, and that must come out
@@ -659,7 +703,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         tc_fence_before();
     }
+#if PVR_SCORE_RULE == 2
+    };
+    attend(std::false_type{});
     __syncthreads();
+    if (s_again != 0 && s_abort == 0) {
+        // All copies have landed and all products are done, as the waits above have seen; what may still be
+        // on its way are reports of places that are free.  Past them the barriers begin anew.
+        fence_async_smem();             // the rows of the output were in Q's place
+        if (warp == kMmaWarp)
+            for (int t = max(0, s_loads - kStages); t < s_loads; ++t)
+                warp_wait(kv_empty + 8 * (t % kStages), (t / kStages) & 1, &s_abort, &g_attn_fault);
+        __syncthreads();
+        if (s_abort == 0) {
+            if (threadIdx.x == 0) {
+                for (uint32_t bar = bars; bar <= drain; bar += 8) mbar_inval(bar);
+                init_barriers();
+            }
+            tc_fence_before();
+            __syncthreads();
+            attend(std::true_type{});
+            __syncthreads();
+        }
+    }
+    const uint32_t tmem = s_tmem;
+#else
+    __syncthreads();
+#endif
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, 512);
