@@ -182,6 +182,12 @@ int attn_paged(const attn_paged_desc *desc, void *workspace, int64_t workspace_b
  * rounding, and the pass over the keys has D whole.  With a cap dq has it too.  Without, dq, and with a
  * prefix alone dk, are as the plain operator's: off by 2.4 to 2.8e-3 of themselves (mean square) on scores
  * of deviation 1.5, by 4.1 to 5.0e-3 of deviation 6, where those that have D whole are by 2.4e-3.
+ *
+ * Bits.  The same call gives the same bits.  Of other inputs a row's bits depend on the keys that the 32
+ * rows of its warp see, (token, query head) pairs side by side: the form of the tanh, chosen by the largest
+ * of their scores, and the moment at which the maximum moves are the warp's.  So a later token's query may
+ * move an earlier row within the errors above, and a row comes out of a packed call, a chunk and a single
+ * token alike within them, not to the bit.
  */
 typedef struct attn_score_rule {
     const float *slopes;           /* device float [n_q_heads], times 1.45 and the longest
