@@ -193,7 +193,9 @@ typedef struct attn_score_rule {
     const float *slopes;           /* device float [n_q_heads], times 1.45 and the longest
                                       distance finite; or NULL: no bias                    */
     const int32_t *prefix;         /* device int32 [n_seqs], keys that all rows of the
-                                      sequence see (cut to its keys, negative as 0); needs
+                                      sequence see (cut to its keys, negative as 0: in a paged
+                                      call those in the cache, so that a prefix that comes in
+                                      several chunks opens with each as far as it has come); needs
                                       causal (else ROPE_ERR_UNSUPPORTED); or NULL          */
     float cap;                     /* 0: none; else > 0; cap, 1.45 cap, scale / cap and
                                       2.9 scale / cap normal in binary32 (else ROPE_ERR_THETA) */

@@ -297,7 +297,10 @@ def attn_paged(q, cache: PagedKVCache, page_table, kv_lens, cu_seqlens, causal: 
     caches; 0: what the page table's width allows).  ``workspace``: a CUDA tensor for
     partial results (``attn_paged_workspace_bytes``); allocated through torch unless given.
     ``score_cap``, ``distance_slopes`` and ``prefix_lens``: rules on the scores, as in
-    ``attn_varlen_fwd`` (C entry point ``attn_paged_rule``).  Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
+    ``attn_varlen_fwd`` (C entry point ``attn_paged_rule``).  A prefix is cut to the keys in the cache: one
+    that comes in several chunks opens with each as far as it has come, and all of it for rows of the chunk
+    that completes it and later ones; give it whole in one chunk where its first rows are to see its last keys.
+    Returns ``out`` [T, Hq, d] (a new tensor unless given)."""
     _torch or _load_torch()
     if out is None:
         out = _empty(q.shape, _bf16, q.device, stream)

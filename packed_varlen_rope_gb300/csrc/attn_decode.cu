@@ -14,7 +14,9 @@
 // further splits join through the workspace in a second launch.
 //
 // Rules on the scores (score_rule.cuh), an instance each: a few operations a score more, hidden by the
-// loads (the batch below, capped: 327-333 us).
+// loads (the batch below, capped: 327-333 us; another draw of it, 1.42 GB: plain 226.5, prefixes 226.7,
+// capped 226.8, slopes of a geometric series from 2^-0.25 to 2^-8 231.1, both 239.0 us).  Keys go upwards, so that
+// with steep slopes a row's maximum moves at nearly every chunk; 2 % is what that costs.
 //
 // Bound by HBM: G operations a byte of cache (64 sequences of 500-16,000 tokens, 32/8 heads
 // of 128: 325-330 us for 2.2 GB, 6.7-6.8 TB/s, a copy's rate); a short sequence by the chain of

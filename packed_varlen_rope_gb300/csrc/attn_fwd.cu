@@ -21,14 +21,16 @@
 // Rules on the scores (score_rule.cuh), an instance each.  A prefix only moves the rows' limits.
 // Shaped scores (capped, biased) become exponents 32 columns at a time between tensor memory and the
 // exponential; with a bias by distance the key tiles go downwards, so that causal rows meet their
-// largest exponents first.  They hold the softmax warps, not the tensor core, back: the packed batch
-// below, 32/8 heads of 128, 501 us plain, 515 with prefixes, 565 with slopes, 635 capped, 795 both
-// (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64
-// 329, 331, 400, 438 and 598 us.
+// largest exponents first.  They hold the softmax warps, not the tensor core, back: a packed batch of
+// 16,384 tokens, 345 us by its operations (another draw of the lengths below, with longer samples), 32/8
+// heads of 128, 501-509 us plain, 515 with prefixes of some samples, 557-578 with slopes, 637 capped, 795-808
+// both (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64,
+// 172 us by its operations, 459, 515, 545, 624 and 841 us.
 //
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
 // elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
-// register spill (none in the packed instances, one of 4 bytes in the paged ones): with 200 KB
+// register spill (packed: none without slopes, 4-16 bytes stored with them; paged: none with a cap, 4 bytes
+// plain, with prefixes or slopes, 8-24 with cap and slopes): with 200 KB
 // of shared memory local memory misses to L2, and the softmax loop waits for it.  One wait per
 // row tile for the issuing warp: a wait costs some 200 cycles while the tensor core
 // reads shared memory, so the arrival of K and V is folded into the barrier of P.
@@ -38,7 +40,7 @@
 // ms, 1,544, over 0.9 s under the power limit (the library's products sustain 1,705; from pages
 // of 128 tokens 5.74 ms); 8,192 tokens 379 and 392 us; packs of short samples are held back by
 // the 6,000 cycles before a CTA's first softmax and the 4,000 after its last (16,384 tokens in
-// samples of 32-8,192: 474 us, 1,237 TFLOP/s).
+// samples of 32-8,192, 309 us by its operations: 474 us, 1,237 TFLOP/s).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -99,7 +101,7 @@ struct Shared {
 // binary32; the two halves of a row need not meet.
 // Where a maximum makes the largest weight 1, here it is rounded to bf16 too: the output is divided by
 // the sum of the rounded weights, so that a row of one key is that key's value (o off by 1.8-2.2e-3 of
-// itself, 2.3-2.4e-3 without, for 40 us of 635; lse takes the sum of the weights as they are).
+// itself, 2.3-2.4e-3 without, for 40 us of 637; lse takes the sum of the weights as they are).
 // Their products with values far from 1 may leave binary32 all the same.  A row whose sum is above
 // kMostSum or below kLeastSum looks at its output, and where that has overflowed, or holds values so
 // small that they may have lost bits, the CTA runs once more, with that row's own lse as its maximum.
