@@ -18,9 +18,10 @@
  *              without a page and for t >= cu_seqlens[n_seqs].
  *
  * When the stack runs out the remaining pages get id -1, which the cache's readers treat as no
- * page (STEP_NO_PAGES); later steps do not fill it: finish the row, which gives back what it got.  Pages past the table's width are not taken (STEP_TABLE_FULL); what does not
- * fit the stack is dropped (STEP_STACK_FULL); tokens past the slots' end get none
- * (STEP_TOKENS_PAST_END, where slots are wanted).  The bits go to *status.
+ * page (STEP_NO_PAGES); later steps do not fill it: finish the row, which gives back what it got.
+ * Pages past the table's width are not taken (STEP_TABLE_FULL); what does not fit the stack is
+ * dropped (STEP_STACK_FULL); tokens past the slots' end get none (STEP_TOKENS_PAST_END, where
+ * slots are wanted).  The bits go to *status.
  *
  * Ownership, streams, errors as in rope_qk.h.  The order is that of the sequences, whatever the
  * timing: the same bits each run.
