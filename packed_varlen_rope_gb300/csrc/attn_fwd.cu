@@ -23,9 +23,9 @@
 // exponential; with a bias by distance the key tiles go downwards, so that causal rows meet their
 // largest exponents first.  They hold the softmax warps, not the tensor core, back: a packed batch of
 // 16,384 tokens, 345 us by its operations (another draw of the lengths below, with longer samples), 32/8
-// heads of 128, 501-509 us plain, 515 with prefixes of some samples, 557-578 with slopes, 637 capped, 795-808
+// heads of 128, 501-509 us plain, 515 with prefixes of some samples, 557-578 with slopes, 637 capped, 795-800
 // both (four warps a scheduler of dependent operations, half of the issue slots taken); 32/32 heads of 64,
-// 172 us by its operations, 459, 515, 545, 624 and 841 us.
+// 172 us by its operations, 461, 515, 546, 624 and 837 us.
 //
 // What it took.  Operands of the tensor core's instructions in uniform registers, issued by an
 // elected lane of a converged warp (from one diverged lane each cost 100 cycles).  Hardly a
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     };
     if (threadIdx.x == 0) {
         s_abort = 0;
-        s_again = 0;
+        if (kFixed) s_again = 0;
         init_barriers();
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), 512);

@@ -18,7 +18,7 @@
 //
 // 16,384 tokens of a packed batch, 32/8 heads of 128, forward and backward: nearly all chunks kSmall
 // (scores of deviation 6, cap 50) 637 and 2,250-2,290 us (kNear in its place: 8 and 1 % more), nearly
-// all kAny (cap 20) 901-915 and 2,815 us, kLarge 1,212-1,223 and 3,270 us; without a cap 501-509 and 1,686-1,713 us.  kAny
+// all kAny (cap 20) 901-915 and 2,815 us, kLarge 1,212-1,219 and 3,270 us; without a cap 501-509 and 1,686-1,713 us.  kAny
 // for every second, third or fourth pair among kNear, to spread the work over the pipes, took 20 to
 // 25 % more forward and 0 to 3 % backward.
 #pragma once
